@@ -31,10 +31,12 @@ ROW_NONFINITE = 0x20
 ROW_INTERNAL = 0x40
 ROW_BAD_LENIENCE = 0x80
 
-# every symbol include/spec_verify.h declares
+# every symbol that include/*.h declares
 EXPORTED = ("spec_verify", "spec_verify_ex", "spec_verify_workspace_size", "spec_verify_host",
             "spec_verify_host_staging_size", "spec_verify_strerror", "spec_verify_static", "spec_verify_gumbel",
-            "spec_verify_kseq", "spec_verify_kseq_workspace_size")
+            "spec_verify_kseq", "spec_verify_kseq_workspace_size", "spec_verify_history_add",
+            "spec_verify_process_logits", "spec_verify_rotate_append", "spec_verify_attention",
+            "spec_verify_attention_workspace_size")
 SV_MAX_KSEQ = 13
 
 SV_ESCRATCH = -6
@@ -92,6 +94,13 @@ def load_library():
     lib.spec_verify_kseq.argtypes = [P, P, I, P, P, P, P, P, U64, I, I, I, P, P, P, P, SZ, P,
                                      ctypes.POINTER(_Options)]
     lib.spec_verify_kseq.restype = I
+    # the structures of include/spec_verify_target.h are passed as packed bytes
+    for name in ("history_add", "process_logits", "rotate_append", "attention"):
+        fn = getattr(lib, "spec_verify_" + name)
+        fn.argtypes = [ctypes.c_char_p, P]
+        fn.restype = I
+    lib.spec_verify_attention_workspace_size.argtypes = [ctypes.c_int64] * 5
+    lib.spec_verify_attention_workspace_size.restype = SZ
     lib.spec_verify_strerror.argtypes = [I]
     lib.spec_verify_strerror.restype = ctypes.c_char_p
     _lib = lib
@@ -392,3 +401,8 @@ def spec_verify_static(target: torch.Tensor, draft: torch.Tensor, draft_tokens: 
                                     ctypes.c_void_p(s.cuda_stream))
     _check(rc)
     return outputs
+
+
+from .target import (ROW_BAD_LENGTH, ROW_BAD_PAGE, ROW_BAD_PENALTY, ROW_BAD_SLOT, PagedCache,  # noqa: E402,F401
+                     TokenHistory, attention_workspace_size, paged_attention, process_logits, rotary_table,
+                     rotate_append)

@@ -1,0 +1,105 @@
+// sv_attend.cu -- host side of spec_verify_attention: checks, the choice of kernel, the
+// workspace.
+#include "sv_attend.cuh"
+
+#include <cstring>
+#include <mutex>
+
+namespace sv {
+namespace {
+
+constexpr double kLog2e = 1.4426950408889634;
+
+// rows of a cache head's tile: 16 or 32 as the rows of a sequence need
+int row_tile(int64_t N, int64_t group) { return N * group <= 16 ? 16 : 32; }
+
+int check_attention(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads, int64_t dim) {
+    if (B < 0 || N < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads) return SV_EINVAL;
+    if (dim != 64 && dim != 128) return SV_EUNSUPPORTED;
+    if (B > SV_MAX_BATCH || q_heads > 65536 || q_heads / kv_heads > SV_MAX_GROUP || N > (1 << 24)) return SV_ETOO_LARGE;
+    return SV_OK;
+}
+
+struct Workspace {
+    size_t cut, ml, o, total;
+};
+Workspace workspace(int64_t dim, int rm) {
+    Workspace w;
+    w.cut = 0;
+    w.ml = align_up(sizeof(Cut) * kMaxCtas, 256);
+    w.o = align_up(w.ml + (size_t)2 * kMaxCtas * rm * 8, 256);
+    w.total = align_up(w.o + (size_t)2 * kMaxCtas * rm * dim * 4, 256);
+    return w;
+}
+
+int sm_count(int dev) {
+    static int counts[64];
+    static std::mutex mu;
+    int n = 0;
+    if (dev < 0 || dev >= 64)
+        return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!counts[dev] && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) counts[dev] = n;
+    return counts[dev];
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t spec_verify_attention_workspace_size(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads,
+                                                       int64_t dim) {
+    if (check_attention(B, N, q_heads, kv_heads, dim) != SV_OK) return 0;
+    return workspace(dim, row_tile(N, q_heads / kv_heads)).total;
+}
+
+extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream) {
+    if (!args || args->struct_size != sizeof(sv_attention_args)) return SV_EINVAL;
+    const sv_attention_args& a = *args;
+    if (a.dtype != SV_BF16 && a.dtype != SV_F16) return SV_EUNSUPPORTED;
+    int rc = check_attention(a.B, a.N, a.q_heads, a.kv_heads, a.dim);
+    if (rc != SV_OK) return rc;
+    if (a.window < 0 || a.max_context < 0 || !(a.scale > 0.0) || a.scale > 1e30) return SV_EINVAL;
+    if (a.B == 0) return SV_OK;
+    if (bad_rows(a.q, a.q_stride_b, a.q_stride_n, a.q_stride_h) ||
+        bad_rows(a.out, a.o_stride_b, a.o_stride_n, a.o_stride_h))
+        return SV_EINVAL;
+    // two output rows on the same memory would race
+    if ((a.q_heads > 1 && a.o_stride_h < a.dim) || (a.N > 1 && a.o_stride_n < a.dim) ||
+        (a.B > 1 && a.o_stride_b < a.dim))
+        return SV_EINVAL;
+    rc = check_cache(a.cache, a.B, a.kv_heads, a.dim);
+    if (rc != SV_OK) return rc;
+    const int group = (int)(a.q_heads / a.kv_heads);
+    const int rm = row_tile(a.N, group);
+    const Workspace w = workspace(a.dim, rm);
+    if (!a.workspace || a.workspace_bytes < (int64_t)w.total) return SV_EWORKSPACE;
+    if ((uintptr_t)a.workspace & 255u) return SV_EINVAL;
+
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SV_ECUDA;
+    const int sms = sm_count(dev);
+    if (sms <= 0) return SV_ECUDA;
+    AttendArgs p;
+    memset(&p, 0, sizeof p);
+    p.a = a;
+    p.group = group;
+    p.qscale = (float)(a.scale * kLog2e);
+    p.capacity = a.cache.pages_per_seq * a.cache.page_size;
+    if (p.capacity > 0x7FFFFF00) p.capacity = 0x7FFFFF00;  // positions are 32-bit
+    char* ws = (char*)a.workspace;
+    p.cut = (Cut*)(ws + w.cut);
+    p.part_ml = (float*)(ws + w.ml);
+    p.part_o = (float*)(ws + w.o);
+    // never more CTAs than tiles: a bound from what the host knows of the lengths
+    const int64_t ctx = a.max_context > 0 && a.max_context < p.capacity ? a.max_context : p.capacity;
+    const double tiles = (double)a.B * a.kv_heads * (double)((a.N * group + rm - 1) / rm) *
+                         (double)((ctx + kKeyTile - 1) / kKeyTile + 1);
+    p.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    if (tiles < p.ctas) p.ctas = (int)tiles;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (launch_attend_rows((int)a.dtype, (int)a.dim, rm / 16, p, s) != cudaSuccess) return SV_ECUDA;
+    if (launch_attend_join((int)a.dtype, (int)a.dim, rm, p, s) != cudaSuccess) return SV_ECUDA;
+    return SV_OK;
+}

@@ -1,0 +1,435 @@
+"""Operators around one verification call: the target's attention over its paged cache,
+the rotary positions that fill it, and what is done to the logits before they are verified.
+
+A round with gamma drafts runs N = gamma + 1 new tokens of each sequence::
+
+    q = sv.rotate_append(q, k, v, table, cache, page_table, cache_lens)      # every layer
+    o = sv.paged_attention(q, cache, page_table, cache_lens, max_context=m)
+    ...
+    z = sv.process_logits(logits, history=history, draft_tokens=x, repetition=r, mask=grammar)
+    res = sv.spec_verify(z, draft_logits, x, temperature, seed=step)
+    history.add(res["out_tokens"])                                           # the -1s are skipped
+    cache_lens += res["accepted_len"] + 1                                    # rejected keys are overwritten
+
+N = 1 is the plain decoding step; a large N is a chunk of a prompt.  The arrays are those of
+``include/spec_verify_target.h``, which states the formulas.  Nothing here synchronises,
+and there is no CPU path.  ``row_status`` (int32 [B], zeroed by the caller) collects the
+ROW_BAD_* bits of sequences whose data is bad; such a sequence gets NaN, which spec_verify
+then reports as ROW_NONFINITE.
+"""
+from __future__ import annotations
+
+import math
+import struct
+from typing import Optional, Tuple
+
+import torch
+
+SV_F16 = 2
+
+ROW_BAD_PENALTY = 0x100
+ROW_BAD_SLOT = 0x200
+ROW_BAD_LENGTH = 0x400
+ROW_BAD_PAGE = 0x800
+
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: SV_F16}
+
+# the C structures are runs of 8-byte fields, filled in one go
+_HISTORY = struct.Struct("<Q3Q3q2Q3q2Qq")
+_LOGITS = struct.Struct("<Q2Q4q4q3Q2q2Q2q3Q3QqQ2qQ")
+_CACHE = "2Q8qQ2q2Q"
+_ROTATE = struct.Struct("<Q4Q6q12qQ3q" + _CACHE + "Q")
+_ATTENTION = struct.Struct("<Q2Q6q6qd2q" + _CACHE + "QqQQ")
+
+
+def _api():
+    from . import _check, load_library
+
+    return load_library(), _check
+
+
+def _p(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _vec(x, B: int, dtype: torch.dtype, device, name: str) -> Optional[torch.Tensor]:
+    """A per-sequence parameter as a contiguous device vector of B entries."""
+    if x is None:
+        return None
+    if torch.is_tensor(x) and x.dtype == dtype and x.device == device and x.dim() == 1 and x.numel() == B and \
+            x.is_contiguous():
+        return x
+    from . import _dev_vec
+
+    return _dev_vec(x, B, dtype, device, name)
+
+
+def _table(x: torch.Tensor, shape, device, name: str) -> torch.Tensor:
+    """An int32 device matrix whose rows are contiguous."""
+    if not torch.is_tensor(x) or x.dim() != 2 or x.shape[0] != shape[0] or x.shape[1] < shape[1]:
+        raise ValueError(f"{name} must be [{shape[0]}, >= {shape[1]}]")
+    if x.dtype != torch.int32 or x.device != device:
+        x = x.to(device=device, dtype=torch.int32)
+    return x if x.stride(1) == 1 or x.shape[1] == 1 else x.contiguous()
+
+
+def _status(row_status, B, device):
+    if row_status is not None and (row_status.dtype != torch.int32 or row_status.device != device or
+                                   tuple(row_status.shape) != (B,) or not row_status.is_contiguous()):
+        raise ValueError("row_status must be a contiguous int32 CUDA tensor of B entries")
+    return row_status
+
+
+class _On:
+    """Device and stream of one call: work and allocations go to ``stream`` when it is given, and the
+    tensors of the call are kept for it."""
+
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.ctx = torch.cuda.stream(self.stream)
+            self.ctx.__enter__()
+        elif torch.cuda.current_device() != self.device.index:
+            self.ctx = torch.cuda.device(self.device)
+            self.ctx.__enter__()
+        return self
+
+    def handle(self) -> int:
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def keep(self, *tensors) -> None:
+        if self.stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+# ---------------------------------------------------------------------------
+# logits
+# ---------------------------------------------------------------------------
+class TokenHistory:
+    """The tokens that the penalties of ``process_logits`` count, for ``slots`` sequences.
+
+    seen, produced: int32 [slots, words] bit planes (token t: bit t % 32 of word t // 32);
+    counts: int32 [slots, V], occurrences in the output.
+    """
+
+    def __init__(self, slots: int, vocab: int, device="cuda"):
+        if slots < 1 or vocab < 1:
+            raise ValueError("slots and vocab must be positive")
+        self.slots, self.vocab = slots, vocab
+        self.words = (vocab + 127) // 128 * 4
+        self.seen = torch.zeros((slots, self.words), dtype=torch.int32, device=device)
+        self.produced = torch.zeros((slots, self.words), dtype=torch.int32, device=device)
+        self.counts = torch.zeros((slots, vocab), dtype=torch.int32, device=device)
+
+    def _call(self, tokens, prompt_lens, total_lens, slots, clear, stream):
+        if not self.counts.is_cuda:
+            raise ValueError("the history must be on a CUDA device")
+        dev = self.counts.device
+        with _On(dev, stream) as on:
+            if not torch.is_tensor(tokens):
+                tokens = torch.as_tensor(tokens, dtype=torch.int32)
+            if tokens.dim() != 2:
+                raise ValueError("tokens must be [B, L]")
+            B, L = tokens.shape
+            tokens = _table(tokens, (B, L), dev, "tokens")
+            slot_of = _vec(slots, B, torch.int32, dev, "slots")
+            if slot_of is None and B > self.slots:
+                raise ValueError(f"{B} rows but only {self.slots} slots")
+            pl = _vec(prompt_lens, B, torch.int32, dev, "prompt_lens")
+            tl = _vec(total_lens, B, torch.int32, dev, "total_lens")
+            lib, check = _api()
+            check(lib.spec_verify_history_add(_HISTORY.pack(
+                _HISTORY.size, _p(self.seen), _p(self.produced), _p(self.counts), self.slots, self.words, self.vocab,
+                _p(slot_of), _p(tokens), B, L, tokens.stride(0), _p(pl), _p(tl), int(clear)), on.handle()))
+            on.keep(tokens, slot_of, pl, tl, self.seen, self.produced, self.counts)
+
+    def load(self, tokens, prompt_lens=None, total_lens=None, slots=None, *, stream=None) -> None:
+        """New sequences take their slots: of row b of tokens [B, L] the first prompt_lens[b] (default: none) are
+        the prompt, those up to total_lens[b] (default: L) output.  slots [B] (default: row b, slot b)."""
+        self._call(tokens, prompt_lens, total_lens, slots, True, stream)
+
+    def add(self, tokens, total_lens=None, slots=None, *, stream=None) -> None:
+        """Output tokens of a round, as spec_verify returns them: [B, L], ids outside [0, vocab) are skipped."""
+        self._call(tokens, None, total_lens, slots, False, stream)
+
+
+def process_logits(logits: torch.Tensor, *, history: Optional[TokenHistory] = None, slots=None,
+                   draft_tokens: Optional[torch.Tensor] = None, repetition=None, frequency=None, presence=None,
+                   bias: Optional[Tuple] = None, mask: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, row_status: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Penalties, biases and masks on logits [B, N, V] (float32 or bfloat16, CUDA, vocabulary contiguous).
+
+    Row i of a sequence counts its history and draft_tokens[b, :i] (int32 [B, >= N - 1]).
+    repetition, frequency, presence: per-sequence tensors, sequences or scalars.
+    bias: (ids int32 [n], values float32 [n], offsets int32 [B + 1]), the added values of each sequence.
+    mask: int32 [B, N, W] or [B, W], W >= ceil(V / 32), 1 = allowed: bit t % 32 of word t // 32 is token t's.
+    out: where to write (may be ``logits``); by default a new tensor.  Returns it.
+    """
+    if not torch.is_tensor(logits) or not logits.is_cuda or logits.dim() != 3:
+        raise ValueError("logits must be a CUDA tensor [B, N, V]")
+    code = _DTYPE.get(logits.dtype)
+    if code not in (0, 1):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    B, N, V = logits.shape
+    dev = logits.device
+    with _On(dev, stream) as on:
+        x = logits if logits.stride(2) == 1 or V == 1 else logits.contiguous()
+        if out is None:
+            out = torch.empty((B, N, V), dtype=logits.dtype, device=dev)
+        elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev or \
+                (V > 1 and out.stride(2) != 1):
+            raise ValueError("out must have the logits' shape, type and device, and a contiguous vocabulary")
+        seen = produced = counts = slot_of = None
+        nslots = words = 0
+        if history is not None:
+            if history.vocab != V or history.counts.device != dev:
+                raise ValueError(f"the history is of {history.vocab} tokens on {history.counts.device}")
+            seen, produced, counts = history.seen, history.produced, history.counts
+            nslots, words = history.slots, history.words
+            slot_of = _vec(slots, B, torch.int32, dev, "slots")
+            if slot_of is None and B > nslots:
+                raise ValueError(f"{B} rows but only {nslots} slots")
+        toks = None if draft_tokens is None or N == 1 else _table(draft_tokens, (B, N - 1), dev, "draft_tokens")
+        rep = _vec(repetition, B, torch.float32, dev, "repetition")
+        freq = _vec(frequency, B, torch.float32, dev, "frequency")
+        pres = _vec(presence, B, torch.float32, dev, "presence")
+        ids = vals = offs = None
+        if bias is not None:
+            ids, vals, offs = bias
+            ids, vals = (_vec(ids, len(ids), torch.int32, dev, "bias ids"),
+                         _vec(vals, len(vals), torch.float32, dev, "bias values"))
+            offs = _vec(offs, B + 1, torch.int32, dev, "bias offsets")
+            if ids.numel() != vals.numel():
+                raise ValueError("bias ids and values differ in length")
+            if ids.numel() == 0:
+                ids = vals = offs = None
+        msb = msn = 0
+        if mask is not None:
+            if mask.dtype != torch.int32 or mask.device != dev:
+                raise ValueError("mask must be an int32 CUDA tensor")
+            if mask.dim() not in (2, 3) or mask.shape[0] != B or (mask.dim() == 3 and mask.shape[1] != N) or \
+                    32 * mask.shape[-1] < V:
+                raise ValueError("mask must be [B, N, W] or [B, W] with W >= ceil(V / 32)")
+            if mask.stride(-1) != 1 and mask.shape[-1] > 1:
+                mask = mask.contiguous()
+            msb, msn = mask.stride(0), (mask.stride(1) if mask.dim() == 3 else 0)
+        st = _status(row_status, B, dev)
+        lib, check = _api()
+        check(lib.spec_verify_process_logits(_LOGITS.pack(
+            _LOGITS.size, _p(x), _p(out), code, B, N, V, x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+            _p(seen), _p(produced), _p(counts), nslots, words, _p(slot_of),
+            _p(toks), 0 if toks is None else toks.stride(0), 0 if toks is None else toks.shape[1],
+            _p(rep), _p(freq), _p(pres), _p(ids), _p(vals), _p(offs), 0 if ids is None else ids.numel(),
+            _p(mask), msb, msn, _p(st)), on.handle()))
+        on.keep(x, out, seen, produced, counts, slot_of, toks, rep, freq, pres, ids, vals, offs, mask, st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# paged cache
+# ---------------------------------------------------------------------------
+class PagedCache:
+    """Keys and values of one layer in pages: k, v [pages, kv_heads, page_size, head_dim], bfloat16 or float16.
+
+    Position j of a sequence is row j % page_size of the page that its page table names at j // page_size.
+    """
+
+    def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
+        shape = (pages, kv_heads, page_size, head_dim)
+        self._set(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+    @classmethod
+    def from_tensors(cls, k: torch.Tensor, v: torch.Tensor) -> "PagedCache":
+        """A cache over the caller's memory; any order of page, head and row in memory (views are fine), as long
+        as the head dimension is contiguous and every row starts on a 16-byte boundary."""
+        self = cls.__new__(cls)
+        self._set(k, v)
+        return self
+
+    def _set(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim] of one shape, type and device")
+        if k.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"the cache must be bfloat16 or float16, got {k.dtype}")
+        if k.shape[2] < 16 or k.shape[2] % 16:
+            raise ValueError(f"page_size must be a multiple of 16, got {k.shape[2]}")
+        for t in (k, v):
+            if t.stride(3) != 1 or t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:3]):
+                raise ValueError("rows of the cache must be contiguous and start on 16-byte boundaries")
+        self.k, self.v = k, v
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.dtype, self.device = k.dtype, k.device
+        self._fields = (k.data_ptr(), v.data_ptr(), self.pages, self.page_size, *k.stride()[:3], *v.stride()[:3])
+
+    def _pack(self, page_table, lens, new):
+        return self._fields + (_p(page_table), page_table.stride(0), page_table.shape[1], _p(lens), _p(new))
+
+
+def rotary_table(length: int, rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] = None,
+                 device="cuda") -> torch.Tensor:
+    """float32 [length, 2, rotary_dim / 2]: the cosines and sines of positions 0 .. length - 1.
+
+    Pair j turns by base^(-2j / rotary_dim) per position; the angles are formed in 64 bits.  scaling, for
+    contexts longer than the model was trained on:
+      {"type": "linear", "factor": s}    positions divided by s
+      {"type": "ntk", "factor": s}       base * s^(d / (d - 2)): the slowest pair is stretched by s
+      {"type": "yarn", "factor": s, "original_length": L, "beta_fast": 32, "beta_slow": 1}
+          pairs that make more than beta_fast turns over L stay, those with fewer than beta_slow are stretched
+          by s, a ramp between; cosines and sines are scaled by 0.1 ln(s) + 1 ("attention_factor" overrides)
+    """
+    if length < 1 or rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("length must be positive and rotary_dim even")
+    d, half = rotary_dim, rotary_dim // 2
+    j = torch.arange(half, dtype=torch.float64, device=device)
+    mscale = 1.0
+    freq = None
+    if scaling is not None:
+        kind, s = scaling.get("type"), float(scaling.get("factor", 1.0))
+        if not s >= 1.0:
+            raise ValueError("the scaling factor must be at least 1")
+        if kind == "linear":
+            freq = base ** (-2.0 * j / d) / s
+        elif kind == "ntk":
+            if d <= 2:
+                raise ValueError("ntk scaling needs rotary_dim > 2")
+            freq = (base * s ** (d / (d - 2.0))) ** (-2.0 * j / d)
+        elif kind == "yarn":
+            L = float(scaling["original_length"])
+
+            def pair_of(turns):  # the (real-valued) pair that makes so many turns over L positions
+                return d * math.log(L / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+            lo = max(math.floor(pair_of(float(scaling.get("beta_fast", 32.0)))), 0)
+            hi = min(math.ceil(pair_of(float(scaling.get("beta_slow", 1.0)))), d - 1)
+            ramp = ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+            freq = base ** (-2.0 * j / d)
+            freq = freq * (1.0 - ramp) + freq / s * ramp
+            mscale = float(scaling.get("attention_factor", 0.1 * math.log(s) + 1.0))
+        else:
+            raise ValueError(f"unknown rotary scaling {kind!r}")
+    else:
+        freq = base ** (-2.0 * j / d)
+    angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.stack(((angle.cos() * mscale).float(), (angle.sin() * mscale).float()), 1)
+
+
+def _rows(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
+    """[B, N, heads, dim] with contiguous, 16-byte aligned heads; a copy if it has not."""
+    if not torch.is_tensor(t) or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape) if torch.is_tensor(t) else type(t)}")
+    if t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be {dtype} on {device} like the cache, got {t.dtype} on {t.device}")
+    s = t.stride()
+    if s[3] != 1 or (s[0] | s[1] | s[2]) & 7 or t.data_ptr() & 15:
+        t = t.contiguous()
+        if t.data_ptr() & 15:  # a contiguous view that starts off a boundary
+            t = t.clone()
+    return t
+
+
+def _out_rows(out, q, name="out"):
+    if out is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    s = out.stride()
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or s[3] != 1 or \
+            (s[0] | s[1] | s[2]) & 7 or out.data_ptr() & 15:
+        raise ValueError(f"{name} must have q's shape, type and device, with contiguous, 16-byte aligned heads")
+    return out
+
+
+def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cache: PagedCache,
+                  page_table: torch.Tensor, cache_lens: torch.Tensor, num_new: Optional[torch.Tensor] = None, *,
+                  interleaved: bool = False, out: Optional[torch.Tensor] = None,
+                  row_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotates q [B, N, q_heads, dim] and k [B, N, kv_heads, dim] by their positions, writes k and v to the cache.
+
+    New token i of sequence b has position cache_lens[b] + i (int32 [B]); num_new [B] of the N are there
+    (default: all).  table: from rotary_table, at least as long as the last position; its rotary_dim
+    (a multiple of 16) may be less than dim.  Pairs are (j, j + rotary_dim / 2), or (2j, 2j + 1) with
+    interleaved.  Returns the rotated q (``out``, which may be q; rows past num_new are zeros).
+    """
+    if not torch.is_tensor(q) or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, N, q_heads, dim]")
+    B, N, Hq, D = q.shape
+    dev = q.device
+    if D != cache.head_dim or dev != cache.device:
+        raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
+    if table.dim() != 3 or table.shape[1] != 2 or table.dtype != torch.float32 or table.device != dev or \
+            not table.is_contiguous():
+        raise ValueError("table must be a contiguous float32 CUDA tensor [length, 2, rotary_dim / 2]")
+    rot = 2 * table.shape[2]
+    if rot % 16 or rot > D or rot < 16:
+        raise ValueError(f"rotary_dim must be a multiple of 16 and at most {D}, got {rot}")
+    with _On(dev, stream) as on:
+        x = _rows(q, (B, N, Hq, D), cache.dtype, dev, "q")
+        k = _rows(k, (B, N, cache.kv_heads, D), cache.dtype, dev, "k")
+        v = _rows(v, (B, N, cache.kv_heads, D), cache.dtype, dev, "v")
+        o = _out_rows(out, q)
+        pt = _table(page_table, (B, 1), dev, "page_table")
+        lens = _vec(cache_lens, B, torch.int32, dev, "cache_lens")
+        new = _vec(num_new, B, torch.int32, dev, "num_new")
+        st = _status(row_status, B, dev)
+        lib, check = _api()
+        check(lib.spec_verify_rotate_append(_ROTATE.pack(
+            _ROTATE.size, _p(x), _p(o), _p(k), _p(v), _DTYPE[cache.dtype], B, N, Hq, cache.kv_heads, D,
+            *x.stride()[:3], *o.stride()[:3], *k.stride()[:3], *v.stride()[:3], _p(table), table.shape[0], rot,
+            int(bool(interleaved)), *cache._pack(pt, lens, new), _p(st)), on.handle()))
+        on.keep(x, o, k, v, table, cache.k, cache.v, pt, lens, new, st)
+    return o
+
+
+def attention_workspace_size(B: int, N: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    """Bytes of workspace that one paged_attention call of this shape needs (0 for a shape it does not take)."""
+    return int(_api()[0].spec_verify_attention_workspace_size(B, N, q_heads, kv_heads, dim))
+
+
+def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, cache_lens: torch.Tensor,
+                    num_new: Optional[torch.Tensor] = None, *, scale: Optional[float] = None, window: int = 0,
+                    max_context: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                    row_status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    wait_limit_ns: int = 0, stream=None) -> torch.Tensor:
+    """Attention of the new tokens q [B, N, q_heads, dim] (dim 64 or 128) over the cache that holds their keys.
+
+    Token i of sequence b sees the positions up to cache_lens[b] + i, with window > 0 only the last ``window``
+    of them.  scale: default 1 / sqrt(dim).  max_context: the host's upper bound of cache_lens + num_new
+    (default: the page table's width); it only sizes the launch.  Rows past num_new are zeros.
+    workspace: uint8 of attention_workspace_size() bytes (default: from torch's allocator, per call).
+    """
+    if not torch.is_tensor(q) or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, N, q_heads, dim]")
+    B, N, Hq, D = q.shape
+    dev = q.device
+    if D != cache.head_dim or dev != cache.device:
+        raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
+    if Hq % cache.kv_heads:
+        raise ValueError(f"{Hq} query heads cannot share {cache.kv_heads} cache heads evenly")
+    if window < 0:
+        raise ValueError("window must be 0 (none) or positive")
+    lib, check = _api()
+    with _On(dev, stream) as on:
+        x = _rows(q, (B, N, Hq, D), cache.dtype, dev, "q")
+        o = _out_rows(out, q)
+        pt = _table(page_table, (B, 1), dev, "page_table")
+        lens = _vec(cache_lens, B, torch.int32, dev, "cache_lens")
+        new = _vec(num_new, B, torch.int32, dev, "num_new")
+        st = _status(row_status, B, dev)
+        if workspace is None:
+            workspace = torch.empty(lib.spec_verify_attention_workspace_size(B, N, Hq, cache.kv_heads, D),
+                                    dtype=torch.uint8, device=dev)
+        check(lib.spec_verify_attention(_ATTENTION.pack(
+            _ATTENTION.size, _p(x), _p(o), _DTYPE[cache.dtype], B, N, Hq, cache.kv_heads, D, *x.stride()[:3],
+            *o.stride()[:3], 1.0 / math.sqrt(D) if scale is None else float(scale), window, max_context or 0,
+            *cache._pack(pt, lens, new), _p(workspace), workspace.numel(), _p(st), int(wait_limit_ns)), on.handle()))
+        on.keep(x, o, cache.k, cache.v, pt, lens, new, st, workspace)
+    return o
