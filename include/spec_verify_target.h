@@ -40,10 +40,10 @@ extern "C" {
 #define SV_MAX_GROUP 64                     /* query heads per cache head */
 
 /*
- * Token history.  Per slot (a sequence's place in the server): seen, produced
- * [slots, words] bit planes, token t at bit t & 31 of word t >> 5, words >=
- * ceil(V / 32); counts [slots, V].  A token of the prompt sets `seen`; a token
- * of the output sets `seen` and `produced` and adds 1 to its count.
+ * Token history.  Per slot (a sequence's place in the server): seen [slots, words], a
+ * bit plane, token t at bit t & 31 of word t >> 5, words >= ceil(V / 32); counts
+ * [slots, V].  A token of the prompt or the output sets its bit; one of the output
+ * adds 1 to its count.
  *
  * tokens [B, L] (row stride tokens_stride); of row b the first prompt_lens[b]
  * (NULL: none) belong to the prompt, those from there to total_lens[b] (NULL: L)
@@ -55,7 +55,6 @@ extern "C" {
 typedef struct {
     uint64_t struct_size;
     uint32_t* seen;
-    uint32_t* produced;
     int32_t* counts;
     int64_t slots, words, V;
     const int32_t* slot_of;
@@ -100,7 +99,6 @@ typedef struct {
     int64_t dtype, B, N, V;
     int64_t logits_stride_b, logits_stride_n, out_stride_b, out_stride_n;
     const uint32_t* seen;
-    const uint32_t* produced;
     const int32_t* counts;
     int64_t slots, words;
     const int32_t* slot_of;

@@ -3,9 +3,8 @@
 //
 // The work on a logit is a handful of operations; what bounds the call is reading and
 // writing [B, N, V] once.  Everything else is kept small beside that: which tokens
-// were seen and produced are bit planes (V / 8 bytes a sequence each), so a count is
-// only fetched where the bit says that there is one, and a vector of logits that the
-// mask hides as a whole is not read.
+// were seen is a bit plane (V / 8 bytes a sequence), so a count is only fetched where
+// the bit says so, and a vector of logits that the mask hides as a whole is not read.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,18 +21,16 @@ constexpr int kLWarps = kLThreads / 32;
 // biases of one chunk that each warp can hold; a chunk with more re-reads the list
 constexpr int kLBiasCap = 64;
 
-// VEC bits of a bit plane from token e0 on (e0 may be negative or run past the
-// end; those bits are 0)
-template <int VEC>
-__device__ __forceinline__ uint32_t plane_bits(const uint32_t* __restrict__ p, int e0, int V) {
+// 32 bits of a bit plane from token e0 on (e0 may be negative or run past the end;
+// those bits are 0)
+__device__ __forceinline__ uint32_t plane_word(const uint32_t* __restrict__ p, int e0, int V) {
     const int i = e0 >> 5, sh = e0 & 31, last = (V - 1) >> 5;
-    const uint32_t lo = (i >= 0 && i <= last) ? __ldg(p + i) : 0u;
-    uint32_t w = lo >> sh;
-    if (sh + VEC > 32) {
+    uint32_t w = (i >= 0 && i <= last) ? __ldg(p + i) : 0u;
+    if (sh) {
         const uint32_t hi = (i + 1 >= 0 && i + 1 <= last) ? __ldg(p + i + 1) : 0u;
-        w = __funnelshift_r(lo, hi, sh);
+        w = __funnelshift_r(w, hi, sh);
     }
-    return w & ((1u << VEC) - 1u);
+    return w;
 }
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -41,46 +38,39 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void unpack(const uint4& r, float (&z)[VEC]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    if constexpr (sizeof(T) == 2) {
+// -inf where the bit of a vector's element is 0
+__device__ __forceinline__ uint4 hide(uint4 r, uint32_t ok, const __nv_bfloat16*) {
+    uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            z[2 * i] = __uint_as_float(w[i] << 16);
-            z[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = __uint_as_float(w[i]);
-    }
-}
-template <typename T, int VEC>
-__device__ __forceinline__ uint4 pack(const float (&z)[VEC]) {
-    uint32_t w[4];
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(z[2 * i], z[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(z[i]);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t keep = (ok >> (2 * i) & 1u ? 0x0000FFFFu : 0u) | (ok >> (2 * i + 1) & 1u ? 0xFFFF0000u : 0u);
+        w[i] = (w[i] & keep) | (0xFF80FF80u & ~keep);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 hide(uint4 r, uint32_t ok, const float*) {
+    const uint32_t lowest = 0xFF800000u;
+    return make_uint4(ok & 1u ? r.x : lowest, ok & 2u ? r.y : lowest, ok & 4u ? r.z : lowest, ok & 8u ? r.w : lowest);
 }
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
-// One CTA adjusts a chunk of kLThreads * U vectors of one row.  Tokens that the
-// draft prefix or the bias list name ("special") are marked in a bit map of the
-// chunk first, so that the plain tokens of a vector never look at either list.
-template <typename T, int U>
+// One CTA adjusts a chunk of WORDS * 32 tokens of one row, in two passes.  The first
+// copies the chunk with the mask applied: nearly all of the tokens need no more than
+// that.  The tokens that do (in the history, the draft prefix or the bias list) are
+// gathered into a list from their bit planes, one word of 32 tokens a thread, and the
+// second pass takes them one a thread, reading the logit again.  Left to the threads of
+// the first pass, the few such tokens of a row cost each of their warps the whole
+// arithmetic: that form took 886 us for [256, 8, 128256] bf16.
+template <typename T, int WORDS>
 __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int chunks) {
     constexpr int VEC = 16 / (int)sizeof(T);
-    constexpr int CHUNK = kLThreads * U * VEC;
-    __shared__ uint32_t s_special[CHUNK / 32];
+    constexpr int CHUNK = WORDS * 32;
+    constexpr int U = CHUNK / (kLThreads * VEC);
+    static_assert(U * kLThreads * VEC == CHUNK && WORDS <= kLThreads, "whole vectors for every thread");
+    __shared__ uint32_t s_ok[WORDS], s_seen[WORDS], s_special[WORDS];
+    __shared__ uint16_t s_list[CHUNK];
+    __shared__ int s_count;
     __shared__ int s_bias_at[kLWarps][kLBiasCap];
     __shared__ float s_bias_val[kLWarps][kLBiasCap];
     __shared__ int s_bias_n[kLWarps];
@@ -92,8 +82,8 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int
     const int V = (int)a.V, b = (int)(row / a.N), i = (int)(row % a.N);
     const T* in = (const T*)a.logits + b * a.logits_stride_b + i * a.logits_stride_n;
     T* out = (T*)a.out + b * a.out_stride_b + i * a.out_stride_n;
-    // vectors lie on 16-byte boundaries of the row's memory: vector j covers the
-    // tokens j * VEC - skew and on
+    // vectors lie on 16-byte boundaries of the row's memory: the chunk begins up to a
+    // vector before its place
     const int skew = (int)(((uintptr_t)in & 15u) / sizeof(T));
     const bool vec = (((uintptr_t)in ^ (uintptr_t)out) & 15u) == 0;
     const int first = chunk * CHUNK - skew;
@@ -115,11 +105,7 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int
         for (int e = max(first, 0) + t; e < min(first + CHUNK, V); e += kLThreads) store1(out + e, NAN);
         return;
     }
-    const uint32_t* seen = a.seen ? a.seen + slot * a.words : nullptr;
-    const uint32_t* produced = a.seen ? a.produced + slot * a.words : nullptr;
-    const int32_t* counts = a.seen ? a.counts + slot * a.V : nullptr;
     const uint32_t* mask = a.mask ? a.mask + b * a.mask_stride_b + i * a.mask_stride_n : nullptr;
-
     const int nprefix = a.draft_tokens ? (int)min((int64_t)i, a.draft_len) : 0;
     int blo = 0, bhi = 0;
     if (a.bias_ids) {
@@ -128,32 +114,30 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int
     }
     const bool special = nprefix > 0 || bhi > blo;
 
-    // masks, then the logits that they leave
-    uint32_t ok[U];
+    uint32_t ok = 0xFFFFFFFFu, seen = 0u;
+    if (t < WORDS) {
+        if (mask) ok = plane_word(mask, first + 32 * t, V);
+        if (a.seen) seen = plane_word(a.seen + slot * a.words, first + 32 * t, V);
+        s_ok[t] = ok;
+        s_seen[t] = seen;
+        s_special[t] = 0u;
+    }
+    if (t == 0) s_count = 0;
+    __syncthreads();
+
+    // the logits that the mask leaves; a vector that it hides whole is not read
     uint4 raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int e0 = first + (u * kLThreads + t) * VEC;
-        ok[u] = mask ? plane_bits<VEC>(mask, e0, V) : ((1u << VEC) - 1u);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int e0 = first + (u * kLThreads + t) * VEC;
+        const int at = (u * kLThreads + t) * VEC, e0 = first + at;
+        const uint32_t m = (s_ok[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
         raw[u] = make_uint4(0, 0, 0, 0);
-        if (ok[u] && e0 >= 0 && e0 + VEC <= V && vec) raw[u] = *reinterpret_cast<const uint4*>(in + e0);
-    }
-    uint32_t was[U], made[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int e0 = first + (u * kLThreads + t) * VEC;
-        was[u] = seen ? plane_bits<VEC>(seen, e0, V) & ok[u] : 0u;
-        made[u] = was[u] ? plane_bits<VEC>(produced, e0, V) & ok[u] : 0u;
+        if (m && vec && e0 >= 0 && e0 + VEC <= V) raw[u] = *reinterpret_cast<const uint4*>(in + e0);
     }
 
+    // the tokens that need more
     bool overflow = false;
     if (special) {
-        for (int w = t; w < CHUNK / 32; w += kLThreads) s_special[w] = 0u;
-        __syncthreads();
         if (t < nprefix) {
             const int x = a.draft_tokens[b * a.draft_stride + t];
             s_draft[t] = x;
@@ -183,64 +167,70 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int
         if (lane == 0) s_bias_n[warp] = n;
         overflow = __syncthreads_or(n > kLBiasCap);
     }
+    if (special || a.seen) {
+        // (the list's order differs from run to run; what is done to a token does not depend on it)
+        if (t < WORDS) {
+            uint32_t w = (seen | s_special[t]) & ok;
+            if (w) {
+                int k = atomicAdd(&s_count, __popc(w));
+                for (; w; w &= w - 1) s_list[k++] = (uint16_t)(32 * t + __ffs(w) - 1);
+            }
+        }
+    }
 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int at0 = (u * kLThreads + t) * VEC, e0 = first + at0;
-        if (e0 >= V || e0 + VEC <= 0) continue;
-        const bool whole = e0 >= 0 && e0 + VEC <= V && vec;
-        float z[VEC];
-        unpack<T, VEC>(raw[u], z);
-        if (!whole) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (e0 + v >= 0 && e0 + v < V && (ok[u] >> v & 1u)) z[v] = load1(in + e0 + v);
-        }
-        uint32_t spec = 0;
-        if (special) spec = (s_special[at0 >> 5] >> (at0 & 31)) & ((1u << VEC) - 1u) & ok[u];
-        if (was[u] | spec) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                if (!((was[u] | spec) >> v & 1u)) continue;
-                int n = (made[u] >> v & 1u) ? counts[e0 + v] : 0;
-                bool hit = was[u] >> v & 1u;
-                if (spec >> v & 1u) {
-                    int own = 0;
-                    for (int j = 0; j < nprefix; ++j) own += s_draft[j] == e0 + v;
-                    n += own;
-                    hit |= own > 0;
-                }
-                float x = z[v];
-                if (hit) {
-                    x = x > 0.0f ? x / rep : x * rep;
-                    x -= freq * (float)n;
-                    if (n > 0) x -= pres;
-                }
-                if (spec >> v & 1u) {
-                    float add = 0.0f;
-                    if (!overflow) {
-                        for (int w = 0; w < kLWarps; ++w)
-                            for (int j = 0; j < s_bias_n[w]; ++j)
-                                if (s_bias_at[w][j] == at0 + v) add += s_bias_val[w][j];
-                    } else {
-                        for (int j = blo; j < bhi; ++j)
-                            if (a.bias_ids[j] == e0 + v) add += a.bias_values[j];
-                    }
-                    x += add;
-                }
-                z[v] = x;
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v)
-            if (!(ok[u] >> v & 1u)) z[v] = -INFINITY;
-        if (whole) {
-            *reinterpret_cast<uint4*>(out + e0) = pack<T, VEC>(z);
+        const int at = (u * kLThreads + t) * VEC, e0 = first + at;
+        const uint32_t m = (s_ok[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
+        if (vec && e0 >= 0 && e0 + VEC <= V) {
+            *reinterpret_cast<uint4*>(out + e0) = hide(raw[u], m, in);
         } else {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                if (e0 + v >= 0 && e0 + v < V) store1(out + e0 + v, z[v]);
+            for (int v = 0; v < VEC; ++v) {
+                const int e = e0 + v;
+                if (e >= 0 && e < V) {
+                    if (m >> v & 1u)
+                        out[e] = in[e];
+                    else
+                        store1(out + e, -INFINITY);
+                }
+            }
         }
+    }
+    if (!special && !a.seen) return;
+    __syncthreads();  // the list; and the copies of these logits, which the next stores replace
+
+    const int32_t* counts = a.seen ? a.counts + slot * a.V : nullptr;
+    for (int k = t; k < s_count; k += kLThreads) {
+        const int at = s_list[k], e = first + at;
+        float x = load1(in + e);  // unchanged by the copy, in place too
+        bool hit = s_seen[at >> 5] >> (at & 31) & 1u;
+        int n = hit ? counts[e] : 0;
+        const bool sp = s_special[at >> 5] >> (at & 31) & 1u;
+        if (sp) {
+            int own = 0;
+            for (int j = 0; j < nprefix; ++j) own += s_draft[j] == e;
+            n += own;
+            hit |= own > 0;
+        }
+        if (hit) {
+            x = x > 0.0f ? x / rep : x * rep;
+            x -= freq * (float)n;
+            if (n > 0) x -= pres;
+        }
+        if (sp) {
+            float add = 0.0f;
+            if (!overflow) {
+                for (int w = 0; w < kLWarps; ++w)
+                    for (int j = 0; j < s_bias_n[w]; ++j)
+                        if (s_bias_at[w][j] == at) add += s_bias_val[w][j];
+            } else {
+                for (int j = blo; j < bhi; ++j)
+                    if (a.bias_ids[j] == e) add += a.bias_values[j];
+            }
+            x += add;
+        }
+        store1(out + e, x);
     }
 }
 
@@ -251,10 +241,7 @@ __global__ void history_clear_kernel(sv_history_args a) {
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
     const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     for (int64_t i = t; i < a.V; i += step) a.counts[slot * a.V + i] = 0;
-    for (int64_t i = t; i < a.words; i += step) {
-        a.seen[slot * a.words + i] = 0u;
-        a.produced[slot * a.words + i] = 0u;
-    }
+    for (int64_t i = t; i < a.words; i += step) a.seen[slot * a.words + i] = 0u;
 }
 
 // integer atomics only: the result does not depend on their order
@@ -269,23 +256,18 @@ __global__ void history_add_kernel(sv_history_args a) {
         const int x = a.tokens[b * a.tokens_stride + j];
         if (x < 0 || x >= a.V) continue;
         atomicOr(a.seen + slot * a.words + (x >> 5), 1u << (x & 31));
-        if (j >= prompt) {
-            atomicOr(a.produced + slot * a.words + (x >> 5), 1u << (x & 31));
-            atomicAdd(a.counts + slot * a.V + x, 1);
-        }
+        if (j >= prompt) atomicAdd(a.counts + slot * a.V + x, 1);
     }
 }
 
-template <typename T, int U>
+template <typename T, int WORDS>
 cudaError_t launch_logits(const sv_logits_args& a, cudaStream_t s) {
-    constexpr int VEC = 16 / (int)sizeof(T);
-    // a row that starts off a 16-byte boundary needs up to one vector more
-    const int64_t nvec = (a.V + VEC - 1) / VEC + (VEC > 1 ? 1 : 0);
+    constexpr int64_t VEC = 16 / (int)sizeof(T), CHUNK = WORDS * 32;
+    // a row that starts off a 16-byte boundary begins up to VEC - 1 tokens before its first chunk
     const bool aligned = ((uintptr_t)a.logits & 15u) == 0 && (a.logits_stride_b * sizeof(T)) % 16 == 0 &&
                          (a.logits_stride_n * sizeof(T)) % 16 == 0;
-    const int64_t need = aligned ? (a.V + VEC - 1) / VEC : nvec;
-    const int64_t chunks = (need + kLThreads * U - 1) / (kLThreads * U);
-    logits_kernel<T, U><<<(unsigned)(a.B * a.N * chunks), kLThreads, 0, s>>>(a, (int)chunks);
+    const int64_t chunks = (a.V + (aligned ? 0 : VEC - 1) + CHUNK - 1) / CHUNK;
+    logits_kernel<T, WORDS><<<(unsigned)(a.B * a.N * chunks), kLThreads, 0, s>>>(a, (int)chunks);
     return cudaGetLastError();
 }
 
@@ -300,7 +282,7 @@ extern "C" int spec_verify_history_add(const sv_history_args* args, void* stream
     if (a.B > 65535 || a.V > SV_MAX_VOCAB || a.L > 0x7FFFFFFF) return SV_ETOO_LARGE;
     if (!a.slot_of && a.B > a.slots) return SV_EINVAL;
     if (a.B == 0) return SV_OK;
-    if (!a.seen || !a.produced || !a.counts || (!a.tokens && a.L > 0)) return SV_EINVAL;
+    if (!a.seen || !a.counts || (!a.tokens && a.L > 0)) return SV_EINVAL;
     cudaStream_t s = (cudaStream_t)stream;
     if (a.clear) {
         sv::history_clear_kernel<<<dim3((unsigned)((a.V + 4095) / 4096), (unsigned)a.B), 256, 0, s>>>(a);
@@ -327,21 +309,20 @@ extern "C" int spec_verify_process_logits(const sv_logits_args* args, void* stre
     // two output rows on the same memory would race
     if (a.N > 1 && a.out_stride_n < a.V) return SV_EINVAL;
     if (a.B > 1 && a.out_stride_b < a.V) return SV_EINVAL;
-    if (a.seen && (!a.produced || !a.counts || a.slots < 0 || a.words < (a.V + 31) / 32)) return SV_EINVAL;
+    if (a.seen && (!a.counts || a.slots < 0 || a.words < (a.V + 31) / 32)) return SV_EINVAL;
     if (a.seen && !a.slot_of && a.B > a.slots) return SV_EINVAL;
     if (a.draft_tokens && (a.draft_len < 0 || a.draft_stride < 0)) return SV_EINVAL;
     if (a.bias_ids && (!a.bias_values || !a.bias_offsets || a.bias_total < 0 || a.bias_total > 0x7FFFFFFF))
         return SV_EINVAL;
     if (a.mask && (a.mask_stride_b < 0 || a.mask_stride_n < 0)) return SV_EINVAL;
-    const int64_t chunks = (a.V + 1) / (sv::kLThreads * (16 / (int)es)) + 2;  // an upper bound
-    if (a.B * a.N * chunks > 0x7FFFFFFF) return SV_ETOO_LARGE;
+    if (a.B * a.N * ((a.V + 7) / 2048 + 1) > 0x7FFFFFFF) return SV_ETOO_LARGE;
     cudaStream_t s = (cudaStream_t)stream;
-    // 64 bytes a thread where that still leaves every SM several CTAs, else 16
-    const bool wide = a.B * a.N * ((a.V * (int64_t)es + 16383) / 16384) >= 2048;
+    // chunks of 8192 tokens where that still leaves every SM several CTAs, else of 2048
+    const bool wide = a.B * a.N * ((a.V + 8191) / 8192) >= 2048;
     cudaError_t e;
     if (a.dtype == SV_BF16)
-        e = wide ? sv::launch_logits<__nv_bfloat16, 4>(a, s) : sv::launch_logits<__nv_bfloat16, 1>(a, s);
+        e = wide ? sv::launch_logits<__nv_bfloat16, 256>(a, s) : sv::launch_logits<__nv_bfloat16, 64>(a, s);
     else
-        e = wide ? sv::launch_logits<float, 4>(a, s) : sv::launch_logits<float, 1>(a, s);
+        e = wide ? sv::launch_logits<float, 256>(a, s) : sv::launch_logits<float, 64>(a, s);
     return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }

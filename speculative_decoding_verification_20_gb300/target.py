@@ -35,8 +35,8 @@ ROW_BAD_PAGE = 0x800
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: SV_F16}
 
 # the C structures are runs of 8-byte fields, filled in one go
-_HISTORY = struct.Struct("<Q3Q3q2Q3q2Qq")
-_LOGITS = struct.Struct("<Q2Q4q4q3Q2q2Q2q3Q3QqQ2qQ")
+_HISTORY = struct.Struct("<Q2Q3q2Q3q2Qq")
+_LOGITS = struct.Struct("<Q2Q4q4q2Q2q2Q2q3Q3QqQ2qQ")
 _CACHE = "2Q8qQ2q2Q"
 _ROTATE = struct.Struct("<Q4Q6q12qQ3q" + _CACHE + "Q")
 _ATTENTION = struct.Struct("<Q2Q6q6qd2q" + _CACHE + "QqQQ")
@@ -118,7 +118,7 @@ class _On:
 class TokenHistory:
     """The tokens that the penalties of ``process_logits`` count, for ``slots`` sequences.
 
-    seen, produced: int32 [slots, words] bit planes (token t: bit t % 32 of word t // 32);
+    seen: int32 [slots, words], a bit plane (token t: bit t % 32 of word t // 32);
     counts: int32 [slots, V], occurrences in the output.
     """
 
@@ -128,7 +128,6 @@ class TokenHistory:
         self.slots, self.vocab = slots, vocab
         self.words = (vocab + 127) // 128 * 4
         self.seen = torch.zeros((slots, self.words), dtype=torch.int32, device=device)
-        self.produced = torch.zeros((slots, self.words), dtype=torch.int32, device=device)
         self.counts = torch.zeros((slots, vocab), dtype=torch.int32, device=device)
 
     def _call(self, tokens, prompt_lens, total_lens, slots, clear, stream):
@@ -149,9 +148,9 @@ class TokenHistory:
             tl = _vec(total_lens, B, torch.int32, dev, "total_lens")
             lib, check = _api()
             check(lib.spec_verify_history_add(_HISTORY.pack(
-                _HISTORY.size, _p(self.seen), _p(self.produced), _p(self.counts), self.slots, self.words, self.vocab,
+                _HISTORY.size, _p(self.seen), _p(self.counts), self.slots, self.words, self.vocab,
                 _p(slot_of), _p(tokens), B, L, tokens.stride(0), _p(pl), _p(tl), int(clear)), on.handle()))
-            on.keep(tokens, slot_of, pl, tl, self.seen, self.produced, self.counts)
+            on.keep(tokens, slot_of, pl, tl, self.seen, self.counts)
 
     def load(self, tokens, prompt_lens=None, total_lens=None, slots=None, *, stream=None) -> None:
         """New sequences take their slots: of row b of tokens [B, L] the first prompt_lens[b] (default: none) are
@@ -190,12 +189,12 @@ def process_logits(logits: torch.Tensor, *, history: Optional[TokenHistory] = No
         elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev or \
                 (V > 1 and out.stride(2) != 1):
             raise ValueError("out must have the logits' shape, type and device, and a contiguous vocabulary")
-        seen = produced = counts = slot_of = None
+        seen = counts = slot_of = None
         nslots = words = 0
         if history is not None:
             if history.vocab != V or history.counts.device != dev:
                 raise ValueError(f"the history is of {history.vocab} tokens on {history.counts.device}")
-            seen, produced, counts = history.seen, history.produced, history.counts
+            seen, counts = history.seen, history.counts
             nslots, words = history.slots, history.words
             slot_of = _vec(slots, B, torch.int32, dev, "slots")
             if slot_of is None and B > nslots:
@@ -228,11 +227,11 @@ def process_logits(logits: torch.Tensor, *, history: Optional[TokenHistory] = No
         lib, check = _api()
         check(lib.spec_verify_process_logits(_LOGITS.pack(
             _LOGITS.size, _p(x), _p(out), code, B, N, V, x.stride(0), x.stride(1), out.stride(0), out.stride(1),
-            _p(seen), _p(produced), _p(counts), nslots, words, _p(slot_of),
+            _p(seen), _p(counts), nslots, words, _p(slot_of),
             _p(toks), 0 if toks is None else toks.stride(0), 0 if toks is None else toks.shape[1],
             _p(rep), _p(freq), _p(pres), _p(ids), _p(vals), _p(offs), 0 if ids is None else ids.numel(),
             _p(mask), msb, msn, _p(st)), on.handle()))
-        on.keep(x, out, seen, produced, counts, slot_of, toks, rep, freq, pres, ids, vals, offs, mask, st)
+        on.keep(x, out, seen, counts, slot_of, toks, rep, freq, pres, ids, vals, offs, mask, st)
     return out
 
 

@@ -48,7 +48,7 @@ def test_structures_match_the_header(lib, tmp_path):
 
 
 def test_history_refusals(lib):
-    base = dict(size=None, seen=GOOD, produced=GOOD, counts=GOOD, slots=4, words=4, V=100, slot_of=0, tokens=GOOD, B=2,
+    base = dict(size=None, seen=GOOD, counts=GOOD, slots=4, words=4, V=100, slot_of=0, tokens=GOOD, B=2,
                 L=5, stride=5, prompt=0, total=0, clear=0)
     f = lambda **kw: _call(lib.spec_verify_history_add, tg._HISTORY, base, **kw)
     assert lib.spec_verify_history_add(None, None) == -1
@@ -65,11 +65,11 @@ def test_history_refusals(lib):
 
 def test_logits_refusals(lib):
     base = dict(size=None, logits=GOOD, out=GOOD, dtype=0, B=2, N=3, V=100, lb=300, ln=100, ob=300, on=100, seen=0,
-                produced=0, counts=0, slots=0, words=0, slot_of=0, draft=0, ds=0, dl=0, rep=0, freq=0, pres=0, ids=0,
+                counts=0, slots=0, words=0, slot_of=0, draft=0, ds=0, dl=0, rep=0, freq=0, pres=0, ids=0,
                 vals=0, offs=0, nbias=0, mask=0, mb=0, mn=0, status=0)
     f = lambda **kw: _call(lib.spec_verify_process_logits, tg._LOGITS, base, **kw)
     assert lib.spec_verify_process_logits(None, None) == -1
-    assert f(size=240) == -1
+    assert f(size=232) == -1
     assert f(B=0) == 0
     assert f(dtype=2) == -2
     assert f(N=0) == -1
@@ -80,9 +80,9 @@ def test_logits_refusals(lib):
     assert f(out=GOOD + 2) == -1
     assert f(on=99) == -1  # output rows on one another
     assert f(ob=0) == -1
-    assert f(seen=GOOD, produced=GOOD, counts=GOOD, slots=4, words=3) == -1
-    assert f(seen=GOOD, produced=GOOD, counts=GOOD, slots=1, words=4) == -1
-    assert f(seen=GOOD, produced=0, counts=GOOD, slots=4, words=4) == -1
+    assert f(seen=GOOD, counts=GOOD, slots=4, words=3) == -1
+    assert f(seen=GOOD, counts=GOOD, slots=1, words=4) == -1
+    assert f(seen=GOOD, counts=0, slots=4, words=4) == -1
     assert f(ids=GOOD, vals=GOOD, offs=0, nbias=4) == -1
     assert f(ids=GOOD, vals=GOOD, offs=GOOD, nbias=-1) == -1
     assert f(draft=GOOD, ds=-1) == -1

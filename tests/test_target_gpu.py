@@ -194,8 +194,8 @@ def test_history_load_add_and_slots():
     h.load(torch.tensor([[1, 2, 3, 2, 999], [5, 5, 5, 5, 5]], dtype=torch.int32, device="cuda"), [2, 0], [5, 3], [4, 1])
     c = h.counts.cpu()
     assert c[4, 1] == 0 and c[4, 2] == 1 and c[4, 3] == 1 and c[4, 999] == 1 and c[1, 5] == 3 and int(c.sum()) == 6
-    seen, made = ref.bits_of(h.seen, V).cpu(), ref.bits_of(h.produced, V).cpu()
-    assert seen[4].nonzero().flatten().tolist() == [1, 2, 3, 999] and made[4].nonzero().flatten().tolist() == [2, 3, 999]
+    seen = ref.bits_of(h.seen, V).cpu()
+    assert seen[4].nonzero().flatten().tolist() == [1, 2, 3, 999] and seen[1].nonzero().flatten().tolist() == [5]
     h.add(torch.tensor([[7, 7, -1, -1], [1000, 5, 2 ** 31 - 1, -5]], dtype=torch.int32, device="cuda"), slots=[4, 1])
     c = h.counts.cpu()
     assert c[4, 7] == 2 and c[1, 5] == 4 and int(c.sum()) == 9
