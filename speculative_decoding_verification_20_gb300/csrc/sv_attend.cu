@@ -10,8 +10,8 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
 
-// rows of a cache head's tile: 16 or 32 as the rows of a sequence need
-int row_tile(int64_t N, int64_t group) { return N * group <= 16 ? 16 : 32; }
+// rows of a cache head's tile: 16 or 32 where that holds a sequence's rows, else 256
+int row_tile(int64_t N, int64_t group) { return N * group <= 16 ? 16 : N * group <= 32 ? 32 : 256; }
 
 int check_attention(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads, int64_t dim) {
     if (B < 0 || N < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads) return SV_EINVAL;
@@ -99,7 +99,10 @@ extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream
     p.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     if (tiles < p.ctas) p.ctas = (int)tiles;
     cudaStream_t s = (cudaStream_t)stream;
-    if (launch_attend_rows((int)a.dtype, (int)a.dim, rm / 16, p, s) != cudaSuccess) return SV_ECUDA;
+    const unsigned long long wait_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNs;
+    const cudaError_t e = rm == 256 ? launch_attend_tiles((int)a.dtype, (int)a.dim, p, wait_ns, s)
+                                    : launch_attend_rows((int)a.dtype, (int)a.dim, rm / 16, p, s);
+    if (e != cudaSuccess) return SV_ECUDA;
     if (launch_attend_join((int)a.dtype, (int)a.dim, rm, p, s) != cudaSuccess) return SV_ECUDA;
     return SV_OK;
 }

@@ -213,6 +213,7 @@ __device__ __forceinline__ float fast_exp2(float x) {  // 2^x; 2^-inf = 0
 
 // the two kernels' launchers (RM rows a tile) and the join of the cut units
 cudaError_t launch_attend_rows(int dtype, int dim, int mt, const AttendArgs& p, cudaStream_t s);
+cudaError_t launch_attend_tiles(int dtype, int dim, const AttendArgs& p, unsigned long long wait_ns, cudaStream_t s);
 cudaError_t launch_attend_join(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s);
 
 }  // namespace sv

@@ -376,56 +376,57 @@ template <typename T, int D, int RM>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ AttendArgs p) {
     constexpr int PER = D / 32;  // columns a lane
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31, r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    long long c = blockIdx.x;
-    const Cut k = p.cut[c];
+    const int lane = threadIdx.x & 31;
+    const Cut k = p.cut[blockIdx.x];
     if (k.total == 0) return;
     // CTA c has the tiles [total * c / ctas, total * (c + 1) / ctas)
-    const long long ctas = min((long long)p.ctas, k.total);
-    if (k.total * c / ctas == k.base || c == 0 || k.total * (c - 1) / ctas > k.base) return;
-    const int rr = k.rt * RM + r;
-    if (rr >= k.n * p.group) return;
+    const long long ctas = min((long long)p.ctas, k.total), c0 = blockIdx.x;
+    if (k.total * c0 / ctas == k.base || c0 == 0 || k.total * (c0 - 1) / ctas > k.base) return;
     Unit u;
     u.b = k.b;
     u.h = k.h;
-    float top = -INFINITY, l = 0.0f, acc[PER];
+    const int rows = min(RM, k.n * p.group - k.rt * RM);
+    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
+         r += gridDim.y * (kJoinThreads / 32)) {
+        float top = -INFINITY, l = 0.0f, acc[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
 #pragma unroll 4
-    for (--c; c < ctas; ++c) {
-        const long long from = k.total * c / ctas;
-        if (from >= k.end) break;
-        const int64_t place = 2 * c + (from >= k.base ? 0 : 1);
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
-        float x[PER];
-        const float* src = p.part_o + (place * RM + r) * D + lane * PER;
-        if constexpr (PER == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(src);
-            x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-        } else {
-            const float2 y = *reinterpret_cast<const float2*>(src);
-            x[0] = y.x, x[1] = y.y;
-        }
-        if (ml.x == -INFINITY) {
-            l += ml.y;  // 0, or the NaN of a bad page
-            continue;
-        }
-        const float now = fmaxf(top, ml.x);
-        const float fa = fast_exp2(top - now), fb = fast_exp2(ml.x - now);
+        for (long long c = c0 - 1; c < ctas; ++c) {
+            const long long from = k.total * c / ctas;
+            if (from >= k.end) break;
+            const int64_t place = 2 * c + (from >= k.base ? 0 : 1);
+            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
+            float x[PER];
+            const float* src = p.part_o + (place * RM + r) * D + lane * PER;
+            if constexpr (PER == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(src);
+                x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(src);
+                x[0] = y.x, x[1] = y.y;
+            }
+            if (ml.x == -INFINITY) {
+                l += ml.y;  // 0, or the NaN of a bad page or a wait that ran out
+                continue;
+            }
+            const float now = fmaxf(top, ml.x);
+            const float fa = fast_exp2(top - now), fb = fast_exp2(ml.x - now);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = acc[i] * fa + x[i] * fb;
-        l = l * fa + ml.y * fb;
-        top = now;
+            for (int i = 0; i < PER; ++i) acc[i] = acc[i] * fa + x[i] * fb;
+            l = l * fa + ml.y * fb;
+            top = now;
+        }
+        const float inv = 1.0f / l;
+        uint32_t w[PER / 2];
+#pragma unroll
+        for (int i = 0; i < PER / 2; ++i) w[i] = Pair<T>::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+        T* dst = out_row<T>(p, u, k.rt * RM + r) + lane * PER;
+        if constexpr (PER == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t*>(dst) = w[0];
     }
-    const float inv = 1.0f / l;
-    uint32_t w[PER / 2];
-#pragma unroll
-    for (int i = 0; i < PER / 2; ++i) w[i] = Pair<T>::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    T* dst = out_row<T>(p, u, rr) + lane * PER;
-    if constexpr (PER == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    else
-        *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
 template <typename T, int D, int MT>
@@ -444,7 +445,7 @@ cudaError_t launch_join(const AttendArgs& p, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)p.ctas, RM / (kJoinThreads / 32));
+    cfg.gridDim = dim3((unsigned)p.ctas, RM < 64 ? RM / (kJoinThreads / 32) : 8);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = attr;
@@ -463,14 +464,15 @@ cudaError_t launch_attend_rows(int dtype, int dim, int mt, const AttendArgs& p, 
     return mt == 1 ? launch_rows<__half, 128, 1>(p, s) : launch_rows<__half, 128, 2>(p, s);
 }
 
+template <typename T, int D>
+cudaError_t join_of(int rm, const AttendArgs& p, cudaStream_t s) {
+    return rm == 16 ? launch_join<T, D, 16>(p, s) : rm == 32 ? launch_join<T, D, 32>(p, s) : launch_join<T, D, 256>(p, s);
+}
+
 cudaError_t launch_attend_join(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s) {
-    if (dtype == SV_BF16) {
-        if (dim == 64)
-            return rm == 16 ? launch_join<__nv_bfloat16, 64, 16>(p, s) : launch_join<__nv_bfloat16, 64, 32>(p, s);
-        return rm == 16 ? launch_join<__nv_bfloat16, 128, 16>(p, s) : launch_join<__nv_bfloat16, 128, 32>(p, s);
-    }
-    if (dim == 64) return rm == 16 ? launch_join<__half, 64, 16>(p, s) : launch_join<__half, 64, 32>(p, s);
-    return rm == 16 ? launch_join<__half, 128, 16>(p, s) : launch_join<__half, 128, 32>(p, s);
+    if (dtype == SV_BF16)
+        return dim == 64 ? join_of<__nv_bfloat16, 64>(rm, p, s) : join_of<__nv_bfloat16, 128>(rm, p, s);
+    return dim == 64 ? join_of<__half, 64>(rm, p, s) : join_of<__half, 128>(rm, p, s);
 }
 
 }  // namespace sv

@@ -1,0 +1,690 @@
+// sv_attend_tiles.cu -- attention of many query rows a cache head: chunks of a prompt, and
+// rounds whose group fills a tile.
+//
+// Here the products bound the call, so they run on the tensor cores' own memory
+// (tcgen05): a unit is 256 query rows, two tiles of 128 that share every key tile of 128
+// keys.  Twelve warps, one job each:
+//   warps 0-3, 4-7  the softmax of one row tile each, a thread a row: scores from tensor
+//                   memory, weights back to it (in place of the scores), output rows at the end
+//   warp 8          issues the products: S = Q K^T from shared memory, O += P V with P from
+//                   tensor memory
+//   warp 9          loads keys and values by TMA, page by page, into a ring
+// While one tile's softmax runs, the products of the other fill the tensor cores:
+// PV and the next S of tile A, then those of tile B.  The output stays in tensor memory
+// over all keys; the running maximum it refers to is only raised when a row's scores
+// outgrow it by 2^8, so that rescaling the output is rare.  Weights of up to 2^8 lose
+// nothing in the 16-bit types' relative step, and sums are 32-bit.
+//
+// Pages become boxes of gcd(page_size, 128) keys x 64 elements.  A box with no visible
+// key, or on a bad page, is loaded from past the last page, where TMA gives zeros: its
+// scores are masked, and its values add nothing.  Rows of a box past the sequence's end
+// are zeroed in shared memory before their product, since they may hold anything.
+//
+// Every wait has a limit.  When one runs out, the CTA writes NaN for what is left of its
+// part, sets SV_ROW_INTERNAL, lets its copies and products finish (with a limit) and ends.
+#include <cuda.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "sv_attend.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kTThreads = 384;
+// registers a thread: softmax warps, the others; their sum has to fit the launch's share
+constexpr int kSoftRegs = 208, kOtherRegs = 72;
+constexpr int kTRows = 256;
+constexpr int kBadSlots = 16;  // units that the loader can be ahead by, and more
+
+template <int D>
+struct TilesCfg {
+    static constexpr int kTileBytes = kKeyTile * D * 2;
+    static constexpr int kQBytes = kTRows * D * 2;
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kHalves = D / 64;                // 128-byte columns of a tile
+    static constexpr int kHalfBytes = kKeyTile * 128;     // 128 rows of one
+    static constexpr int kSmem = kQBytes + kStages * kTileBytes + 1024;  // and room to align
+    // tensor memory columns: scores (and weights) of the two tiles, then their outputs
+    static constexpr int kS = 0, kO = 256;
+};
+
+struct TilesArgs {
+    AttendArgs p;
+    unsigned long long wait_ns;
+    int box;  // keys of a box
+};
+
+// ---- barriers ------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint64_t* b, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    return ok;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// without the hardware's own patience
+__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    return ok;
+}
+// False once the wait has run out, here or (dead) in another warp of the CTA.  A limit
+// below the device timer's tick means one look.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, unsigned long long limit, volatile int* dead) {
+    if (limit < 1000) {
+        if (bar_test(b, parity)) return true;
+        *dead = 1;
+        return false;
+    }
+    if (bar_try(b, parity)) return true;
+    const unsigned long long t0 = now_ns();
+    while (!bar_try(b, parity)) {
+        if (*dead) return false;
+        if (now_ns() - t0 >= limit) {
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// ---- tensor memory and products -------------------------------------------
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
+    // rows of 128 bytes, swizzled in groups of 8 rows (1024 bytes)
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t half_bytes) {
+    // the same memory read across: 64 contiguous elements of N, blocks of them half_bytes
+    // apart; groups of 8 keys 1024 bytes apart
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(half_bytes >> 4) << 16) | (64ull << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+#define SV_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), \
+                    "=r"(a[i + 6]), "=r"(a[i + 7])
+#define SV_I8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), \
+                    "r"(a[i + 6]), "r"(a[i + 7])
+// 32 columns of the thread's row; the values are there when this returns
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24)
+        : "r"(addr)
+        : "memory");
+}
+// 128 columns
+__device__ __forceinline__ void tmem_load128(uint32_t addr, uint32_t* r) {
+    asm volatile(
+        "{\n.reg .b32 a1, a2, a3;\nadd.u32 a1, %128, 32;\nadd.u32 a2, %128, 64;\nadd.u32 a3, %128, 96;\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,"
+        "%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [a1];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,"
+        "%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [a2];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,"
+        "%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [a3];\n"
+        "tcgen05.wait::ld.sync.aligned;\n}\n"
+        : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24), SV_R8(r, 32), SV_R8(r, 40), SV_R8(r, 48), SV_R8(r, 56),
+          SV_R8(r, 64), SV_R8(r, 72), SV_R8(r, 80), SV_R8(r, 88), SV_R8(r, 96), SV_R8(r, 104), SV_R8(r, 112),
+          SV_R8(r, 120)
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        SV_I8(r, 0), SV_I8(r, 8), SV_I8(r, 16), SV_I8(r, 24)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                        uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4,%5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// the visible keys of a unit's rows
+__device__ __forceinline__ void unit_keys(const AttendArgs& p, const Unit& u, int& lo, int& hi) {
+    const int r0 = u.rt * kTRows, r1 = min(r0 + kTRows, u.n * p.group) - 1;
+    hi = u.past + r1 / p.group;
+    lo = p.a.window > 0 ? (int)max((int64_t)0, u.past + r0 / p.group + 1 - p.a.window) : 0;
+}
+
+// How many bits of the tensor cores' kind::f16 instruction: fp32 results, T operands,
+// B across (values) or along (keys) its rows
+template <typename T>
+__device__ constexpr uint32_t idesc(int n, bool b_across) {
+    const uint32_t f = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | (b_across ? 1u << 16 : 0u) | ((uint32_t)(n / 8) << 17) | (8u << 24);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTThreads, 1)
+    attend_tiles_kernel(const __grid_constant__ TilesArgs ta, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+    using C = TilesCfg<D>;
+    const AttendArgs& p = ta.p;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];     // ring of key and value tiles
+    __shared__ uint64_t s_q[2], s_scores[2], s_weights[2], s_out[2];  // per row tile
+    __shared__ uint64_t s_last;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_dead;
+    __shared__ int s_bad[kBadSlots];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    grid_dependents_go();
+    // swizzled tiles start on 1024-byte boundaries
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    unsigned char* smem_p = smem_raw + (smem - smem_u32(smem_raw));
+    const uint32_t q_s = smem, ring_s = smem + C::kQBytes;
+    fill_idle_rows<T, kTThreads>(p);
+    Part part;
+    find_part<kTRows, kTThreads>(p, part);
+    if (part.todo == 0) return;
+
+    if (t == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            bar_init(&s_full[s], 1);
+            bar_init(&s_empty[s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            bar_init(&s_q[x], 128);
+            bar_init(&s_scores[x], 1);
+            bar_init(&s_weights[x], 128);
+            bar_init(&s_out[x], 1);
+        }
+        bar_init(&s_last, 1);
+        s_dead = 0;
+        for (int i = 0; i < kBadSlots; ++i) s_bad[i] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_smem();
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int* dead = &s_dead;
+    const unsigned long long limit = ta.wait_ns;
+    const int tile0 = part.u.t0 + (int)(part.begin - part.base);
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        const int x = warp >> 2;            // row tile
+        const int row = t & 127;            // row of it
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + C::kS + x * 128 + lanes, tO = tmem + C::kO + x * D + lanes;
+        Unit u = part.u;
+        int tile = tile0, left = part.todo, index = 0;
+        uint32_t n_scores = 0, n_out = 0;  // phases seen
+        bool alive = true;
+
+        // the rows of unit w into shared memory, swizzled as the products read them
+        auto load_q = [&](const Unit& w) {
+            const int r = w.rt * kTRows + x * 128 + row, rows = w.n * p.group;
+            if (w.rt * kTRows + x * 128 >= rows) return;
+            unsigned char* dst = smem_p + x * 128 * D * 2 + row * 128;
+            const T* src = q_row<T>(p, w, min(r, rows - 1));
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < rows) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                *reinterpret_cast<uint4*>(dst + (c / 8) * C::kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = v;
+            }
+            fence_async_smem();
+            bar_arrive(&s_q[x]);
+        };
+        load_q(u);
+        while (left > 0) {
+            const int rows = u.n * p.group, r = u.rt * kTRows + x * 128 + row;
+            const int first = tile, end = min(u.t1, tile + left);
+            const bool whole = first == u.t0 && end == u.t1;
+            const bool mine = u.rt * kTRows + x * 128 < rows;  // the tile has rows
+            left -= end - first;
+            Unit next = u;
+            if (left > 0) next_unit<kTRows>(p, next);
+            if (mine) {
+                const int pos = u.past + min(r, rows - 1) / p.group;
+                // of the warp's rows: the least and the greatest position
+                const int wr0 = u.rt * kTRows + x * 128 + (row & ~31);
+                const int pos0 = u.past + min(wr0, rows - 1) / p.group;
+                const int pos1 = u.past + min(wr0 + 31, rows - 1) / p.group;
+                float ref = -INFINITY, sum = 0.0f;
+                for (; alive && tile < end; ++tile) {
+                    alive = bar_wait(&s_scores[x], n_scores & 1, limit, dead);
+                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    if (!alive) break;
+                    ++n_scores;
+                    fence_after();
+                    float s[kKeyTile];
+                    tmem_load128(tS, reinterpret_cast<uint32_t*>(s));
+                    const int k0 = tile * kKeyTile;
+                    if (k0 + kKeyTile - 1 > pos0 || (p.a.window > 0 && k0 <= (int64_t)pos1 - p.a.window)) {
+                        const int64_t from = p.a.window > 0 ? pos - p.a.window + 1 : 0;
+                        const int a = (int)max(from - k0, (int64_t)0), b = pos - k0;  // visible: [a, b]
+#pragma unroll
+                        for (int j = 0; j < kKeyTile; ++j)
+                            if (j < a || j > b) s[j] = -INFINITY;
+                    }
+                    float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int j = 4; j < kKeyTile; j += 4)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[j + e]);
+                    const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.qscale;
+                    if (tile == first) {
+                        ref = m;
+                    } else if (__any_sync(0xFFFFFFFFu, m > ref + 8.0f)) {
+                        // raise the reference; the output so far shrinks by as much
+                        const float now = fmaxf(ref, m);
+                        const float f = now == -INFINITY ? 1.0f : fast_exp2(ref - now);
+                        alive = bar_wait(&s_out[x], n_out & 1, limit, dead);  // the product before this one
+                        alive = __all_sync(0xFFFFFFFFu, alive);
+                        if (!alive) break;
+                        fence_after();
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_load32(tO + c, reinterpret_cast<uint32_t*>(o));
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] *= f;
+                            tmem_store32(tO + c, reinterpret_cast<const uint32_t*>(o));
+                        }
+                        sum *= f;
+                        ref = now;
+                    }
+                    if (tile != first) ++n_out;
+                    const float base = ref == -INFINITY ? 0.0f : ref;  // nothing visible yet: weights 0
+                    float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float a = fast_exp2(fmaf(s[half * 64 + 2 * j], p.qscale, -base));
+                            const float b = fast_exp2(fmaf(s[half * 64 + 2 * j + 1], p.qscale, -base));
+                            add[(2 * j) & 3] += a;
+                            add[(2 * j + 1) & 3] += b;
+                            w[j] = Pair<T>::pack(a, b);  // 16 bits into the product, as the values
+                        }
+                        tmem_store32(tS + half * 32, w);
+                    }
+                    sum += (add[0] + add[1]) + (add[2] + add[3]);
+                    tmem_store_wait();
+                    fence_before();
+                    bar_arrive(&s_weights[x]);
+                }
+                // all scores of the unit are through: its queries make room for the next
+                if (alive && left > 0) load_q(next);
+                if (alive) {
+                    alive = bar_wait(&s_out[x], n_out & 1, limit, dead);
+                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    ++n_out;
+                }
+                fence_after();
+                const bool bad = !alive || s_bad[index % kBadSlots];
+                const int place = 2 * blockIdx.x + (index == 0 ? 0 : 1);
+                const int64_t part_row = (int64_t)place * kTRows + x * 128 + row;
+                const float l = bad ? NAN : sum;
+                const float inv = 1.0f / l;
+                T* dst = r < rows ? out_row<T>(p, u, r) : nullptr;
+                if (!whole && r < rows)
+                    *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(alive ? ref : -INFINITY, l);
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (alive) {
+                        tmem_load32(tO + c, reinterpret_cast<uint32_t*>(o));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+                    }
+                    if (r < rows) {
+                        if (whole) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8)
+                                *reinterpret_cast<uint4*>(dst + c + j) =
+                                    make_uint4(Pair<T>::pack(o[j] * inv, o[j + 1] * inv),
+                                               Pair<T>::pack(o[j + 2] * inv, o[j + 3] * inv),
+                                               Pair<T>::pack(o[j + 4] * inv, o[j + 5] * inv),
+                                               Pair<T>::pack(o[j + 6] * inv, o[j + 7] * inv));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                *reinterpret_cast<float4*>(p.part_o + part_row * D + c + j) =
+                                    make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                    }
+                }
+                fence_before();
+            } else if (alive && left > 0) {
+                load_q(next);
+            }
+            if (!alive && lane == 0 && p.a.row_status) atomicOr(p.a.row_status + u.b, SV_ROW_INTERNAL);
+            u = next;
+            tile = u.t0;
+            ++index;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8) {
+            // ------------------------------------------------------------ products
+            constexpr uint32_t i_s = idesc<T>(kKeyTile, false), i_o = idesc<T>(D, true);
+            Unit u = part.u;
+            int tile = tile0, left = part.todo;
+            uint32_t stage = 0, turn = 0;      // ring place and its phase
+            uint32_t n_q[2] = {0, 0}, n_w[2] = {0, 0};
+            bool alive = true;
+            auto next_stage = [&]() {
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    turn ^= 1;
+                }
+            };
+            auto scores = [&](int x, uint32_t ks) {
+                if (lane == 0) {
+                    const uint32_t qs = q_s + x * 128 * D * 2;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = (k / 4) * C::kHalfBytes + (k % 4) * 32;
+                        mma_ss(tmem + C::kS + x * 128, desc_k_major(qs + at), desc_k_major(ks + at), i_s, k > 0);
+                    }
+                    mma_commit(&s_scores[x]);
+                }
+                __syncwarp();
+            };
+            while (alive && left > 0) {
+                const int rows = u.n * p.group - u.rt * kTRows;
+                const int tiles_x = rows > 128 ? 2 : 1;
+                const int first = tile, end = min(u.t1, tile + left);
+                int lo, hi;
+                unit_keys(p, u, lo, hi);
+                const int vend = u.past + u.n;
+                for (int x = 0; alive && x < tiles_x; ++x) alive = bar_wait(&s_q[x], n_q[x]++ & 1, limit, dead);
+                alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
+                alive = __all_sync(0xFFFFFFFFu, alive);
+                if (!alive) break;
+                fence_after();
+                for (int x = 0; x < tiles_x; ++x) scores(x, ring_s + stage * C::kTileBytes);
+                if (lane == 0) mma_commit(&s_empty[stage]);
+                next_stage();
+                for (; tile < end; ++tile, --left) {
+                    const bool more = tile + 1 < end;
+                    const uint32_t kstage = stage;
+                    if (more) {
+                        alive = bar_wait(&s_full[stage], turn, limit, dead);
+                        next_stage();
+                    }
+                    const uint32_t vstage = stage;
+                    alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
+                    next_stage();
+                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    if (!alive) break;
+                    const uint32_t ks = ring_s + kstage * C::kTileBytes, vs = ring_s + vstage * C::kTileBytes;
+                    // rows of a box outside the visible keys: what they hold times 0 must be 0
+                    const int k0 = tile * kKeyTile;
+                    const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, vend - k0));
+                    const int z0_from = z0 / ta.box * ta.box, z1_to = (z1 + ta.box - 1) / ta.box * ta.box;
+                    if (z0 > z0_from || z1 < z1_to) {
+                        constexpr int RC = D / 8;  // 16-byte pieces of a row
+                        for (int i = lane; i < ((z0 - z0_from) + (z1_to - z1)) * RC; i += 32) {
+                            const int zr = i / RC, c = i % RC;
+                            const int rr = zr < z0 - z0_from ? z0_from + zr : z1 + zr - (z0 - z0_from);
+                            *reinterpret_cast<uint4*>(smem_p + (vs - smem) + (c / 8) * C::kHalfBytes + rr * 128 +
+                                                      ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                    }
+                    for (int x = 0; alive && x < tiles_x; ++x) {
+                        alive = bar_wait(&s_weights[x], n_w[x]++ & 1, limit, dead);
+                        alive = __all_sync(0xFFFFFFFFu, alive);
+                        if (!alive) break;
+                        fence_after();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int k = 0; k < kKeyTile / 16; ++k)
+                                mma_ts(tmem + C::kO + x * D, tmem + C::kS + x * 128 + k * 8,
+                                       desc_mn_major(vs + k * 16 * 128, C::kHalfBytes), i_o, tile > first || k > 0);
+                            mma_commit(&s_out[x]);
+                        }
+                        __syncwarp();
+                        if (more) scores(x, ks);
+                    }
+                    if (!alive) break;
+                    if (lane == 0) {
+                        if (more) mma_commit(&s_empty[kstage]);
+                        mma_commit(&s_empty[vstage]);
+                    }
+                    __syncwarp();
+                }
+                if (alive && left > 0) {
+                    next_unit<kTRows>(p, u);
+                    tile = u.t0;
+                }
+            }
+            // products still in flight end before tensor memory is given back
+            if (lane == 0) mma_commit(&s_last);
+            __syncwarp();
+            const unsigned long long t0 = now_ns();
+            while (!bar_try(&s_last, 0) && now_ns() - t0 < kWaitLimitNs) {}
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ loads
+            Unit u = part.u;
+            int tile = tile0, left = part.todo, index = 0;
+            uint32_t stage = 0, turn = 0;
+            const int page_size = (int)p.a.cache.page_size, per = kKeyTile / ta.box;
+            const bool loads = lane < per * C::kHalves;
+            const int box = lane / C::kHalves, half = lane % C::kHalves;
+            const int no_page = (int)p.a.cache.pages;  // past the last: zeros
+            bool alive = true;
+            int issued = 0;
+            auto put = [&](const CUtensorMap* map, const Unit& w, int page, int in_page) {
+                alive = bar_wait(&s_empty[stage], turn ^ 1, limit, dead);
+                alive = __all_sync(0xFFFFFFFFu, alive);
+                if (!alive) return;
+                if (lane == 0) bar_expect(&s_full[stage], C::kTileBytes);
+                __syncwarp();
+                if (loads)
+                    tma_box(ring_s + stage * C::kTileBytes + half * C::kHalfBytes + box * ta.box * 128, map, half * 64,
+                            in_page, w.h, page, &s_full[stage]);
+                ++issued;
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    turn ^= 1;
+                }
+            };
+            // the lane's box of a tile: page id (bad and invisible ones: no_page)
+            auto find = [&](const Unit& w, int tl, int& page, int& in_page) -> bool {
+                int lo, hi;
+                unit_keys(p, w, lo, hi);
+                const int k = tl * kKeyTile + box * ta.box;
+                page = no_page;
+                in_page = 0;
+                if (!loads || k > hi || k + ta.box <= lo) return false;
+                page = p.a.cache.page_table[w.b * p.a.cache.page_table_stride + k / page_size];
+                in_page = k % page_size;
+                if (page < 0 || page >= no_page) {
+                    page = no_page;
+                    return true;
+                }
+                return false;
+            };
+            while (alive && left > 0) {
+                const int end = min(u.t1, tile + left);
+                int page, in_page, vpage, vin;
+                bool bad = find(u, tile, vpage, vin);
+                if (lane == 0) s_bad[index % kBadSlots] = 0;
+                __syncwarp();
+                put(&kmap, u, vpage, vin);
+                for (; alive && tile < end; ++tile, --left) {
+                    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) {
+                        *(volatile int*)&s_bad[index % kBadSlots] = 1;
+                        if (p.a.row_status) atomicOr(p.a.row_status + u.b, SV_ROW_BAD_PAGE);
+                        __threadfence_block();
+                    }
+                    if (tile + 1 < end) {
+                        bad = find(u, tile + 1, page, in_page);
+                        put(&kmap, u, page, in_page);
+                        if (!alive) break;
+                    }
+                    put(&vmap, u, vpage, vin);
+                    vpage = page;
+                    vin = in_page;
+                }
+                ++index;
+                if (alive && left > 0) {
+                    next_unit<kTRows>(p, u);
+                    tile = u.t0;
+                }
+            }
+            // copies still in flight end before the CTA does (whoever gave up)
+            const unsigned long long t0 = now_ns();
+            const int n = min(issued, C::kStages);
+            for (int i = 0; i < n; ++i) {
+                stage = stage == 0 ? C::kStages - 1 : stage - 1;
+                if (stage == C::kStages - 1) turn ^= 1;
+                while (!bar_try(&s_full[stage], turn) && now_ns() - t0 < kWaitLimitNs) {}
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// the driver's encoder of tensor maps, fetched through the runtime (no link-time dependency)
+EncodeFn encoder() {
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (EncodeFn)f;
+    });
+    return fn;
+}
+
+// pages as [pages][heads][page_size][dim], boxes of `box` rows x 64 elements, swizzled
+bool encode(CUtensorMap* m, int dtype, const void* base, const AttendArgs& p, int64_t sp, int64_t sh, int64_t ss,
+            int box) {
+    EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.a.dim, (cuuint64_t)p.a.cache.page_size, (cuuint64_t)p.a.kv_heads,
+                                (cuuint64_t)p.a.cache.pages};
+    // a stride that no second element uses may be anything: give the encoder a plain one
+    if (p.a.kv_heads == 1) sh = ss;
+    if (p.a.cache.pages == 1) sp = ss;
+    const cuuint64_t strides[3] = {(cuuint64_t)ss * 2, (cuuint64_t)sh * 2, (cuuint64_t)sp * 2};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return fn(m, dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+              const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t launch_tiles(const AttendArgs& p, unsigned long long wait_ns, cudaStream_t s) {
+    constexpr int bytes = TilesCfg<D>::kSmem;
+    TilesArgs ta;
+    ta.p = p;
+    ta.wait_ns = wait_ns;
+    ta.box = 16;
+    while (ta.box < kKeyTile && p.a.cache.page_size % (2 * ta.box) == 0) ta.box *= 2;
+    CUtensorMap km, vm;
+    const sv_paged_cache& c = p.a.cache;
+    if (!encode(&km, (int)p.a.dtype, c.k_pages, p, c.k_stride_page, c.k_stride_head, c.k_stride_slot, ta.box) ||
+        !encode(&vm, (int)p.a.dtype, c.v_pages, p, c.v_stride_page, c.v_stride_head, c.v_stride_slot, ta.box))
+        return cudaErrorInvalidValue;
+    // once a device: room in shared memory, and proof that the register split fits the launch
+    static std::mutex mu;
+    static bool ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (dev < 0 || dev >= 64 || !ready[dev]) {
+            cudaFuncAttributes at;
+            if ((e = cudaFuncGetAttributes(&at, attend_tiles_kernel<T, D>)) != cudaSuccess) return e;
+            if (at.numRegs * kTThreads < 256 * kSoftRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
+            e = cudaFuncSetAttribute(attend_tiles_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (e != cudaSuccess) return e;
+            if (dev >= 0 && dev < 64) ready[dev] = true;
+        }
+    }
+    attend_tiles_kernel<T, D><<<p.ctas, kTThreads, bytes, s>>>(ta, km, vm);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tiles(int dtype, int dim, const AttendArgs& p, unsigned long long wait_ns, cudaStream_t s) {
+    if (dtype == SV_BF16)
+        return dim == 64 ? launch_tiles<__nv_bfloat16, 64>(p, wait_ns, s) : launch_tiles<__nv_bfloat16, 128>(p, wait_ns, s);
+    return dim == 64 ? launch_tiles<__half, 64>(p, wait_ns, s) : launch_tiles<__half, 128>(p, wait_ns, s);
+}
+
+}  // namespace sv

@@ -394,6 +394,19 @@ def test_attention_is_repeatable_on_other_streams_and_in_graphs(N):
     check_attention(s, past, new, got=out)
 
 
+def test_attention_gives_up_a_wait_and_recovers():
+    """A limit that no wait can keep: NaN and a status, and the next call is unaffected."""
+    N, past, new = 150, [3000, 200], [150, 150]
+    s = paged(2, N, 8, 2, 128, BF, 32, past, new, seed=6)
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    got = sv.paged_attention(s["q"], s["cache"], s["table"], s["lens"], s["new"], row_status=st, wait_limit_ns=1)
+    assert st.tolist() == [sv.ROW_INTERNAL] * 2
+    assert bool(got.isnan().any(-1).all(1).all(1).any())
+    st.zero_()
+    check_attention(s, past, new, row_status=st)
+    assert st.tolist() == [0, 0]
+
+
 # ---------------------------------------------------------------------------
 # rotary positions
 # ---------------------------------------------------------------------------
