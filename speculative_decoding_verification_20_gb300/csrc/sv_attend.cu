@@ -16,7 +16,9 @@ int row_tile(int64_t N, int64_t group) { return N * group <= 16 ? 16 : N * group
 int check_attention(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads, int64_t dim) {
     if (B < 0 || N < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads) return SV_EINVAL;
     if (dim != 64 && dim != 128) return SV_EUNSUPPORTED;
-    if (B > SV_MAX_BATCH || q_heads > 65536 || q_heads / kv_heads > SV_MAX_GROUP || N > (1 << 24)) return SV_ETOO_LARGE;
+    if (B > SV_MAX_BATCH || q_heads > 65536 || q_heads / kv_heads > SV_MAX_GROUP || N > kMaxRows ||
+        N * (q_heads / kv_heads) > kMaxRows)
+        return SV_ETOO_LARGE;
     return SV_OK;
 }
 
@@ -85,6 +87,11 @@ extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream
     memset(&p, 0, sizeof p);
     p.a = a;
     p.group = group;
+    p.group_inv = group > 1 ? (uint32_t)(((1ull << 32) + group - 1) / group) : 0u;
+    p.page_shift = -1;
+    for (int i = 4; i <= 16; ++i)
+        if (a.cache.page_size == (int64_t)1 << i) p.page_shift = i;
+    p.max_row_tiles = (int)((a.N * group + rm - 1) / rm);
     p.qscale = (float)(a.scale * kLog2e);
     p.capacity = a.cache.pages_per_seq * a.cache.page_size;
     if (p.capacity > 0x7FFFFF00) p.capacity = 0x7FFFFF00;  // positions are 32-bit

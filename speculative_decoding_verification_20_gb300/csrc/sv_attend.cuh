@@ -20,21 +20,28 @@ constexpr int kMaxCtas = 152;  // one CTA per SM; also sizes the workspace
 
 // a CTA's first unit and its place in the list
 struct Cut {
-    long long total;       // tiles in the list (0: the CTA has none)
-    long long base, end;   // the unit's tiles of the list
-    int b, h, rt, past, n;
+    long long base, end;  // the unit's tiles of the list
+    long long per;        // tiles a CTA; the first `more` CTAs have one tile more
+    int more, ctas;       // CTAs with work (0: this one has none)
+    int b, h, rt, n;
 };
 
 struct AttendArgs {
     sv_attention_args a;
-    int group;      // query heads per cache head
-    float qscale;   // scale * log2(e): scores are kept as powers of two
-    int ctas;       // CTAs that share the work (at most kMaxCtas)
-    int64_t capacity;   // positions that the page table addresses
-    struct Cut* cut;    // [ctas] each CTA's first unit, for the join
-    float* part_o;      // [2 * ctas][RM][dim]
-    float* part_ml;     // [2 * ctas][RM][2] running maximum (in log2 units) and sum
+    int group;           // query heads per cache head
+    uint32_t group_inv;  // 2^32 / group, rounded up (0: group is 1)
+    int page_shift;      // log2 of page_size, or -1
+    int max_row_tiles;   // row tiles of a sequence with all N new tokens
+    float qscale;        // scale * log2(e): scores are kept as powers of two
+    int ctas;            // CTAs that share the work (at most kMaxCtas)
+    int64_t capacity;    // positions that the page table addresses
+    Cut* cut;            // [ctas] each CTA's first unit, for the join
+    float* part_o;       // [2 * ctas][RM][dim]
+    float* part_ml;      // [2 * ctas][RM][2] running maximum (in log2 units) and sum
 };
+// r / group by a product: exact for r < 2^26 and groups up to 64, since the error of
+// group_inv, below group / 2^32 relative to it, then stays below 1 / group
+constexpr int64_t kMaxRows = 1 << 26;
 
 #ifdef __CUDACC__
 
@@ -45,56 +52,77 @@ struct Unit {
     int t0, t1;
 };
 
+__device__ __forceinline__ int by_group(const AttendArgs& p, int r) {
+    return p.group_inv ? (int)__umulhi((uint32_t)r, p.group_inv) : r;
+}
+__device__ __forceinline__ int page_of(const AttendArgs& p, int key) {
+    return p.page_shift >= 0 ? key >> p.page_shift : key / (int)p.a.cache.page_size;
+}
+// the visible keys [lo, hi] of a tile of rows
+template <int RM>
+__device__ __forceinline__ void tile_keys(const AttendArgs& p, int past, int n, int rt, int& lo, int& hi) {
+    const int r0 = rt * RM, r1 = min(r0 + RM, n * p.group) - 1;
+    lo = p.a.window > 0 ? (int)max((int64_t)0, past + by_group(p, r0) + 1 - p.a.window) : 0;
+    hi = past + by_group(p, r1);
+}
+template <int RM>
+__device__ __forceinline__ int tile_count(const AttendArgs& p, int past, int n, int rt) {
+    int lo, hi;
+    tile_keys<RM>(p, past, n, rt, lo, hi);
+    return hi / kKeyTile + 1 - lo / kKeyTile;
+}
 template <int RM>
 __device__ __forceinline__ void unit_tiles(const AttendArgs& p, Unit& u) {
-    const int rows = u.n * p.group;
-    const int r0 = u.rt * RM, r1 = min(r0 + RM, rows) - 1;
-    const int lo = p.a.window > 0 ? (int)max((int64_t)0, u.past + r0 / p.group + 1 - p.a.window) : 0;
-    const int hi = u.past + r1 / p.group;  // last visible key
+    int lo, hi;
+    tile_keys<RM>(p, u.past, u.n, u.rt, lo, hi);
     u.t0 = lo / kKeyTile;
     u.t1 = hi / kKeyTile + 1;
 }
-
-// key tiles of one head of sequence b
 template <int RM>
-__device__ __forceinline__ long long head_tiles(const AttendArgs& p, int past, int n) {
-    const int nrt = (n * p.group + RM - 1) / RM;
-    long long c = 0;
-    Unit u;
-    u.past = past;
-    u.n = n;
-    for (u.rt = 0; u.rt < nrt; ++u.rt) {
-        unit_tiles<RM>(p, u);
-        c += u.t1 - u.t0;
-    }
-    return c;
-}
-
-template <int RM>
-__device__ __forceinline__ long long seq_tiles(const AttendArgs& p, int b) {
-    const SeqLens s = seq_lens(p.a.cache, b, (int)p.a.N, p.capacity);
-    return head_tiles<RM>(p, s.past, s.n) * p.a.kv_heads;
+__device__ __forceinline__ int row_tiles(const AttendArgs& p, int n) {
+    return (n * p.group + RM - 1) / RM;
 }
 
 // The CTA's part of the list: its first unit, the tile in it to begin with, and how
 // many tiles to do in all.  Every thread of the CTA calls this and gets the same
-// answer, and the first unit is left for the join.
+// answer, and the first unit is left for the join.  s_tiles: NT words of shared memory.
 struct Part {
-    long long begin, total;  // the CTA's first tile of the list, tiles in the list
-    long long base;          // list index of the first unit's first tile
     int todo;
+    int tile;  // in u
     Unit u;
 };
 template <int RM, int NT>
-__device__ void find_part(const AttendArgs& p, Part& part) {
+__device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
     __shared__ long long s_warp[NT / 32];
     __shared__ long long s_before;
     __shared__ int s_seq;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = (int)p.a.B;
-    long long total = 0, mine = 0;
+    // key tiles of one head of sequence b0 + t: by a thread alone, or where a sequence has
+    // many row tiles by a warp
+    auto head_tiles = [&](int b0) -> int {
+        if (p.max_row_tiles <= 4) {
+            if (b0 + t >= B) return 0;
+            const SeqLens s = seq_lens(p.a.cache, b0 + t, (int)p.a.N, p.capacity);
+            int c = 0;
+            for (int rt = row_tiles<RM>(p, s.n); rt-- > 0;) c += tile_count<RM>(p, s.past, s.n, rt);
+            return c;
+        }
+        __syncthreads();
+        for (int i = warp; i < NT && b0 + i < B; i += NT / 32) {
+            const SeqLens s = seq_lens(p.a.cache, b0 + i, (int)p.a.N, p.capacity);
+            int c = 0;
+            for (int rt = lane; rt < row_tiles<RM>(p, s.n); rt += 32) c += tile_count<RM>(p, s.past, s.n, rt);
+            c = warp_sum(c);
+            if (lane == 0) s_tiles[i] = c;
+        }
+        __syncthreads();
+        return b0 + t < B ? s_tiles[t] : 0;
+    };
+    long long total = 0;
+    int mine = 0;
     for (int b0 = 0; b0 < B; b0 += NT) {
-        mine = b0 + t < B ? seq_tiles<RM>(p, b0 + t) : 0;
-        total += mine;
+        mine = head_tiles(b0);
+        total += (long long)mine * p.a.kv_heads;
     }
     total = warp_sum(total);
     if (lane == 0) s_warp[warp] = total;
@@ -103,20 +131,21 @@ __device__ void find_part(const AttendArgs& p, Part& part) {
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) total += s_warp[w];
     __syncthreads();
-    part.total = total;
-    const long long ctas = min((long long)p.ctas, total);
-    const int c = blockIdx.x;
+    const int c = blockIdx.x, ctas = total < p.ctas ? (int)total : p.ctas;
     part.todo = 0;
     if (c >= ctas) {
-        if (t == 0) p.cut[c].total = 0;
+        if (t == 0) p.cut[c].ctas = 0;
         return;
     }
-    part.begin = total * c / ctas;
-    part.todo = (int)(total * (c + 1) / ctas - part.begin);
+    const long long per = total >> 31 ? total / ctas : (long long)((uint32_t)total / (uint32_t)ctas);
+    const int more = (int)(total - per * ctas);
+    const long long begin = per * c + min(c, more);
+    part.todo = (int)per + (c < more ? 1 : 0);
     long long base = 0;
     for (int b0 = 0; b0 < B; b0 += NT) {
-        if (B > NT) mine = b0 + t < B ? seq_tiles<RM>(p, b0 + t) : 0;
-        long long x = mine;
+        if (B > NT) mine = head_tiles(b0);
+        const long long own = (long long)mine * p.a.kv_heads;
+        long long x = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
@@ -124,15 +153,16 @@ __device__ void find_part(const AttendArgs& p, Part& part) {
         }
         if (lane == 31) s_warp[warp] = x;
         __syncthreads();
-        long long before = base + x - mine;
+        long long before = base + x - own;
         for (int w = 0; w < warp; ++w) before += s_warp[w];
-        if (part.begin >= before && part.begin < before + mine) {
+        if (begin >= before && begin < before + own) {
             s_seq = b0 + t;
             s_before = before;
+            s_tiles[0] = mine;
         }
         for (int w = 0; w < NT / 32; ++w) base += s_warp[w];
         __syncthreads();
-        if (base > part.begin) break;
+        if (base > begin) break;
     }
     // then the head and the row tile
     Unit& u = part.u;
@@ -140,25 +170,37 @@ __device__ void find_part(const AttendArgs& p, Part& part) {
     const SeqLens s = seq_lens(p.a.cache, u.b, (int)p.a.N, p.capacity);
     u.past = s.past;
     u.n = s.n;
-    const long long per_head = head_tiles<RM>(p, s.past, s.n);
-    long long at = part.begin - s_before;
-    u.h = (int)(at / per_head);
-    at -= u.h * per_head;
-    part.base = s_before + u.h * per_head;
-    for (u.rt = 0;; ++u.rt) {
-        unit_tiles<RM>(p, u);
-        if (at < u.t1 - u.t0) break;
-        at -= u.t1 - u.t0;
-        part.base += u.t1 - u.t0;
+    const int per_head = s_tiles[0];
+    const long long off = begin - s_before;
+    u.h = off >> 31 ? (int)(off / per_head) : (int)((uint32_t)off / (uint32_t)per_head);
+    int at = (int)(off - (long long)u.h * per_head);
+    for (int rt0 = 0;; rt0 += 32) {  // (at < per_head: a row tile holds it)
+        const int n = rt0 + lane < row_tiles<RM>(p, s.n) ? tile_count<RM>(p, s.past, s.n, rt0 + lane) : 0;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        const unsigned past_it = __ballot_sync(0xFFFFFFFFu, x > at);
+        if (past_it) {
+            const int l = __ffs(past_it) - 1;
+            u.rt = rt0 + l;
+            at -= __shfl_sync(0xFFFFFFFFu, x - n, l);
+            break;
+        }
+        at -= __shfl_sync(0xFFFFFFFFu, x, 31);
+        if (rt0 + 32 >= row_tiles<RM>(p, s.n)) break;
     }
-    if (t == 0) p.cut[c] = Cut{total, part.base, part.base + (u.t1 - u.t0), u.b, u.h, u.rt, u.past, u.n};
+    unit_tiles<RM>(p, u);
+    part.tile = u.t0 + at;
+    if (t == 0) p.cut[c] = Cut{begin - at, begin - at + (u.t1 - u.t0), per, more, ctas, u.b, u.h, u.rt, u.n};
 }
 
 // the unit after u (there is one: the caller counts tiles)
 template <int RM>
 __device__ __forceinline__ void next_unit(const AttendArgs& p, Unit& u) {
-    const int nrt = (u.n * p.group + RM - 1) / RM;
-    if (++u.rt == nrt) {
+    if (++u.rt == row_tiles<RM>(p, u.n)) {
         u.rt = 0;
         if (++u.h == p.a.kv_heads) {
             u.h = 0;
@@ -193,14 +235,16 @@ __device__ void fill_idle_rows(const AttendArgs& p) {
 }
 
 template <typename T>
-__device__ __forceinline__ T* out_row(const AttendArgs& p, const Unit& u, int r) {
-    return (T*)p.a.out + (int64_t)u.b * p.a.o_stride_b + (int64_t)(r / p.group) * p.a.o_stride_n +
-           (int64_t)(u.h * p.group + r % p.group) * p.a.o_stride_h;
+__device__ __forceinline__ T* out_row(const AttendArgs& p, int b, int h, int r) {
+    const int i = by_group(p, r);
+    return (T*)p.a.out + (int64_t)b * p.a.o_stride_b + (int64_t)i * p.a.o_stride_n +
+           (int64_t)(h * p.group + r - i * p.group) * p.a.o_stride_h;
 }
 template <typename T>
-__device__ __forceinline__ const T* q_row(const AttendArgs& p, const Unit& u, int r) {
-    return (const T*)p.a.q + (int64_t)u.b * p.a.q_stride_b + (int64_t)(r / p.group) * p.a.q_stride_n +
-           (int64_t)(u.h * p.group + r % p.group) * p.a.q_stride_h;
+__device__ __forceinline__ const T* q_row(const AttendArgs& p, int b, int h, int r) {
+    const int i = by_group(p, r);
+    return (const T*)p.a.q + (int64_t)b * p.a.q_stride_b + (int64_t)i * p.a.q_stride_n +
+           (int64_t)(h * p.group + r - i * p.group) * p.a.q_stride_h;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {  // 2^x; 2^-inf = 0

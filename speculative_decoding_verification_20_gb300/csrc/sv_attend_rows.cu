@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kAThreads, 1) attend_rows_kernel(const __grid_
     grid_dependents_go();
     fill_idle_rows<T, kAThreads>(p);
     Part part;
-    find_part<RM, kAThreads>(p, part);
+    find_part<RM, kAThreads>(p, part, reinterpret_cast<int*>(s_join));
     if (part.todo == 0) return;
 
     unsigned char* ring = smem + warp * (C::kStages * C::kStageBytes);
@@ -99,23 +99,23 @@ __global__ void __launch_bounds__(kAThreads, 1) attend_rows_kernel(const __grid_
     // the filling side: unit, tile in it, tiles left.  One block is in reach of a unit's
     // rows if it holds a key that a row of the tile sees.
     Unit fu = part.u;
-    int ft = part.u.t0 + (int)(part.begin - part.base), fleft = part.todo;
+    int ft = part.tile, fleft = part.todo;
     uint32_t bad_pages = 0;  // bit s: the block in stage s lies on a bad page
     auto fill = [&](int stage) {
         if (fleft > 0) {
             const int kb = ft * kAWarps + warp;  // block index
             const int k0 = kb * kBlk;
-            const int r0 = fu.rt * RM, r1 = min(r0 + RM, fu.n * p.group) - 1;
-            const int hi = fu.past + r1 / p.group;
-            const int lo = p.a.window > 0 ? (int)max((int64_t)0, fu.past + r0 / p.group + 1 - p.a.window) : 0;
+            int lo, hi;
+            tile_keys<RM>(p, fu.past, fu.n, fu.rt, lo, hi);
             bad_pages &= ~(1u << stage);
             if (k0 <= hi && k0 + kBlk > lo) {
-                const int page = p.a.cache.page_table[fu.b * p.a.cache.page_table_stride + k0 / page_size];
+                const int index = page_of(p, k0);
+                const int page = p.a.cache.page_table[fu.b * p.a.cache.page_table_stride + index];
                 if (page < 0 || page >= p.a.cache.pages) {
                     bad_pages |= 1u << stage;
                     if (lane == 0 && p.a.row_status) atomicOr(p.a.row_status + fu.b, SV_ROW_BAD_PAGE);
                 } else {
-                    const int64_t in_page = k0 % page_size;
+                    const int64_t in_page = k0 - index * page_size;
                     const T* k = (const T*)p.a.cache.k_pages + page * p.a.cache.k_stride_page +
                                  fu.h * p.a.cache.k_stride_head + in_page * p.a.cache.k_stride_slot;
                     const T* v = (const T*)p.a.cache.v_pages + page * p.a.cache.v_stride_page +
@@ -141,15 +141,14 @@ __global__ void __launch_bounds__(kAThreads, 1) attend_rows_kernel(const __grid_
     for (int s = 0; s < C::kStages - 1; ++s) fill(s);
 
     Unit u = part.u;
-    int tile = part.u.t0 + (int)(part.begin - part.base);
+    int tile = part.tile;
     int left = part.todo, stage = 0;
-    long long ubase = part.base;  // list index of u's first tile
     bool first_unit = true;
     while (left > 0) {
         const int rows = min(RM, u.n * p.group - u.rt * RM), r00 = u.rt * RM;
-        const int i_first = r00 / p.group, i_last = (r00 + rows - 1) / p.group;
-        const int hi = u.past + i_last;
-        const int lo = p.a.window > 0 ? (int)max((int64_t)0, u.past + i_first + 1 - p.a.window) : 0;
+        const int i_first = by_group(p, r00);
+        int lo, hi;
+        tile_keys<RM>(p, u.past, u.n, u.rt, lo, hi);
         const int end = min(u.t1, tile + left);
         const bool from_start = tile == u.t0, to_end = end == u.t1;
 
@@ -161,8 +160,8 @@ __global__ void __launch_bounds__(kAThreads, 1) attend_rows_kernel(const __grid_
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = m * 16 + g + e * 8;
-                qpos[m][e] = r < rows ? u.past + (r00 + r) / p.group : -1;
-                const T* q = q_row<T>(p, u, r00 + min(r, rows - 1));
+                qpos[m][e] = r < rows ? u.past + by_group(p, r00 + r) : -1;
+                const T* q = q_row<T>(p, u.b, u.h, r00 + min(r, rows - 1));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(kAThreads, 1) attend_rows_kernel(const __grid_
                         const float inv = 1.0f / l;
                         uint2 pk = make_uint2(Pair<T>::pack(acc.x * inv, acc.y * inv),
                                               Pair<T>::pack(acc.z * inv, acc.w * inv));
-                        *reinterpret_cast<uint2*>(out_row<T>(p, u, r00 + rr) + half * C::kJoinCols + c) = pk;
+                        *reinterpret_cast<uint2*>(out_row<T>(p, u.b, u.h, r00 + rr) + half * C::kJoinCols + c) = pk;
                     } else {
                         *reinterpret_cast<float4*>(p.part_o + ((int64_t)place * RM + rr) * D + half * C::kJoinCols +
                                                    c) = acc;
@@ -360,7 +359,6 @@ __global__ void __launch_bounds__(kAThreads, 1) attend_rows_kernel(const __grid_
         }
         first_unit = false;
         if (left > 0) {
-            ubase += u.t1 - u.t0;
             next_unit<RM>(p, u);
             tile = u.t0;
         }
@@ -378,13 +376,10 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const Cut k = p.cut[blockIdx.x];
-    if (k.total == 0) return;
-    // CTA c has the tiles [total * c / ctas, total * (c + 1) / ctas)
-    const long long ctas = min((long long)p.ctas, k.total), c0 = blockIdx.x;
-    if (k.total * c0 / ctas == k.base || c0 == 0 || k.total * (c0 - 1) / ctas > k.base) return;
-    Unit u;
-    u.b = k.b;
-    u.h = k.h;
+    const long long ctas = k.ctas, c0 = blockIdx.x;
+    if (ctas == 0) return;
+    auto begin = [&](long long c) { return k.per * c + min(c, (long long)k.more); };  // a CTA's first tile
+    if (begin(c0) == k.base || c0 == 0 || begin(c0 - 1) > k.base) return;
     const int rows = min(RM, k.n * p.group - k.rt * RM);
     for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
          r += gridDim.y * (kJoinThreads / 32)) {
@@ -393,7 +388,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
         for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
 #pragma unroll 4
         for (long long c = c0 - 1; c < ctas; ++c) {
-            const long long from = k.total * c / ctas;
+            const long long from = begin(c);
             if (from >= k.end) break;
             const int64_t place = 2 * c + (from >= k.base ? 0 : 1);
             const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
@@ -421,7 +416,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
         uint32_t w[PER / 2];
 #pragma unroll
         for (int i = 0; i < PER / 2; ++i) w[i] = Pair<T>::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-        T* dst = out_row<T>(p, u, k.rt * RM + r) + lane * PER;
+        T* dst = out_row<T>(p, k.b, k.h, k.rt * RM + r) + lane * PER;
         if constexpr (PER == 4)
             *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
         else

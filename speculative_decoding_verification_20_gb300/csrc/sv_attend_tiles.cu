@@ -99,42 +99,70 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, unsigned 
         *dead = 1;
         return false;
     }
-    if (bar_try(b, parity)) return true;
-    const unsigned long long t0 = now_ns();
-    while (!bar_try(b, parity)) {
+    // (the device timer is slow to read: only after many tries)
+    unsigned long long t0 = 0;
+    for (uint32_t i = 0; !bar_try(b, parity); ++i) {
         if (*dead) return false;
-        if (now_ns() - t0 >= limit) {
-            *dead = 1;
-            return false;
+        if ((i & 255u) == 255u) {
+            const unsigned long long t = now_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 >= limit) {
+                *dead = 1;
+                return false;
+            }
         }
     }
     return true;
 }
 
 // ---- tensor memory and products -------------------------------------------
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
-    // rows of 128 bytes, swizzled in groups of 8 rows (1024 bytes)
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// Descriptors of swizzled operands in shared memory, groups of 8 rows (1024 bytes) apart:
+// the low word has the address (in 16 bytes) and, for values, which are read across
+// (64 contiguous elements of N, then the next block of 64), the distance of the blocks.
+// The high word is the same for all.
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_keys(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_values(uint32_t addr, uint32_t block_bytes) {
+    return (addr >> 4) | ((block_bytes >> 4) << 16);
 }
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t half_bytes) {
-    // the same memory read across: 64 contiguous elements of N, blocks of them half_bytes
-    // apart; groups of 8 keys 1024 bytes apart
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(half_bytes >> 4) << 16) | (64ull << 32) | (1ull << 46) |
-           (2ull << 61);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n.reg .pred p;\n.reg .b64 da, db;\nsetp.ne.u32 p, %5, 0;\nmov.b64 da, {%1, %4};\nmov.b64 db, {%2, %4};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"((uint32_t)add)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n.reg .pred p;\n.reg .b64 db;\nsetp.ne.u32 p, %5, 0;\nmov.b64 db, {%2, %4};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"((uint32_t)add)
         : "memory");
+}
+// one lane of the warp, the same each time; the products are issued from code that the
+// compiler can see to be uniform (descriptors in uniform registers)
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+// two 32-bit operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 d, a, b;\n"
+        "mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ void mma_commit(uint64_t* b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b))
@@ -184,6 +212,13 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
         SV_I8(r, 0), SV_I8(r, 8), SV_I8(r, 16), SV_I8(r, 24)
         : "memory");
 }
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            addr),
+        SV_I8(r, 0), SV_I8(r, 8)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -195,15 +230,8 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         : "memory");
 }
 
-// the visible keys of a unit's rows
-__device__ __forceinline__ void unit_keys(const AttendArgs& p, const Unit& u, int& lo, int& hi) {
-    const int r0 = u.rt * kTRows, r1 = min(r0 + kTRows, u.n * p.group) - 1;
-    hi = u.past + r1 / p.group;
-    lo = p.a.window > 0 ? (int)max((int64_t)0, u.past + r0 / p.group + 1 - p.a.window) : 0;
-}
-
-// How many bits of the tensor cores' kind::f16 instruction: fp32 results, T operands,
-// B across (values) or along (keys) its rows
+// the instruction descriptor: fp32 results, T operands, n columns, B read across its rows
+// (values) or along them (keys), 128 rows
 template <typename T>
 __device__ constexpr uint32_t idesc(int n, bool b_across) {
     const uint32_t f = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
@@ -218,7 +246,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const AttendArgs& p = ta.p;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];     // ring of key and value tiles
-    __shared__ uint64_t s_q[2], s_scores[2], s_weights[2], s_out[2];  // per row tile
+    __shared__ uint64_t s_q[2], s_scores[2], s_weights[2][2], s_out[2];  // per row tile (weights: halves)
     __shared__ uint64_t s_last;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
@@ -231,7 +259,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const uint32_t q_s = smem, ring_s = smem + C::kQBytes;
     fill_idle_rows<T, kTThreads>(p);
     Part part;
-    find_part<kTRows, kTThreads>(p, part);
+    find_part<kTRows, kTThreads>(p, part, reinterpret_cast<int*>(smem_p));
     if (part.todo == 0) return;
 
     if (t == 0) {
@@ -242,7 +270,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         for (int x = 0; x < 2; ++x) {
             bar_init(&s_q[x], 128);
             bar_init(&s_scores[x], 1);
-            bar_init(&s_weights[x], 128);
+            bar_init(&s_weights[x][0], 128);
+            bar_init(&s_weights[x][1], 128);
             bar_init(&s_out[x], 1);
         }
         bar_init(&s_last, 1);
@@ -262,7 +291,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
     const unsigned long long limit = ta.wait_ns;
-    const int tile0 = part.u.t0 + (int)(part.begin - part.base);
+    const int tile0 = part.tile;
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
@@ -281,7 +310,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const int r = w.rt * kTRows + x * 128 + row, rows = w.n * p.group;
             if (w.rt * kTRows + x * 128 >= rows) return;
             unsigned char* dst = smem_p + x * 128 * D * 2 + row * 128;
-            const T* src = q_row<T>(p, w, min(r, rows - 1));
+            const T* src = q_row<T>(p, w.b, w.h, min(r, rows - 1));
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
                 uint4 v = make_uint4(0, 0, 0, 0);
@@ -301,11 +330,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
             Unit next = u;
             if (left > 0) next_unit<kTRows>(p, next);
             if (mine) {
-                const int pos = u.past + min(r, rows - 1) / p.group;
+                const int pos = u.past + by_group(p, min(r, rows - 1));
                 // of the warp's rows: the least and the greatest position
                 const int wr0 = u.rt * kTRows + x * 128 + (row & ~31);
-                const int pos0 = u.past + min(wr0, rows - 1) / p.group;
-                const int pos1 = u.past + min(wr0 + 31, rows - 1) / p.group;
+                const int pos0 = u.past + by_group(p, min(wr0, rows - 1));
+                const int pos1 = u.past + by_group(p, min(wr0 + 31, rows - 1));
                 float ref = -INFINITY, sum = 0.0f;
                 for (; alive && tile < end; ++tile) {
                     alive = bar_wait(&s_scores[x], n_scores & 1, limit, dead);
@@ -325,9 +354,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     }
                     float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int j = 4; j < kKeyTile; j += 4)
+                    for (int j = 4; j < kKeyTile - 4; j += 8)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[j + e]);
+                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], s[j + 2 * e]), s[j + 2 * e + 1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[kKeyTile - 4 + e]);
                     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.qscale;
                     if (tile == first) {
                         ref = m;
@@ -352,24 +383,28 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     }
                     if (tile != first) ++n_out;
                     const float base = ref == -INFINITY ? 0.0f : ref;  // nothing visible yet: weights 0
-                    float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float2 qs = make_float2(p.qscale, p.qscale), mb = make_float2(-base, -base);
+                    float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t w[32];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float a = fast_exp2(fmaf(s[half * 64 + 2 * j], p.qscale, -base));
-                            const float b = fast_exp2(fmaf(s[half * 64 + 2 * j + 1], p.qscale, -base));
-                            add[(2 * j) & 3] += a;
-                            add[(2 * j + 1) & 3] += b;
-                            w[j] = Pair<T>::pack(a, b);  // 16 bits into the product, as the values
+                        for (int j = 0; j < 16; ++j) {
+                            float2 e = fma2(make_float2(s[c * 32 + 2 * j], s[c * 32 + 2 * j + 1]), qs, mb);
+                            e.x = fast_exp2(e.x);
+                            e.y = fast_exp2(e.y);
+                            add[j & 1] = add2(add[j & 1], e);
+                            w[j] = Pair<T>::pack(e.x, e.y);  // 16 bits into the product, as the values
                         }
-                        tmem_store32(tS + half * 32, w);
+                        tmem_store16(tS + c * 16, w);
+                        if (c & 1) {  // half of the keys: their product can start
+                            tmem_store_wait();
+                            fence_before();
+                            bar_arrive(&s_weights[x][c >> 1]);
+                        }
                     }
-                    sum += (add[0] + add[1]) + (add[2] + add[3]);
-                    tmem_store_wait();
-                    fence_before();
-                    bar_arrive(&s_weights[x]);
+                    add[0] = add2(add[0], add[1]);
+                    sum += add[0].x + add[0].y;
                 }
                 // all scores of the unit are through: its queries make room for the next
                 if (alive && left > 0) load_q(next);
@@ -384,7 +419,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 const int64_t part_row = (int64_t)place * kTRows + x * 128 + row;
                 const float l = bad ? NAN : sum;
                 const float inv = 1.0f / l;
-                T* dst = r < rows ? out_row<T>(p, u, r) : nullptr;
+                T* dst = r < rows ? out_row<T>(p, u.b, u.h, r) : nullptr;
                 if (!whole && r < rows)
                     *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(alive ? ref : -INFINITY, l);
                 for (int c = 0; c < D; c += 32) {
@@ -437,13 +472,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     turn ^= 1;
                 }
             };
+            const uint32_t tm = uniform(tmem), q_desc = uniform(desc_keys(q_s));
             auto scores = [&](int x, uint32_t ks) {
-                if (lane == 0) {
-                    const uint32_t qs = q_s + x * 128 * D * 2;
+                const uint32_t a = q_desc + x * (128 * D * 2 >> 4), b = uniform(desc_keys(ks));
+                if (elect()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = (k / 4) * C::kHalfBytes + (k % 4) * 32;
-                        mma_ss(tmem + C::kS + x * 128, desc_k_major(qs + at), desc_k_major(ks + at), i_s, k > 0);
+                        const uint32_t at = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
+                        mma_ss(tm + C::kS + x * 128, a + at, b + at, i_s, k > 0);
                     }
                     mma_commit(&s_scores[x]);
                 }
@@ -454,7 +490,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 const int tiles_x = rows > 128 ? 2 : 1;
                 const int first = tile, end = min(u.t1, tile + left);
                 int lo, hi;
-                unit_keys(p, u, lo, hi);
+                tile_keys<kTRows>(p, u.past, u.n, u.rt, lo, hi);
                 const int vend = u.past + u.n;
                 for (int x = 0; alive && x < tiles_x; ++x) alive = bar_wait(&s_q[x], n_q[x]++ & 1, limit, dead);
                 alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
@@ -462,7 +498,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 if (!alive) break;
                 fence_after();
                 for (int x = 0; x < tiles_x; ++x) scores(x, ring_s + stage * C::kTileBytes);
-                if (lane == 0) mma_commit(&s_empty[stage]);
+                if (elect()) mma_commit(&s_empty[stage]);
+                __syncwarp();
                 next_stage();
                 for (; tile < end; ++tile, --left) {
                     const bool more = tile + 1 < end;
@@ -492,23 +529,29 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         fence_async_smem();
                         __syncwarp();
                     }
+                    const uint32_t v_desc = uniform(desc_values(vs, C::kHalfBytes));
                     for (int x = 0; alive && x < tiles_x; ++x) {
-                        alive = bar_wait(&s_weights[x], n_w[x]++ & 1, limit, dead);
-                        alive = __all_sync(0xFFFFFFFFu, alive);
-                        if (!alive) break;
-                        fence_after();
-                        if (lane == 0) {
 #pragma unroll
-                            for (int k = 0; k < kKeyTile / 16; ++k)
-                                mma_ts(tmem + C::kO + x * D, tmem + C::kS + x * 128 + k * 8,
-                                       desc_mn_major(vs + k * 16 * 128, C::kHalfBytes), i_o, tile > first || k > 0);
-                            mma_commit(&s_out[x]);
+                        for (int half = 0; half < 2; ++half) {
+                            alive = alive && bar_wait(&s_weights[x][half], n_w[x] & 1, limit, dead);
+                            alive = __all_sync(0xFFFFFFFFu, alive);
+                            if (!alive) break;
+                            fence_after();
+                            if (elect()) {
+#pragma unroll
+                                for (int k = half * 4; k < half * 4 + 4; ++k)
+                                    mma_ts(tm + C::kO + x * D, tm + C::kS + x * 128 + k * 8,
+                                           v_desc + k * (16 * 128 >> 4), i_o, tile > first || k > 0);
+                                if (half) mma_commit(&s_out[x]);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
+                        if (!alive) break;
+                        ++n_w[x];
                         if (more) scores(x, ks);
                     }
                     if (!alive) break;
-                    if (lane == 0) {
+                    if (elect()) {
                         if (more) mma_commit(&s_empty[kstage]);
                         mma_commit(&s_empty[vstage]);
                     }
@@ -520,7 +563,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 }
             }
             // products still in flight end before tensor memory is given back
-            if (lane == 0) mma_commit(&s_last);
+            if (elect()) mma_commit(&s_last);
             __syncwarp();
             const unsigned long long t0 = now_ns();
             while (!bar_try(&s_last, 0) && now_ns() - t0 < kWaitLimitNs) {}
@@ -553,13 +596,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
             // the lane's box of a tile: page id (bad and invisible ones: no_page)
             auto find = [&](const Unit& w, int tl, int& page, int& in_page) -> bool {
                 int lo, hi;
-                unit_keys(p, w, lo, hi);
+                tile_keys<kTRows>(p, w.past, w.n, w.rt, lo, hi);
                 const int k = tl * kKeyTile + box * ta.box;
                 page = no_page;
                 in_page = 0;
                 if (!loads || k > hi || k + ta.box <= lo) return false;
-                page = p.a.cache.page_table[w.b * p.a.cache.page_table_stride + k / page_size];
-                in_page = k % page_size;
+                const int at = page_of(p, k);
+                page = p.a.cache.page_table[w.b * p.a.cache.page_table_stride + at];
+                in_page = k - at * page_size;
                 if (page < 0 || page >= no_page) {
                     page = no_page;
                     return true;
