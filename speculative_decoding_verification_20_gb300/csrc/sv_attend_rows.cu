@@ -366,62 +366,103 @@ __global__ void __launch_bounds__(kAThreads, 1) attend_rows_kernel(const __grid_
     cp_wait<0>();
 }
 
-// One warp a row of a unit that was cut: the partial results of the CTAs that worked on
-// it, in order.  Block c looks at the unit in which CTA c began; the first CTA that began
-// inside a unit joins it.
+// A unit that was cut: the partial results of the CTAs that worked on it, in order.  Block
+// c looks at the unit in which CTA c began; the first CTA that began inside a unit joins it.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinCols = 16;
+__device__ __forceinline__ bool join_unit(const AttendArgs& p, Cut& k) {
+    grid_dependency_wait();
+    k = p.cut[blockIdx.x];
+    const long long c = blockIdx.x;
+    if (k.ctas == 0 || c == 0) return false;
+    return k.per * c + min(c, (long long)k.more) != k.base && k.per * (c - 1) + min(c - 1, (long long)k.more) <= k.base;
+}
+// calls f(place) for the unit's partial results in order
+template <typename F>
+__device__ __forceinline__ void join_each(const Cut& k, F f) {
+#pragma unroll 4
+    for (int c = blockIdx.x - 1; c < k.ctas; ++c) {
+        const long long from = k.per * c + min(c, k.more);  // a CTA's first tile
+        if (from >= k.end) break;
+        f((int64_t)(2 * c + (from >= k.base ? 0 : 1)));
+    }
+}
+// adds (m, l, x) to the running (top, sum, acc)
+template <int N>
+__device__ __forceinline__ void join_add(float& top, float& sum, float (&acc)[N], float m, float l, const float (&x)[N]) {
+    if (m == -INFINITY) {
+        sum += l;  // 0, or the NaN of a bad page or a wait that ran out
+        return;
+    }
+    const float now = fmaxf(top, m);
+    const float fa = fast_exp2(top - now), fb = fast_exp2(m - now);
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = acc[i] * fa + x[i] * fb;
+    sum = sum * fa + l * fb;
+    top = now;
+}
+
+// results by rows: a warp a row
 template <typename T, int D, int RM>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ AttendArgs p) {
     constexpr int PER = D / 32;  // columns a lane
-    grid_dependency_wait();
+    Cut k;
+    if (!join_unit(p, k)) return;
     const int lane = threadIdx.x & 31;
-    const Cut k = p.cut[blockIdx.x];
-    const long long ctas = k.ctas, c0 = blockIdx.x;
-    if (ctas == 0) return;
-    auto begin = [&](long long c) { return k.per * c + min(c, (long long)k.more); };  // a CTA's first tile
-    if (begin(c0) == k.base || c0 == 0 || begin(c0 - 1) > k.base) return;
-    const int rows = min(RM, k.n * p.group - k.rt * RM);
-    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += gridDim.y * (kJoinThreads / 32)) {
-        float top = -INFINITY, l = 0.0f, acc[PER];
+    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    if (r >= k.n * p.group - k.rt * RM) return;
+    float top = -INFINITY, l = 0.0f, acc[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-        for (long long c = c0 - 1; c < ctas; ++c) {
-            const long long from = begin(c);
-            if (from >= k.end) break;
-            const int64_t place = 2 * c + (from >= k.base ? 0 : 1);
-            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
-            float x[PER];
-            const float* src = p.part_o + (place * RM + r) * D + lane * PER;
-            if constexpr (PER == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(src);
-                x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-            } else {
-                const float2 y = *reinterpret_cast<const float2*>(src);
-                x[0] = y.x, x[1] = y.y;
-            }
-            if (ml.x == -INFINITY) {
-                l += ml.y;  // 0, or the NaN of a bad page or a wait that ran out
-                continue;
-            }
-            const float now = fmaxf(top, ml.x);
-            const float fa = fast_exp2(top - now), fb = fast_exp2(ml.x - now);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) acc[i] = acc[i] * fa + x[i] * fb;
-            l = l * fa + ml.y * fb;
-            top = now;
+    for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
+    join_each(k, [&](int64_t place) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
+        const float* src = p.part_o + (place * RM + r) * D + lane * PER;
+        float x[PER];
+        if constexpr (PER == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(src);
+            x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+        } else {
+            const float2 y = *reinterpret_cast<const float2*>(src);
+            x[0] = y.x, x[1] = y.y;
         }
-        const float inv = 1.0f / l;
-        uint32_t w[PER / 2];
+        join_add(top, l, acc, ml.x, ml.y, x);
+    });
+    const float inv = 1.0f / l;
+    uint32_t w[PER / 2];
 #pragma unroll
-        for (int i = 0; i < PER / 2; ++i) w[i] = Pair<T>::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-        T* dst = out_row<T>(p, k.b, k.h, k.rt * RM + r) + lane * PER;
-        if constexpr (PER == 4)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        else
-            *reinterpret_cast<uint32_t*>(dst) = w[0];
-    }
+    for (int i = 0; i < PER / 2; ++i) w[i] = Pair<T>::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    T* dst = out_row<T>(p, k.b, k.h, k.rt * RM + r) + lane * PER;
+    if constexpr (PER == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t*>(dst) = w[0];
+}
+
+// results by columns: a thread has kJoinCols columns of a row, a warp 32 rows
+template <typename T, int D, int RM>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_columns_kernel(const __grid_constant__ AttendArgs p) {
+    static_assert(RM == kJoinThreads, "a thread a row");
+    Cut k;
+    if (!join_unit(p, k)) return;
+    const int r = threadIdx.x, c0 = blockIdx.y * kJoinCols;
+    if (r >= k.n * p.group - k.rt * RM) return;
+    float top = -INFINITY, l = 0.0f, acc[kJoinCols];
+#pragma unroll
+    for (int i = 0; i < kJoinCols; ++i) acc[i] = 0.0f;
+    join_each(k, [&](int64_t place) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
+        float x[kJoinCols];
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) x[i] = p.part_o[(place * D + c0 + i) * RM + r];
+        join_add(top, l, acc, ml.x, ml.y, x);
+    });
+    const float inv = 1.0f / l;
+    uint32_t w[kJoinCols / 2];
+#pragma unroll
+    for (int i = 0; i < kJoinCols / 2; ++i) w[i] = Pair<T>::pack(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    uint4* dst = reinterpret_cast<uint4*>(out_row<T>(p, k.b, k.h, k.rt * RM + r) + c0);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 template <typename T, int D, int MT>
@@ -440,12 +481,17 @@ cudaError_t launch_join(const AttendArgs& p, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)p.ctas, RM < 64 ? RM / (kJoinThreads / 32) : 8);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, RM>, p);
+    if constexpr (RM == kJoinThreads) {
+        cfg.gridDim = dim3((unsigned)p.ctas, D / kJoinCols);
+        return cudaLaunchKernelEx(&cfg, attend_join_columns_kernel<T, D, RM>, p);
+    } else {
+        cfg.gridDim = dim3((unsigned)p.ctas, RM / (kJoinThreads / 32));
+        return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, RM>, p);
+    }
 }
 
 }  // namespace

@@ -6,8 +6,8 @@
 // keys.  Twelve warps, one job each:
 //   warps 0-3, 4-7  the softmax of one row tile each, a thread a row: scores from tensor
 //                   memory, weights back to it (in place of the scores), output rows at the end
-//   warp 8          issues the products: S = Q K^T from shared memory, O += P V with P from
-//                   tensor memory
+//   warps 8, 10     issue the products of one row tile each: S = Q K^T from shared memory,
+//                   O += P V with P from tensor memory
 //   warp 9          loads keys and values by TMA, page by page, into a ring
 // While one tile's softmax runs, the products of the other fill the tensor cores:
 // PV and the next S of tile A, then those of tile B.  The output stays in tensor memory
@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kTThreads = 384;
 // registers a thread: softmax warps, the others; their sum has to fit the launch's share
-constexpr int kSoftRegs = 208, kOtherRegs = 72;
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
 constexpr int kTRows = 256;
 constexpr int kBadSlots = 16;  // units that the loader can be ahead by, and more
 
@@ -92,27 +92,26 @@ __device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
     return ok;
 }
 // False once the wait has run out, here or (dead) in another warp of the CTA.  A limit
-// below the device timer's tick means one look.
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, unsigned long long limit, volatile int* dead) {
-    if (limit < 1000) {
-        if (bar_test(b, parity)) return true;
-        *dead = 1;
-        return false;
-    }
-    // (the device timer is slow to read: only after many tries)
+// below the device timer's tick means one look.  (The timer is slow to read: only after
+// many tries.)
+__device__ __forceinline__ bool bar_wait_long(uint64_t* b, uint32_t parity, unsigned long long limit, volatile int* dead) {
     unsigned long long t0 = 0;
-    for (uint32_t i = 0; !bar_try(b, parity); ++i) {
+    for (uint32_t i = 0; limit >= 1000; ++i) {
+        if (bar_try(b, parity)) return true;
         if (*dead) return false;
         if ((i & 255u) == 255u) {
             const unsigned long long t = now_ns();
             if (t0 == 0) t0 = t;
-            if (t - t0 >= limit) {
-                *dead = 1;
-                return false;
-            }
+            if (t - t0 >= limit) break;
         }
     }
-    return true;
+    *dead = 1;
+    return false;
+}
+// by a whole warp, with one answer
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, unsigned long long limit, volatile int* dead) {
+    if (__all_sync(0xFFFFFFFFu, bar_test(b, parity))) return true;
+    return __all_sync(0xFFFFFFFFu, bar_wait_long(b, parity, limit, dead));
 }
 
 // ---- tensor memory and products -------------------------------------------
@@ -257,15 +256,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* smem_p = smem_raw + (smem - smem_u32(smem_raw));
     const uint32_t q_s = smem, ring_s = smem + C::kQBytes;
-    fill_idle_rows<T, kTThreads>(p);
-    Part part;
-    find_part<kTRows, kTThreads>(p, part, reinterpret_cast<int*>(smem_p));
-    if (part.todo == 0) return;
-
     if (t == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             bar_init(&s_full[s], 1);
-            bar_init(&s_empty[s], 1);
+            bar_init(&s_empty[s], 2);
         }
         for (int x = 0; x < 2; ++x) {
             bar_init(&s_q[x], 128);
@@ -274,7 +268,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             bar_init(&s_weights[x][1], 128);
             bar_init(&s_out[x], 1);
         }
-        bar_init(&s_last, 1);
+        bar_init(&s_last, 2);
         s_dead = 0;
         for (int i = 0; i < kBadSlots; ++i) s_bad[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -285,6 +279,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    fill_idle_rows<T, kTThreads>(p);
+    Part part;
+    find_part<kTRows, kTThreads>(p, part, reinterpret_cast<int*>(smem_p));
     fence_before();
     __syncthreads();
     fence_after();
@@ -293,7 +290,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const unsigned long long limit = ta.wait_ns;
     const int tile0 = part.tile;
 
-    if (warp < 8) {
+    if (part.todo == 0) {
+        // nothing to do
+    } else if (warp < 8) {
         // ---------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int x = warp >> 2;            // row tile
@@ -307,15 +306,24 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
         // the rows of unit w into shared memory, swizzled as the products read them
         auto load_q = [&](const Unit& w) {
-            const int r = w.rt * kTRows + x * 128 + row, rows = w.n * p.group;
+            const int rows = w.n * p.group;
             if (w.rt * kTRows + x * 128 >= rows) return;
-            unsigned char* dst = smem_p + x * 128 * D * 2 + row * 128;
-            const T* src = q_row<T>(p, w.b, w.h, min(r, rows - 1));
+            unsigned char* dst = smem_p + x * 128 * D * 2;
+            constexpr int RC = D / 8, STEP = 32 / RC;  // 16-byte pieces of a row, rows a step
+            const int c = lane % RC, r0 = w.rt * kTRows + x * 128, i0 = (row & ~31) + lane / RC;
+            constexpr int AHEAD = 8;
+#pragma unroll 1
+            for (int i = i0; i < i0 + 32; i += AHEAD * STEP) {
+                uint4 v[AHEAD];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows) v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-                *reinterpret_cast<uint4*>(dst + (c / 8) * C::kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = v;
+                for (int k = 0; k < AHEAD; ++k)
+                    v[k] = __ldg(reinterpret_cast<const uint4*>(
+                                     q_row<T>(p, w.b, w.h, min(r0 + i + k * STEP, rows - 1))) + c);
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const int j = i + k * STEP;  // (rows past the last are computed and dropped)
+                    *reinterpret_cast<uint4*>(dst + (c / 8) * C::kHalfBytes + j * 128 + (((c & 7) ^ (j & 7)) << 4)) = v[k];
+                }
             }
             fence_async_smem();
             bar_arrive(&s_q[x]);
@@ -328,7 +336,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const bool mine = u.rt * kTRows + x * 128 < rows;  // the tile has rows
             left -= end - first;
             Unit next = u;
-            if (left > 0) next_unit<kTRows>(p, next);
             if (mine) {
                 const int pos = u.past + by_group(p, min(r, rows - 1));
                 // of the warp's rows: the least and the greatest position
@@ -338,7 +345,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 float ref = -INFINITY, sum = 0.0f;
                 for (; alive && tile < end; ++tile) {
                     alive = bar_wait(&s_scores[x], n_scores & 1, limit, dead);
-                    alive = __all_sync(0xFFFFFFFFu, alive);
                     if (!alive) break;
                     ++n_scores;
                     fence_after();
@@ -367,8 +373,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         const float now = fmaxf(ref, m);
                         const float f = now == -INFINITY ? 1.0f : fast_exp2(ref - now);
                         alive = bar_wait(&s_out[x], n_out & 1, limit, dead);  // the product before this one
-                        alive = __all_sync(0xFFFFFFFFu, alive);
-                        if (!alive) break;
+                            if (!alive) break;
                         fence_after();
 #pragma unroll
                         for (int c = 0; c < D; c += 32) {
@@ -407,21 +412,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     sum += add[0].x + add[0].y;
                 }
                 // all scores of the unit are through: its queries make room for the next
+                if (left > 0) next_unit<kTRows>(p, next);
                 if (alive && left > 0) load_q(next);
                 if (alive) {
                     alive = bar_wait(&s_out[x], n_out & 1, limit, dead);
-                    alive = __all_sync(0xFFFFFFFFu, alive);
                     ++n_out;
                 }
                 fence_after();
                 const bool bad = !alive || s_bad[index % kBadSlots];
                 const int place = 2 * blockIdx.x + (index == 0 ? 0 : 1);
-                const int64_t part_row = (int64_t)place * kTRows + x * 128 + row;
+                // partial results lie by columns, so that a warp's stores are whole lines
+                float* part_o = p.part_o + (int64_t)place * kTRows * D + x * 128 + row;
                 const float l = bad ? NAN : sum;
                 const float inv = 1.0f / l;
                 T* dst = r < rows ? out_row<T>(p, u.b, u.h, r) : nullptr;
                 if (!whole && r < rows)
-                    *reinterpret_cast<float2*>(p.part_ml + part_row * 2) = make_float2(alive ? ref : -INFINITY, l);
+                    *reinterpret_cast<float2*>(p.part_ml + ((int64_t)place * kTRows + x * 128 + row) * 2) = make_float2(alive ? ref : -INFINITY, l);
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     if (alive) {
@@ -441,15 +447,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
                                                Pair<T>::pack(o[j + 6] * inv, o[j + 7] * inv));
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4*>(p.part_o + part_row * D + c + j) =
-                                    make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            for (int j = 0; j < 32; ++j) part_o[(int64_t)(c + j) * kTRows] = o[j];
                         }
                     }
                 }
                 fence_before();
-            } else if (alive && left > 0) {
-                load_q(next);
+            } else if (left > 0) {
+                next_unit<kTRows>(p, next);
+                if (alive) load_q(next);
             }
             if (!alive && lane == 0 && p.a.row_status) atomicOr(p.a.row_status + u.b, SV_ROW_INTERNAL);
             u = next;
@@ -458,104 +463,108 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8) {
+        if (warp == 8 || warp == 10) {
             // ------------------------------------------------------------ products
+            // of row tile x.  (One warp for both left the tensor cores idle between its
+            // batches: they take in only a few products ahead, and each hand-over costs a
+            // few hundred cycles.)
             constexpr uint32_t i_s = idesc<T>(kKeyTile, false), i_o = idesc<T>(D, true);
+            const int x = uniform(warp == 8 ? 0 : 1);
             Unit u = part.u;
             int tile = tile0, left = part.todo;
-            uint32_t stage = 0, turn = 0;      // ring place and its phase
-            uint32_t n_q[2] = {0, 0}, n_w[2] = {0, 0};
+            uint32_t stage = 0, turn = 0;  // ring place and its phase
+            uint32_t n_q = 0, n_w = 0;
             bool alive = true;
+            const uint32_t tS = uniform(tmem) + C::kS + x * 128, tO = uniform(tmem) + C::kO + x * D;
+            const uint32_t q_desc = uniform(desc_keys(q_s + x * 128 * D * 2));
             auto next_stage = [&]() {
                 if (++stage == C::kStages) {
                     stage = 0;
                     turn ^= 1;
                 }
             };
-            const uint32_t tm = uniform(tmem), q_desc = uniform(desc_keys(q_s));
-            auto scores = [&](int x, uint32_t ks) {
-                const uint32_t a = q_desc + x * (128 * D * 2 >> 4), b = uniform(desc_keys(ks));
+            auto scores = [&](uint32_t place) {
+                const uint32_t b = uniform(desc_keys(ring_s + place * C::kTileBytes));
                 if (elect()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t at = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
-                        mma_ss(tm + C::kS + x * 128, a + at, b + at, i_s, k > 0);
+                        mma_ss(tS, q_desc + at, b + at, i_s, k > 0);
                     }
                     mma_commit(&s_scores[x]);
+                    mma_commit(&s_empty[place]);
                 }
                 __syncwarp();
             };
             while (alive && left > 0) {
-                const int rows = u.n * p.group - u.rt * kTRows;
-                const int tiles_x = rows > 128 ? 2 : 1;
-                const int first = tile, end = min(u.t1, tile + left);
-                int lo, hi;
-                tile_keys<kTRows>(p, u.past, u.n, u.rt, lo, hi);
-                const int vend = u.past + u.n;
-                for (int x = 0; alive && x < tiles_x; ++x) alive = bar_wait(&s_q[x], n_q[x]++ & 1, limit, dead);
-                alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
-                alive = __all_sync(0xFFFFFFFFu, alive);
-                if (!alive) break;
-                fence_after();
-                for (int x = 0; x < tiles_x; ++x) scores(x, ring_s + stage * C::kTileBytes);
-                if (elect()) mma_commit(&s_empty[stage]);
-                __syncwarp();
-                next_stage();
-                for (; tile < end; ++tile, --left) {
-                    const bool more = tile + 1 < end;
-                    const uint32_t kstage = stage;
-                    if (more) {
+                const int end = min(u.t1, tile + left);
+                if (u.rt * kTRows + x * 128 >= u.n * p.group) {
+                    // no rows in this tile: only hand the ring's places on
+                    for (int i = 2 * (end - tile); alive && i > 0; --i) {
                         alive = bar_wait(&s_full[stage], turn, limit, dead);
+                        if (alive && lane == 0) bar_arrive(&s_empty[stage]);
                         next_stage();
                     }
-                    const uint32_t vstage = stage;
-                    alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
-                    next_stage();
-                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    left -= end - tile;
+                } else {
+                    const int first = tile;
+                    int lo, hi;
+                    tile_keys<kTRows>(p, u.past, u.n, u.rt, lo, hi);
+                    const int vend = u.past + u.n;
+                    alive = bar_wait(&s_q[x], n_q++ & 1, limit, dead) && bar_wait(&s_full[stage], turn, limit, dead);
                     if (!alive) break;
-                    const uint32_t ks = ring_s + kstage * C::kTileBytes, vs = ring_s + vstage * C::kTileBytes;
-                    // rows of a box outside the visible keys: what they hold times 0 must be 0
-                    const int k0 = tile * kKeyTile;
-                    const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, vend - k0));
-                    const int z0_from = z0 / ta.box * ta.box, z1_to = (z1 + ta.box - 1) / ta.box * ta.box;
-                    if (z0 > z0_from || z1 < z1_to) {
-                        constexpr int RC = D / 8;  // 16-byte pieces of a row
-                        for (int i = lane; i < ((z0 - z0_from) + (z1_to - z1)) * RC; i += 32) {
-                            const int zr = i / RC, c = i % RC;
-                            const int rr = zr < z0 - z0_from ? z0_from + zr : z1 + zr - (z0 - z0_from);
-                            *reinterpret_cast<uint4*>(smem_p + (vs - smem) + (c / 8) * C::kHalfBytes + rr * 128 +
-                                                      ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    fence_after();
+                    scores(stage);
+                    next_stage();
+                    for (; tile < end; ++tile, --left) {
+                        const bool more = tile + 1 < end;
+                        const uint32_t kstage = stage;
+                        if (more) {
+                            alive = bar_wait(&s_full[stage], turn, limit, dead);
+                            next_stage();
                         }
-                        fence_async_smem();
-                        __syncwarp();
-                    }
-                    const uint32_t v_desc = uniform(desc_values(vs, C::kHalfBytes));
-                    for (int x = 0; alive && x < tiles_x; ++x) {
+                        const uint32_t vstage = stage;
+                        alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
+                        if (!alive) break;
+                        next_stage();
+                        const uint32_t vs = ring_s + vstage * C::kTileBytes;
+                        // rows of a box outside the visible keys: what they hold times 0 must be
+                        // 0 (both tiles' warps write these zeros, each before its product)
+                        const int k0 = tile * kKeyTile;
+                        if (k0 < lo || k0 + kKeyTile > vend) {
+                            const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, vend - k0));
+                            const int from = z0 & ~(ta.box - 1), to = (z1 + ta.box - 1) & ~(ta.box - 1);
+                            constexpr int RC = D / 8;  // 16-byte pieces of a row
+                            for (int i = lane; i < (z0 - from + to - z1) * RC; i += 32) {
+                                const int zr = i / RC, c = i % RC;
+                                const int rr = zr < z0 - from ? from + zr : z1 + zr - (z0 - from);
+                                *reinterpret_cast<uint4*>(smem_p + (vs - smem) + (c / 8) * C::kHalfBytes + rr * 128 +
+                                                          ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_async_smem();
+                            __syncwarp();
+                        }
+                        const uint32_t v_desc = uniform(desc_values(vs, C::kHalfBytes));
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            alive = alive && bar_wait(&s_weights[x][half], n_w[x] & 1, limit, dead);
-                            alive = __all_sync(0xFFFFFFFFu, alive);
+                            alive = alive && bar_wait(&s_weights[x][half], n_w & 1, limit, dead);
                             if (!alive) break;
                             fence_after();
                             if (elect()) {
 #pragma unroll
                                 for (int k = half * 4; k < half * 4 + 4; ++k)
-                                    mma_ts(tm + C::kO + x * D, tm + C::kS + x * 128 + k * 8,
-                                           v_desc + k * (16 * 128 >> 4), i_o, tile > first || k > 0);
-                                if (half) mma_commit(&s_out[x]);
+                                    mma_ts(tO, tS + k * 8, v_desc + k * (16 * 128 >> 4), i_o, tile > first || k > 0);
+                                if (half) {
+                                    mma_commit(&s_out[x]);
+                                    mma_commit(&s_empty[vstage]);
+                                }
                             }
                             __syncwarp();
                         }
                         if (!alive) break;
-                        ++n_w[x];
-                        if (more) scores(x, ks);
+                        ++n_w;
+                        if (more) scores(kstage);
                     }
-                    if (!alive) break;
-                    if (elect()) {
-                        if (more) mma_commit(&s_empty[kstage]);
-                        mma_commit(&s_empty[vstage]);
-                    }
-                    __syncwarp();
                 }
                 if (alive && left > 0) {
                     next_unit<kTRows>(p, u);
@@ -580,7 +589,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
             int issued = 0;
             auto put = [&](const CUtensorMap* map, const Unit& w, int page, int in_page) {
                 alive = bar_wait(&s_empty[stage], turn ^ 1, limit, dead);
-                alive = __all_sync(0xFFFFFFFFu, alive);
                 if (!alive) return;
                 if (lane == 0) bar_expect(&s_full[stage], C::kTileBytes);
                 __syncwarp();
