@@ -10,8 +10,11 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
 
-// rows of a cache head's tile: 16 or 32 where that holds a sequence's rows, else 256
-int row_tile(int64_t N, int64_t group) { return N * group <= 16 ? 16 : N * group <= 32 ? 32 : 256; }
+// rows of a cache head's tile: 16, 32 or 64 where that holds a sequence's rows, else 256
+int row_tile(int64_t N, int64_t group) {
+    const int64_t rows = N * group;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
+}
 
 int check_attention(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads, int64_t dim) {
     if (B < 0 || N < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads) return SV_EINVAL;
@@ -45,7 +48,51 @@ int sm_count(int dev) {
     return counts[dev];
 }
 
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// the driver's encoder of tensor maps, fetched through the runtime (no link-time dependency)
+EncodeFn encoder() {
+    static EncodeFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (EncodeFn)f;
+    });
+    return fn;
+}
+
+// pages as [pages][heads][dim / 64][page_size][64]
+bool encode(CUtensorMap* m, const void* base, const AttendArgs& p, int64_t sp, int64_t sh, int64_t ss, int box,
+            int parts) {
+    EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[5] = {64, (cuuint64_t)p.a.cache.page_size, (cuuint64_t)p.a.dim / 64,
+                                (cuuint64_t)p.a.kv_heads, (cuuint64_t)p.a.cache.pages};
+    // a stride that no second element uses may be anything: give the encoder a plain one
+    if (p.a.kv_heads == 1) sh = ss;
+    if (p.a.cache.pages == 1) sp = ss;
+    const cuuint64_t strides[4] = {(cuuint64_t)ss * 2, 128, (cuuint64_t)sh * 2, (cuuint64_t)sp * 2};
+    const cuuint32_t boxes[5] = {64, (cuuint32_t)box, (cuuint32_t)parts, 1, 1}, ones[5] = {1, 1, 1, 1, 1};
+    return fn(m, p.a.dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+              const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
+
+bool encode_pages(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, int parts) {
+    const sv_paged_cache& c = p.a.cache;
+    return encode(keys, c.k_pages, p, c.k_stride_page, c.k_stride_head, c.k_stride_slot, box, parts) &&
+           encode(values, c.v_pages, p, c.v_stride_page, c.v_stride_head, c.v_stride_slot, box, parts);
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -106,8 +153,8 @@ extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream
     p.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     if (tiles < p.ctas) p.ctas = (int)tiles;
     cudaStream_t s = (cudaStream_t)stream;
-    const unsigned long long wait_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNs;
-    const cudaError_t e = rm == 256 ? launch_attend_tiles((int)a.dtype, (int)a.dim, p, wait_ns, s)
+    p.wait_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNs;
+    const cudaError_t e = rm == 256 ? launch_attend_tiles((int)a.dtype, (int)a.dim, p, s)
                                     : launch_attend_rows((int)a.dtype, (int)a.dim, rm / 16, p, s);
     if (e != cudaSuccess) return SV_ECUDA;
     if (launch_attend_join((int)a.dtype, (int)a.dim, rm, p, s) != cudaSuccess) return SV_ECUDA;

@@ -10,6 +10,8 @@
 // and its last, so the partials need two places a CTA.
 #pragma once
 
+#include <cuda.h>
+
 #include "sv_internal.cuh"
 #include "sv_paged.cuh"
 
@@ -35,6 +37,7 @@ struct AttendArgs {
     float qscale;        // scale * log2(e): scores are kept as powers of two
     int ctas;            // CTAs that share the work (at most kMaxCtas)
     int64_t capacity;    // positions that the page table addresses
+    unsigned long long wait_ns;  // limit of a wait
     Cut* cut;            // [ctas] each CTA's first unit, for the join
     float* part_o;       // [2 * ctas][RM][dim]
     float* part_ml;      // [2 * ctas][RM][2] running maximum (in log2 units) and sum
@@ -255,9 +258,13 @@ __device__ __forceinline__ float fast_exp2(float x) {  // 2^x; 2^-inf = 0
 
 #endif  // __CUDACC__
 
+// tensor maps of the pages, a head's rows in parts of 64 elements (128 bytes, swizzled):
+// boxes of `box` rows and `parts` parts
+bool encode_pages(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, int parts);
+
 // the two kernels' launchers (RM rows a tile) and the join of the cut units
 cudaError_t launch_attend_rows(int dtype, int dim, int mt, const AttendArgs& p, cudaStream_t s);
-cudaError_t launch_attend_tiles(int dtype, int dim, const AttendArgs& p, unsigned long long wait_ns, cudaStream_t s);
+cudaError_t launch_attend_tiles(int dtype, int dim, const AttendArgs& p, cudaStream_t s);
 cudaError_t launch_attend_join(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s);
 
 }  // namespace sv

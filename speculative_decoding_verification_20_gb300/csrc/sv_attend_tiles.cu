@@ -22,11 +22,10 @@
 //
 // Every wait has a limit.  When one runs out, the CTA writes NaN for what is left of its
 // part, sets SV_ROW_INTERNAL, lets its copies and products finish (with a limit) and ends.
-#include <cuda.h>
-
 #include <mutex>
 #include <type_traits>
 
+#include "sv_async.cuh"
 #include "sv_attend.cuh"
 
 namespace sv {
@@ -52,67 +51,8 @@ struct TilesCfg {
 
 struct TilesArgs {
     AttendArgs p;
-    unsigned long long wait_ns;
     int box;  // keys of a box
 };
-
-// ---- barriers ------------------------------------------------------------
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void bar_init(uint64_t* b, int count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* b) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(b)), "r"(parity)
-        : "memory");
-    return ok;
-}
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// without the hardware's own patience
-__device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(b)), "r"(parity)
-        : "memory");
-    return ok;
-}
-// False once the wait has run out, here or (dead) in another warp of the CTA.  A limit
-// below the device timer's tick means one look.  (The timer is slow to read: only after
-// many tries.)
-__device__ __forceinline__ bool bar_wait_long(uint64_t* b, uint32_t parity, unsigned long long limit, volatile int* dead) {
-    unsigned long long t0 = 0;
-    for (uint32_t i = 0; limit >= 1000; ++i) {
-        if (bar_try(b, parity)) return true;
-        if (*dead) return false;
-        if ((i & 255u) == 255u) {
-            const unsigned long long t = now_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 >= limit) break;
-        }
-    }
-    *dead = 1;
-    return false;
-}
-// by a whole warp, with one answer
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, unsigned long long limit, volatile int* dead) {
-    if (__all_sync(0xFFFFFFFFu, bar_test(b, parity))) return true;
-    return __all_sync(0xFFFFFFFFu, bar_wait_long(b, parity, limit, dead));
-}
 
 // ---- tensor memory and products -------------------------------------------
 // Descriptors of swizzled operands in shared memory, groups of 8 rows (1024 bytes) apart:
@@ -169,7 +109,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* b) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 #define SV_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), \
                     "=r"(a[i + 6]), "=r"(a[i + 7])
@@ -219,15 +158,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
         : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                        uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4,%5}], "
-        "[%6];" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-        : "memory");
-}
 
 // the instruction descriptor: fp32 results, T operands, n columns, B read across its rows
 // (values) or along them (keys), 128 rows
@@ -287,7 +217,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     fence_after();
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
-    const unsigned long long limit = ta.wait_ns;
+    const unsigned long long limit = p.wait_ns;
     const int tile0 = part.tile;
 
     if (part.todo == 0) {
@@ -373,7 +303,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         const float now = fmaxf(ref, m);
                         const float f = now == -INFINITY ? 1.0f : fast_exp2(ref - now);
                         alive = bar_wait(&s_out[x], n_out & 1, limit, dead);  // the product before this one
-                            if (!alive) break;
+                        if (!alive) break;
                         fence_after();
 #pragma unroll
                         for (int c = 0; c < D; c += 32) {
@@ -430,6 +360,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     *reinterpret_cast<float2*>(p.part_ml + ((int64_t)place * kTRows + x * 128 + row) * 2) = make_float2(alive ? ref : -INFINITY, l);
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
+                    __syncwarp();  // tensor memory is read by whole warps
                     if (alive) {
                         tmem_load32(tO + c, reinterpret_cast<uint32_t*>(o));
                     } else {
@@ -593,8 +524,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 if (lane == 0) bar_expect(&s_full[stage], C::kTileBytes);
                 __syncwarp();
                 if (loads)
-                    tma_box(ring_s + stage * C::kTileBytes + half * C::kHalfBytes + box * ta.box * 128, map, half * 64,
-                            in_page, w.h, page, &s_full[stage]);
+                    tma_part(ring_s + stage * C::kTileBytes + half * C::kHalfBytes + box * ta.box * 128, map, half,
+                             in_page, w.h, page, &s_full[stage]);
                 ++issued;
                 if (++stage == C::kStages) {
                     stage = 0;
@@ -660,56 +591,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// the driver's encoder of tensor maps, fetched through the runtime (no link-time dependency)
-EncodeFn encoder() {
-    static EncodeFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = (EncodeFn)f;
-    });
-    return fn;
-}
-
-// pages as [pages][heads][page_size][dim], boxes of `box` rows x 64 elements, swizzled
-bool encode(CUtensorMap* m, int dtype, const void* base, const AttendArgs& p, int64_t sp, int64_t sh, int64_t ss,
-            int box) {
-    EncodeFn fn = encoder();
-    if (!fn) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)p.a.dim, (cuuint64_t)p.a.cache.page_size, (cuuint64_t)p.a.kv_heads,
-                                (cuuint64_t)p.a.cache.pages};
-    // a stride that no second element uses may be anything: give the encoder a plain one
-    if (p.a.kv_heads == 1) sh = ss;
-    if (p.a.cache.pages == 1) sp = ss;
-    const cuuint64_t strides[3] = {(cuuint64_t)ss * 2, (cuuint64_t)sh * 2, (cuuint64_t)sp * 2};
-    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
-    return fn(m, dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-              const_cast<void*>(base), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename T, int D>
-cudaError_t launch_tiles(const AttendArgs& p, unsigned long long wait_ns, cudaStream_t s) {
+cudaError_t launch_tiles(const AttendArgs& p, cudaStream_t s) {
     constexpr int bytes = TilesCfg<D>::kSmem;
     TilesArgs ta;
     ta.p = p;
-    ta.wait_ns = wait_ns;
     ta.box = 16;
     while (ta.box < kKeyTile && p.a.cache.page_size % (2 * ta.box) == 0) ta.box *= 2;
     CUtensorMap km, vm;
-    const sv_paged_cache& c = p.a.cache;
-    if (!encode(&km, (int)p.a.dtype, c.k_pages, p, c.k_stride_page, c.k_stride_head, c.k_stride_slot, ta.box) ||
-        !encode(&vm, (int)p.a.dtype, c.v_pages, p, c.v_stride_page, c.v_stride_head, c.v_stride_slot, ta.box))
-        return cudaErrorInvalidValue;
+    if (!encode_pages(&km, &vm, p, ta.box, 1)) return cudaErrorInvalidValue;
     // once a device: room in shared memory, and proof that the register split fits the launch
     static std::mutex mu;
     static bool ready[64];
@@ -733,10 +623,10 @@ cudaError_t launch_tiles(const AttendArgs& p, unsigned long long wait_ns, cudaSt
 
 }  // namespace
 
-cudaError_t launch_attend_tiles(int dtype, int dim, const AttendArgs& p, unsigned long long wait_ns, cudaStream_t s) {
+cudaError_t launch_attend_tiles(int dtype, int dim, const AttendArgs& p, cudaStream_t s) {
     if (dtype == SV_BF16)
-        return dim == 64 ? launch_tiles<__nv_bfloat16, 64>(p, wait_ns, s) : launch_tiles<__nv_bfloat16, 128>(p, wait_ns, s);
-    return dim == 64 ? launch_tiles<__half, 64>(p, wait_ns, s) : launch_tiles<__half, 128>(p, wait_ns, s);
+        return dim == 64 ? launch_tiles<__nv_bfloat16, 64>(p, s) : launch_tiles<__nv_bfloat16, 128>(p, s);
+    return dim == 64 ? launch_tiles<__half, 64>(p, s) : launch_tiles<__half, 128>(p, s);
 }
 
 }  // namespace sv

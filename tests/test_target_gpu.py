@@ -394,14 +394,16 @@ def test_attention_is_repeatable_on_other_streams_and_in_graphs(N):
     check_attention(s, past, new, got=out)
 
 
-def test_attention_gives_up_a_wait_and_recovers():
+@pytest.mark.parametrize("N", [1, 8, 150])
+def test_attention_gives_up_a_wait_and_recovers(N):
     """A limit that no wait can keep: NaN and a status, and the next call is unaffected."""
-    N, past, new = 150, [3000, 200], [150, 150]
+    past, new = [3000, 200], [N, N]
     s = paged(2, N, 8, 2, 128, BF, 32, past, new, seed=6)
     st = torch.zeros(2, dtype=torch.int32, device="cuda")
     got = sv.paged_attention(s["q"], s["cache"], s["table"], s["lens"], s["new"], row_status=st, wait_limit_ns=1)
-    assert st.tolist() == [sv.ROW_INTERNAL] * 2
-    assert bool(got.isnan().any(-1).all(1).all(1).any())
+    # (a short sequence's waits may be over at the first look)
+    assert st[0] == sv.ROW_INTERNAL and st[1] in (0, sv.ROW_INTERNAL)
+    assert bool(got[0].isnan().any())
     st.zero_()
     check_attention(s, past, new, row_status=st)
     assert st.tolist() == [0, 0]
