@@ -10,10 +10,10 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
 
-// rows of a cache head's tile: 16, 32 or 64 where that holds a sequence's rows, else 256
+// rows of a cache head's tile: 16, 32 or 128 where that holds a sequence's rows, else 256
 int row_tile(int64_t N, int64_t group) {
     const int64_t rows = N * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
 }
 
 int check_attention(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads, int64_t dim) {
@@ -154,8 +154,8 @@ extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream
     if (tiles < p.ctas) p.ctas = (int)tiles;
     cudaStream_t s = (cudaStream_t)stream;
     p.wait_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNs;
-    const cudaError_t e = rm == 256 ? launch_attend_tiles((int)a.dtype, (int)a.dim, p, s)
-                                    : launch_attend_rows((int)a.dtype, (int)a.dim, rm / 16, p, s);
+    const cudaError_t e = rm >= 128 ? launch_attend_tiles((int)a.dtype, (int)a.dim, rm, p, s)
+                                   : launch_attend_rows((int)a.dtype, (int)a.dim, rm / 16, p, s);
     if (e != cudaSuccess) return SV_ECUDA;
     if (launch_attend_join((int)a.dtype, (int)a.dim, rm, p, s) != cudaSuccess) return SV_ECUDA;
     return SV_OK;

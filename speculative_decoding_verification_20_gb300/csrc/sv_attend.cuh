@@ -264,7 +264,7 @@ bool encode_pages(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, i
 
 // the two kernels' launchers (RM rows a tile) and the join of the cut units
 cudaError_t launch_attend_rows(int dtype, int dim, int mt, const AttendArgs& p, cudaStream_t s);
-cudaError_t launch_attend_tiles(int dtype, int dim, const AttendArgs& p, cudaStream_t s);
+cudaError_t launch_attend_tiles(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s);
 cudaError_t launch_attend_join(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s);
 
 }  // namespace sv

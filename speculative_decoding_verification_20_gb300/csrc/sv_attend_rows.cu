@@ -1,7 +1,7 @@
 // sv_attend_rows.cu -- attention of a few query rows a cache head over a long cache:
 // single tokens and verification rounds; and the join of units that were cut.
 //
-// Each key and value is read once for up to 64 query rows, 2 multiply-adds a byte and
+// Each key and value is read once for up to 32 query rows, 2 multiply-adds a byte and
 // row: the call is bound by reading the cache.  Three warps of a CTA do nothing but load:
 // they look the pages up, 32 blocks of 16 keys at a time, and keep a ring of 144 KB of
 // blocks in flight by TMA.  (One such warp takes some 700 cycles a block, twice what the
@@ -489,8 +489,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
 
 // results by columns: a thread has kJoinCols columns of a row, a warp 32 rows
 template <typename T, int D, int RM>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_columns_kernel(const __grid_constant__ AttendArgs p) {
-    static_assert(RM == kJoinThreads, "a thread a row");
+__global__ void __launch_bounds__(RM) attend_join_columns_kernel(const __grid_constant__ AttendArgs p) {
     Cut k;
     if (!join_unit(p, k)) return;
     const int r = threadIdx.x, c0 = blockIdx.y * kJoinCols;
@@ -531,14 +530,15 @@ cudaError_t launch_join(const AttendArgs& p, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if constexpr (RM == kJoinThreads) {
+    if constexpr (RM >= 128) {
+        cfg.blockDim = dim3(RM);
         cfg.gridDim = dim3((unsigned)p.ctas, D / kJoinCols);
         return cudaLaunchKernelEx(&cfg, attend_join_columns_kernel<T, D, RM>, p);
     } else {
+        cfg.blockDim = dim3(kJoinThreads);
         cfg.gridDim = dim3((unsigned)p.ctas, RM / (kJoinThreads / 32));
         return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, RM>, p);
     }
@@ -546,12 +546,12 @@ cudaError_t launch_join(const AttendArgs& p, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t rows_of(int mt, const AttendArgs& p, cudaStream_t s) {
-    return mt == 1 ? launch_rows<T, D, 1>(p, s) : mt == 2 ? launch_rows<T, D, 2>(p, s) : launch_rows<T, D, 4>(p, s);
+    return mt == 1 ? launch_rows<T, D, 1>(p, s) : launch_rows<T, D, 2>(p, s);
 }
 template <typename T, int D>
 cudaError_t join_of(int rm, const AttendArgs& p, cudaStream_t s) {
     return rm == 16 ? launch_join<T, D, 16>(p, s) : rm == 32 ? launch_join<T, D, 32>(p, s)
-         : rm == 64 ? launch_join<T, D, 64>(p, s) : launch_join<T, D, 256>(p, s);
+         : rm == 128 ? launch_join<T, D, 128>(p, s) : launch_join<T, D, 256>(p, s);
 }
 
 }  // namespace

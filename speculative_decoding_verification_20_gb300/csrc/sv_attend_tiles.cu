@@ -34,13 +34,12 @@ namespace {
 constexpr int kTThreads = 384;
 // registers a thread: softmax warps, the others; their sum has to fit the launch's share
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
-constexpr int kTRows = 256;
 constexpr int kBadSlots = 16;  // units that the loader can be ahead by, and more
 
 template <int D>
 struct TilesCfg {
     static constexpr int kTileBytes = kKeyTile * D * 2;
-    static constexpr int kQBytes = kTRows * D * 2;
+    static constexpr int kQBytes = 256 * D * 2;
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kHalves = D / 64;                // 128-byte columns of a tile
     static constexpr int kHalfBytes = kKeyTile * 128;     // 128 rows of one
@@ -167,16 +166,21 @@ __device__ constexpr uint32_t idesc(int n, bool b_across) {
     return (1u << 4) | (f << 7) | (f << 10) | (b_across ? 1u << 16 : 0u) | ((uint32_t)(n / 8) << 17) | (8u << 24);
 }
 
-template <typename T, int D>
+// SPLIT: a unit is one tile of 128 rows, and the two halves of the CTA take its key tiles
+// in turn, each with its own maximum, sum and output; the first half joins them.
+template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(kTThreads, 1)
     attend_tiles_kernel(const __grid_constant__ TilesArgs ta, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
     using C = TilesCfg<D>;
+    constexpr int RM = SPLIT ? 128 : 256;
+    constexpr int STEP = SPLIT ? 2 : 1;  // key tiles from one of a half's to the next
     const AttendArgs& p = ta.p;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];     // ring of key and value tiles
-    __shared__ uint64_t s_q[2], s_scores[2], s_weights[2][2], s_out[2];  // per row tile (weights: halves)
-    __shared__ uint64_t s_last;
+    __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];  // ring of key and value tiles
+    __shared__ uint64_t s_q[2], s_scores[2], s_weights[2][2], s_out[2];  // per half (weights: in two parts)
+    __shared__ uint64_t s_last, s_second, s_joined;
+    __shared__ float2 s_ml[SPLIT ? 128 : 1];  // the second half's maximum and sum
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
     __shared__ int s_bad[kBadSlots];
@@ -189,7 +193,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     if (t == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             bar_init(&s_full[s], 1);
-            bar_init(&s_empty[s], 2);
+            bar_init(&s_empty[s], 2);  // both halves, whether or not they read the stage
         }
         for (int x = 0; x < 2; ++x) {
             bar_init(&s_q[x], 128);
@@ -199,6 +203,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
             bar_init(&s_out[x], 1);
         }
         bar_init(&s_last, 2);
+        bar_init(&s_second, 128);
+        bar_init(&s_joined, 128);
         s_dead = 0;
         for (int i = 0; i < kBadSlots; ++i) s_bad[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -211,73 +217,83 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     fill_idle_rows<T, kTThreads>(p);
     Part part;
-    find_part<kTRows, kTThreads>(p, part, reinterpret_cast<int*>(smem_p));
+    find_part<RM, kTThreads>(p, part, reinterpret_cast<int*>(smem_p));
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
     const unsigned long long limit = p.wait_ns;
-    const int tile0 = part.tile;
 
     if (part.todo == 0) {
         // nothing to do
     } else if (warp < 8) {
         // ---------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        const int x = warp >> 2;            // row tile
-        const int row = t & 127;            // row of it
+        const int x = warp >> 2;              // half of the CTA
+        const int row = t & 127;              // row of its tile
+        const int x0 = SPLIT ? 0 : x * 128;   // the tile's first row in the unit
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + C::kS + x * 128 + lanes, tO = tmem + C::kO + x * D + lanes;
         Unit u = part.u;
-        int tile = tile0, left = part.todo, index = 0;
+        int first = part.tile, left = part.todo, index = 0;
         uint32_t n_scores = 0, n_out = 0;  // phases seen
         bool alive = true;
 
-        // the rows of unit w into shared memory, swizzled as the products read them
-        auto load_q = [&](const Unit& w) {
+        // the rows of unit w (the index-th) into shared memory, swizzled as the products
+        // read them; SPLIT: by the first half, in two places in turn
+        auto load_q = [&](const Unit& w, int index) {
             const int rows = w.n * p.group;
-            if (w.rt * kTRows + x * 128 >= rows) return;
-            unsigned char* dst = smem_p + x * 128 * D * 2;
-            constexpr int RC = D / 8, STEP = 32 / RC;  // 16-byte pieces of a row, rows a step
-            const int c = lane % RC, r0 = w.rt * kTRows + x * 128, i0 = (row & ~31) + lane / RC;
+            if (SPLIT ? x != 0 : w.rt * RM + x0 >= rows) return;
+            unsigned char* dst = smem_p + (SPLIT ? index & 1 : x) * 128 * D * 2;
+            constexpr int RC = D / 8, RS = 32 / RC;  // 16-byte pieces of a row, rows a step
+            const int c = lane % RC, r0 = w.rt * RM + x0, i0 = (row & ~31) + lane / RC;
             constexpr int AHEAD = 8;
 #pragma unroll 1
-            for (int i = i0; i < i0 + 32; i += AHEAD * STEP) {
+            for (int i = i0; i < i0 + 32; i += AHEAD * RS) {
                 uint4 v[AHEAD];
 #pragma unroll
                 for (int k = 0; k < AHEAD; ++k)
                     v[k] = __ldg(reinterpret_cast<const uint4*>(
-                                     q_row<T>(p, w.b, w.h, min(r0 + i + k * STEP, rows - 1))) + c);
+                                     q_row<T>(p, w.b, w.h, min(r0 + i + k * RS, rows - 1))) + c);
 #pragma unroll
                 for (int k = 0; k < AHEAD; ++k) {
-                    const int j = i + k * STEP;  // (rows past the last are computed and dropped)
+                    const int j = i + k * RS;  // (rows past the last are computed and dropped)
                     *reinterpret_cast<uint4*>(dst + (c / 8) * C::kHalfBytes + j * 128 + (((c & 7) ^ (j & 7)) << 4)) = v[k];
                 }
             }
             fence_async_smem();
-            bar_arrive(&s_q[x]);
+            bar_arrive(&s_q[SPLIT ? index & 1 : x]);
         };
-        load_q(u);
+        load_q(u, 0);
         while (left > 0) {
-            const int rows = u.n * p.group, r = u.rt * kTRows + x * 128 + row;
-            const int first = tile, end = min(u.t1, tile + left);
+            const int rows = u.n * p.group, r = u.rt * RM + x0 + row;
+            const int end = min(u.t1, first + left);
             const bool whole = first == u.t0 && end == u.t1;
-            const bool mine = u.rt * kTRows + x * 128 < rows;  // the tile has rows
             left -= end - first;
             Unit next = u;
-            if (mine) {
+            if (SPLIT || u.rt * RM + x0 < rows) {  // the tile has rows
+                const int start = first + (SPLIT ? x : 0);
                 const int pos = u.past + by_group(p, min(r, rows - 1));
-                // of the warp's rows: the least and the greatest position
-                const int wr0 = u.rt * kTRows + x * 128 + (row & ~31);
+                // of the warp's rows: the least and the greatest position; or there is none
+                const int wr0 = r - lane;
                 const int pos0 = u.past + by_group(p, min(wr0, rows - 1));
                 const int pos1 = u.past + by_group(p, min(wr0 + 31, rows - 1));
                 float ref = -INFINITY, sum = 0.0f;
-                for (; alive && tile < end; ++tile) {
+                // the first half has to be through with what the second left of the unit before
+                if (SPLIT && x == 1 && index > 0) alive = alive && bar_wait(&s_joined, (index - 1) & 1, limit, dead);
+                for (int tile = start; alive && tile < end; tile += STEP) {
                     alive = bar_wait(&s_scores[x], n_scores & 1, limit, dead);
                     if (!alive) break;
                     ++n_scores;
                     fence_after();
+                    if (wr0 >= rows) {  // no rows: their lanes' products go nowhere
+                        if (tile != start) ++n_out;
+                        fence_before();
+                        bar_arrive(&s_weights[x][0]);
+                        bar_arrive(&s_weights[x][1]);
+                        continue;
+                    }
                     float s[kKeyTile];
                     tmem_load128(tS, reinterpret_cast<uint32_t*>(s));
                     const int k0 = tile * kKeyTile;
@@ -296,7 +312,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[kKeyTile - 4 + e]);
                     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.qscale;
-                    if (tile == first) {
+                    if (tile == start) {
                         ref = m;
                     } else if (__any_sync(0xFFFFFFFFu, m > ref + 8.0f)) {
                         // raise the reference; the output so far shrinks by as much
@@ -316,7 +332,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         sum *= f;
                         ref = now;
                     }
-                    if (tile != first) ++n_out;
+                    if (tile != start) ++n_out;
                     const float base = ref == -INFINITY ? 0.0f : ref;  // nothing visible yet: weights 0
                     const float2 qs = make_float2(p.qscale, p.qscale), mb = make_float2(-base, -base);
                     float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -342,123 +358,158 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     sum += add[0].x + add[0].y;
                 }
                 // all scores of the unit are through: its queries make room for the next
-                if (left > 0) next_unit<kTRows>(p, next);
-                if (alive && left > 0) load_q(next);
-                if (alive) {
+                if (left > 0) next_unit<RM>(p, next);
+                if (alive && left > 0) load_q(next, index + 1);
+                if (alive && start < end) {
                     alive = bar_wait(&s_out[x], n_out & 1, limit, dead);
                     ++n_out;
                 }
-                fence_after();
-                const bool bad = !alive || s_bad[index % kBadSlots];
-                const int place = 2 * blockIdx.x + (index == 0 ? 0 : 1);
-                // partial results lie by columns, so that a warp's stores are whole lines
-                float* part_o = p.part_o + (int64_t)place * kTRows * D + x * 128 + row;
-                const float l = bad ? NAN : sum;
-                const float inv = 1.0f / l;
-                T* dst = r < rows ? out_row<T>(p, u.b, u.h, r) : nullptr;
-                if (!whole && r < rows)
-                    *reinterpret_cast<float2*>(p.part_ml + ((int64_t)place * kTRows + x * 128 + row) * 2) = make_float2(alive ? ref : -INFINITY, l);
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    __syncwarp();  // tensor memory is read by whole warps
-                    if (alive) {
-                        tmem_load32(tO + c, reinterpret_cast<uint32_t*>(o));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-                    }
-                    if (r < rows) {
-                        if (whole) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 8)
-                                *reinterpret_cast<uint4*>(dst + c + j) =
-                                    make_uint4(Pair<T>::pack(o[j] * inv, o[j + 1] * inv),
-                                               Pair<T>::pack(o[j + 2] * inv, o[j + 3] * inv),
-                                               Pair<T>::pack(o[j + 4] * inv, o[j + 5] * inv),
-                                               Pair<T>::pack(o[j + 6] * inv, o[j + 7] * inv));
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) part_o[(int64_t)(c + j) * kTRows] = o[j];
+                if (SPLIT && x == 1) {
+                    s_ml[row] = make_float2(ref, sum);
+                    fence_before();
+                    bar_arrive(&s_second);
+                } else {
+                    float f0 = 1.0f, f1 = 0.0f;  // of the two halves' outputs
+                    if (SPLIT) {
+                        alive = alive && bar_wait(&s_second, index & 1, limit, dead);
+                        if (alive) {
+                            const float2 ml = s_ml[row];
+                            const float now = fmaxf(ref, ml.x);
+                            f0 = ref == -INFINITY ? 0.0f : fast_exp2(ref - now);
+                            f1 = ml.x == -INFINITY ? 0.0f : fast_exp2(ml.x - now);
+                            ref = now;
+                            sum = sum * f0 + ml.y * f1;
                         }
                     }
+                    fence_after();
+                    const bool bad = !alive || s_bad[index % kBadSlots];
+                    const int place = 2 * blockIdx.x + (index == 0 ? 0 : 1);
+                    // partial results lie by columns, so that a warp's stores are whole lines
+                    float* part_o = p.part_o + (int64_t)place * RM * D + x0 + row;
+                    const float l = bad ? NAN : sum;
+                    const float inv = 1.0f / l;
+                    T* dst = r < rows ? out_row<T>(p, u.b, u.h, r) : nullptr;
+                    if (!whole && r < rows)
+                        *reinterpret_cast<float2*>(p.part_ml + ((int64_t)place * RM + x0 + row) * 2) =
+                            make_float2(alive ? ref : -INFINITY, l);
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        __syncwarp();  // tensor memory is read by whole warps
+                        if (alive) {
+                            tmem_load32(tO + c, reinterpret_cast<uint32_t*>(o));
+                            if (SPLIT) {
+                                if (end - first > 1) {
+                                    float o1[32];
+                                    tmem_load32(tO + D + c, reinterpret_cast<uint32_t*>(o1));
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + o1[j] * f1;
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+                        }
+                        if (r < rows) {
+                            if (whole) {
+#pragma unroll
+                                for (int j = 0; j < 32; j += 8)
+                                    *reinterpret_cast<uint4*>(dst + c + j) =
+                                        make_uint4(Pair<T>::pack(o[j] * inv, o[j + 1] * inv),
+                                                   Pair<T>::pack(o[j + 2] * inv, o[j + 3] * inv),
+                                                   Pair<T>::pack(o[j + 4] * inv, o[j + 5] * inv),
+                                                   Pair<T>::pack(o[j + 6] * inv, o[j + 7] * inv));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) part_o[(int64_t)(c + j) * RM] = o[j];
+                            }
+                        }
+                    }
+                    fence_before();
+                    if (SPLIT) bar_arrive(&s_joined);
                 }
-                fence_before();
             } else if (left > 0) {
-                next_unit<kTRows>(p, next);
-                if (alive) load_q(next);
+                next_unit<RM>(p, next);
+                if (alive) load_q(next, index + 1);
             }
             if (!alive && lane == 0 && p.a.row_status) atomicOr(p.a.row_status + u.b, SV_ROW_INTERNAL);
             u = next;
-            tile = u.t0;
+            first = u.t0;
             ++index;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8 || warp == 10) {
             // ------------------------------------------------------------ products
-            // of row tile x.  (One warp for both left the tensor cores idle between its
+            // of one half each.  (One warp for both left the tensor cores idle between its
             // batches: they take in only a few products ahead, and each hand-over costs a
             // few hundred cycles.)
             constexpr uint32_t i_s = idesc<T>(kKeyTile, false), i_o = idesc<T>(D, true);
             const int x = uniform(warp == 8 ? 0 : 1);
             Unit u = part.u;
-            int tile = tile0, left = part.todo;
-            uint32_t stage = 0, turn = 0;  // ring place and its phase
-            uint32_t n_q = 0, n_w = 0;
+            int first = part.tile, left = part.todo, index = 0;
+            // Places of the ring, counted through: keys and values of one tile, then the next.
+            // Every half waits for every place in order and gives it back, read or not: a
+            // phase parity only tells a barrier's last two phases apart, so that a half that
+            // skipped the other's places could run a lap ahead of them and pass too early.
+            uint32_t at = 0, stage = 0, turn = 0;
+            uint32_t n_w = 0, n_q = 0;
             bool alive = true;
             const uint32_t tS = uniform(tmem) + C::kS + x * 128, tO = uniform(tmem) + C::kO + x * D;
-            const uint32_t q_desc = uniform(desc_keys(q_s + x * 128 * D * 2));
-            auto next_stage = [&]() {
+            auto next_place = [&]() {
+                ++at;
                 if (++stage == C::kStages) {
                     stage = 0;
                     turn ^= 1;
                 }
             };
-            auto scores = [&](uint32_t place) {
-                const uint32_t b = uniform(desc_keys(ring_s + place * C::kTileBytes));
+            // waits up to place i; gives back those before it
+            auto reach = [&](uint32_t i) -> bool {
+                while (at != i) {
+                    if (!bar_wait(&s_full[stage], turn, limit, dead)) return false;
+                    if (lane == 0) bar_arrive(&s_empty[stage]);
+                    next_place();
+                }
+                return bar_wait(&s_full[stage], turn, limit, dead);
+            };
+            // S of the keys in the place that was reached
+            auto scores = [&](uint32_t q_desc) {
+                const uint32_t b = uniform(desc_keys(ring_s + stage * C::kTileBytes));
+                fence_after();
                 if (elect()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
-                        mma_ss(tS, q_desc + at, b + at, i_s, k > 0);
+                        const uint32_t off = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
+                        mma_ss(tS, q_desc + off, b + off, i_s, k > 0);
                     }
                     mma_commit(&s_scores[x]);
-                    mma_commit(&s_empty[place]);
+                    mma_commit(&s_empty[stage]);
                 }
                 __syncwarp();
+                next_place();
             };
             while (alive && left > 0) {
-                const int end = min(u.t1, tile + left);
-                if (u.rt * kTRows + x * 128 >= u.n * p.group) {
-                    // no rows in this tile: only hand the ring's places on
-                    for (int i = 2 * (end - tile); alive && i > 0; --i) {
-                        alive = bar_wait(&s_full[stage], turn, limit, dead);
-                        if (alive && lane == 0) bar_arrive(&s_empty[stage]);
-                        next_stage();
-                    }
-                    left -= end - tile;
-                } else {
-                    const int first = tile;
+                const int end = min(u.t1, first + left);
+                const uint32_t last = at + 2 * (end - first);  // the place after the unit's
+                if (SPLIT || u.rt * RM + x * 128 < u.n * p.group) {
+                    const int start = first + (SPLIT ? x : 0);
                     int lo, hi;
-                    tile_keys<kTRows>(p, u.past, u.n, u.rt, lo, hi);
+                    tile_keys<RM>(p, u.past, u.n, u.rt, lo, hi);
                     const int vend = u.past + u.n;
-                    alive = bar_wait(&s_q[x], n_q++ & 1, limit, dead) && bar_wait(&s_full[stage], turn, limit, dead);
-                    if (!alive) break;
-                    fence_after();
-                    scores(stage);
-                    next_stage();
-                    for (; tile < end; ++tile, --left) {
-                        const bool more = tile + 1 < end;
-                        const uint32_t kstage = stage;
-                        if (more) {
-                            alive = bar_wait(&s_full[stage], turn, limit, dead);
-                            next_stage();
-                        }
-                        const uint32_t vstage = stage;
-                        alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
+                    const uint32_t q_desc = uniform(desc_keys(q_s + (SPLIT ? index & 1 : x) * 128 * D * 2));
+                    uint32_t i = at + 2 * (start - first);
+                    if (start < end) {
+                        // SPLIT: the place of the queries is not written again before this half is
+                        // through with the unit, so the unit's count gives the phase
+                        alive = bar_wait(&s_q[SPLIT ? index & 1 : x], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
+                        alive = alive && reach(i);
+                        if (alive) scores(q_desc);
+                    }
+                    for (int tile = start; alive && tile < end; tile += STEP, i += 2 * STEP) {
+                        const bool more = tile + STEP < end;
+                        alive = reach(i + 1);
                         if (!alive) break;
-                        next_stage();
-                        const uint32_t vs = ring_s + vstage * C::kTileBytes;
+                        const uint32_t vstage = stage, vs = ring_s + stage * C::kTileBytes;
+                        next_place();
                         // rows of a box outside the visible keys: what they hold times 0 must be
                         // 0 (both tiles' warps write these zeros, each before its product)
                         const int k0 = tile * kKeyTile;
@@ -466,8 +517,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                             const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, vend - k0));
                             const int from = z0 & ~(ta.box - 1), to = (z1 + ta.box - 1) & ~(ta.box - 1);
                             constexpr int RC = D / 8;  // 16-byte pieces of a row
-                            for (int i = lane; i < (z0 - from + to - z1) * RC; i += 32) {
-                                const int zr = i / RC, c = i % RC;
+                            for (int j = lane; j < (z0 - from + to - z1) * RC; j += 32) {
+                                const int zr = j / RC, c = j % RC;
                                 const int rr = zr < z0 - from ? from + zr : z1 + zr - (z0 - from);
                                 *reinterpret_cast<uint4*>(smem_p + (vs - smem) + (c / 8) * C::kHalfBytes + rr * 128 +
                                                           ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
@@ -475,6 +526,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                             fence_async_smem();
                             __syncwarp();
                         }
+                        if (!SPLIT && more) alive = reach(i + 2);  // the next keys, while the softmax runs
                         const uint32_t v_desc = uniform(desc_values(vs, C::kHalfBytes));
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -484,7 +536,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                             if (elect()) {
 #pragma unroll
                                 for (int k = half * 4; k < half * 4 + 4; ++k)
-                                    mma_ts(tO, tS + k * 8, v_desc + k * (16 * 128 >> 4), i_o, tile > first || k > 0);
+                                    mma_ts(tO, tS + k * 8, v_desc + k * (16 * 128 >> 4), i_o, tile > start || k > 0);
                                 if (half) {
                                     mma_commit(&s_out[x]);
                                     mma_commit(&s_empty[vstage]);
@@ -494,12 +546,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         }
                         if (!alive) break;
                         ++n_w;
-                        if (more) scores(kstage);
+                        if (more) {
+                            if (SPLIT) alive = reach(i + 2 * STEP);
+                            if (alive) scores(q_desc);
+                        }
                     }
                 }
+                while (alive && at != last) {  // what is left of the unit is the other half's
+                    alive = bar_wait(&s_full[stage], turn, limit, dead);
+                    if (alive && lane == 0) bar_arrive(&s_empty[stage]);
+                    if (alive) next_place();
+                }
+                left -= end - first;
+                ++index;
                 if (alive && left > 0) {
-                    next_unit<kTRows>(p, u);
-                    tile = u.t0;
+                    next_unit<RM>(p, u);
+                    first = u.t0;
                 }
             }
             // products still in flight end before tensor memory is given back
@@ -510,22 +572,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
         } else if (warp == 9) {
             // ------------------------------------------------------------ loads
             Unit u = part.u;
-            int tile = tile0, left = part.todo, index = 0;
+            int tile = part.tile, left = part.todo, index = 0;
             uint32_t stage = 0, turn = 0;
-            const int page_size = (int)p.a.cache.page_size, per = kKeyTile / ta.box;
+            const int per = kKeyTile / ta.box;
             const bool loads = lane < per * C::kHalves;
             const int box = lane / C::kHalves, half = lane % C::kHalves;
             const int no_page = (int)p.a.cache.pages;  // past the last: zeros
             bool alive = true;
             int issued = 0;
-            auto put = [&](const CUtensorMap* map, const Unit& w, int page, int in_page) {
-                alive = bar_wait(&s_empty[stage], turn ^ 1, limit, dead);
+            auto put = [&](const CUtensorMap* map, int h, int page, int in_page) {
+                alive = alive && bar_wait(&s_empty[stage], turn ^ 1, limit, dead);
                 if (!alive) return;
                 if (lane == 0) bar_expect(&s_full[stage], C::kTileBytes);
                 __syncwarp();
                 if (loads)
                     tma_part(ring_s + stage * C::kTileBytes + half * C::kHalfBytes + box * ta.box * 128, map, half,
-                             in_page, w.h, page, &s_full[stage]);
+                             in_page, h, page, &s_full[stage]);
                 ++issued;
                 if (++stage == C::kStages) {
                     stage = 0;
@@ -535,47 +597,49 @@ __global__ void __launch_bounds__(kTThreads, 1)
             // the lane's box of a tile: page id (bad and invisible ones: no_page)
             auto find = [&](const Unit& w, int tl, int& page, int& in_page) -> bool {
                 int lo, hi;
-                tile_keys<kTRows>(p, w.past, w.n, w.rt, lo, hi);
+                tile_keys<RM>(p, w.past, w.n, w.rt, lo, hi);
                 const int k = tl * kKeyTile + box * ta.box;
                 page = no_page;
                 in_page = 0;
                 if (!loads || k > hi || k + ta.box <= lo) return false;
-                const int at = page_of(p, k);
-                page = p.a.cache.page_table[w.b * p.a.cache.page_table_stride + at];
-                in_page = k - at * page_size;
+                const int i = page_of(p, k);
+                page = p.a.cache.page_table[w.b * p.a.cache.page_table_stride + i];
+                in_page = k - i * (int)p.a.cache.page_size;
                 if (page < 0 || page >= no_page) {
                     page = no_page;
                     return true;
                 }
                 return false;
             };
+            int page, in_page;
+            bool bad = find(u, tile, page, in_page);
             while (alive && left > 0) {
                 const int end = min(u.t1, tile + left);
-                int page, in_page, vpage, vin;
-                bool bad = find(u, tile, vpage, vin);
                 if (lane == 0) s_bad[index % kBadSlots] = 0;
                 __syncwarp();
-                put(&kmap, u, vpage, vin);
+                Unit next = u;
+                if (left > end - tile) next_unit<RM>(p, next);
                 for (; alive && tile < end; ++tile, --left) {
                     if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) {
                         *(volatile int*)&s_bad[index % kBadSlots] = 1;
                         if (p.a.row_status) atomicOr(p.a.row_status + u.b, SV_ROW_BAD_PAGE);
                         __threadfence_block();
                     }
-                    if (tile + 1 < end) {
-                        bad = find(u, tile + 1, page, in_page);
-                        put(&kmap, u, page, in_page);
-                        if (!alive) break;
-                    }
-                    put(&vmap, u, vpage, vin);
-                    vpage = page;
-                    vin = in_page;
+                    // the next tile's pages are looked up while this one's copies run
+                    int page1 = no_page, in_page1 = 0;
+                    bad = false;
+                    put(&kmap, u.h, page, in_page);
+                    if (tile + 1 < end)
+                        bad = find(u, tile + 1, page1, in_page1);
+                    else if (left > 1)
+                        bad = find(next, next.t0, page1, in_page1);
+                    put(&vmap, u.h, page, in_page);
+                    page = page1;
+                    in_page = in_page1;
                 }
                 ++index;
-                if (alive && left > 0) {
-                    next_unit<kTRows>(p, u);
-                    tile = u.t0;
-                }
+                u = next;
+                tile = u.t0;
             }
             // copies still in flight end before the CTA does (whoever gave up)
             const unsigned long long t0 = now_ns();
@@ -591,7 +655,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <typename T, int D>
+template <typename T, int D, bool SPLIT>
 cudaError_t launch_tiles(const AttendArgs& p, cudaStream_t s) {
     constexpr int bytes = TilesCfg<D>::kSmem;
     TilesArgs ta;
@@ -610,23 +674,27 @@ cudaError_t launch_tiles(const AttendArgs& p, cudaStream_t s) {
         std::lock_guard<std::mutex> lock(mu);
         if (dev < 0 || dev >= 64 || !ready[dev]) {
             cudaFuncAttributes at;
-            if ((e = cudaFuncGetAttributes(&at, attend_tiles_kernel<T, D>)) != cudaSuccess) return e;
+            if ((e = cudaFuncGetAttributes(&at, attend_tiles_kernel<T, D, SPLIT>)) != cudaSuccess) return e;
             if (at.numRegs * kTThreads < 256 * kSoftRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
-            e = cudaFuncSetAttribute(attend_tiles_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            e = cudaFuncSetAttribute(attend_tiles_kernel<T, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
             if (e != cudaSuccess) return e;
             if (dev >= 0 && dev < 64) ready[dev] = true;
         }
     }
-    attend_tiles_kernel<T, D><<<p.ctas, kTThreads, bytes, s>>>(ta, km, vm);
+    attend_tiles_kernel<T, D, SPLIT><<<p.ctas, kTThreads, bytes, s>>>(ta, km, vm);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t tiles_of(int dim, int rm, const AttendArgs& p, cudaStream_t s) {
+    if (rm == 128) return dim == 64 ? launch_tiles<T, 64, true>(p, s) : launch_tiles<T, 128, true>(p, s);
+    return dim == 64 ? launch_tiles<T, 64, false>(p, s) : launch_tiles<T, 128, false>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_tiles(int dtype, int dim, const AttendArgs& p, cudaStream_t s) {
-    if (dtype == SV_BF16)
-        return dim == 64 ? launch_tiles<__nv_bfloat16, 64>(p, s) : launch_tiles<__nv_bfloat16, 128>(p, s);
-    return dim == 64 ? launch_tiles<__half, 64>(p, s) : launch_tiles<__half, 128>(p, s);
+cudaError_t launch_attend_tiles(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s) {
+    return dtype == SV_BF16 ? tiles_of<__nv_bfloat16>(dim, rm, p, s) : tiles_of<__half>(dim, rm, p, s);
 }
 
 }  // namespace sv
