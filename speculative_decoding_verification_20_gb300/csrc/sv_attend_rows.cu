@@ -16,6 +16,8 @@
 //
 // Scores and outputs use the warp-wide 16x8x16 matrix instructions: 16 rows of them are
 // what a decode step fills.
+#include <atomic>
+
 #include "sv_async.cuh"
 #include "sv_attend.cuh"
 
@@ -415,10 +417,10 @@ __global__ void __launch_bounds__(kAThreads, 1)
     }
 }
 
-// A unit that was cut: the partial results of the CTAs that worked on it, in order.  Block
-// c looks at the unit in which CTA c began; the first CTA that began inside a unit joins it.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinCols = 16;
+// A unit that was cut: the partial results of the CTAs that worked on it, joined in order.
+// Blocks (c, ...) look at the unit in which CTA c began; the first CTA that began inside a
+// unit joins it.  Of a long axis there are many partial results to a row: PG warps take
+// every PG-th each, and their sums meet in shared memory.
 __device__ __forceinline__ bool join_unit(const AttendArgs& p, Cut& k) {
     grid_dependency_wait();
     k = p.cut[blockIdx.x];
@@ -426,11 +428,11 @@ __device__ __forceinline__ bool join_unit(const AttendArgs& p, Cut& k) {
     if (k.ctas == 0 || c == 0) return false;
     return k.per * c + min(c, (long long)k.more) != k.base && k.per * (c - 1) + min(c - 1, (long long)k.more) <= k.base;
 }
-// calls f(place) for the unit's partial results in order
-template <typename F>
-__device__ __forceinline__ void join_each(const Cut& k, F f) {
+// calls f(place) for the unit's partial results g, g + PG, ...
+template <int PG, typename F>
+__device__ __forceinline__ void join_each(const Cut& k, int g, F f) {
 #pragma unroll 4
-    for (int c = blockIdx.x - 1; c < k.ctas; ++c) {
+    for (int c = (int)blockIdx.x - 1 + g; c < k.ctas; c += PG) {
         const long long from = k.per * c + min(c, k.more);  // a CTA's first tile
         if (from >= k.end) break;
         f((int64_t)(2 * c + (from >= k.base ? 0 : 1)));
@@ -451,21 +453,23 @@ __device__ __forceinline__ void join_add(float& top, float& sum, float (&acc)[N]
     top = now;
 }
 
-// results by rows: a warp a row
+// results by rows: a warp has all columns of a row; a block kJoinRows rows
+constexpr int kJoinRows = 4, kJoinGroups = 4;
 template <typename T, int D, int RM>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ AttendArgs p) {
+__global__ void __launch_bounds__(32 * kJoinRows * kJoinGroups)
+    attend_join_kernel(const __grid_constant__ AttendArgs p) {
     constexpr int PER = D / 32;  // columns a lane
+    __shared__ float s_x[kJoinRows][kJoinGroups][D];
+    __shared__ float2 s_ml[kJoinRows][kJoinGroups];
     Cut k;
     if (!join_unit(p, k)) return;
-    const int lane = threadIdx.x & 31;
-    const int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    if (r >= k.n * p.group - k.rt * RM) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = warp / kJoinGroups, g = warp % kJoinGroups, r = blockIdx.y * kJoinRows + j;
+    const bool live = r < k.n * p.group - k.rt * RM;
     float top = -INFINITY, l = 0.0f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
-    join_each(k, [&](int64_t place) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
-        const float* src = p.part_o + (place * RM + r) * D + lane * PER;
+    auto add = [&](const float2 ml, const float* src) {
         float x[PER];
         if constexpr (PER == 4) {
             const float4 y = *reinterpret_cast<const float4*>(src);
@@ -475,7 +479,19 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
             x[0] = y.x, x[1] = y.y;
         }
         join_add(top, l, acc, ml.x, ml.y, x);
-    });
+    };
+    if (live)
+        join_each<kJoinGroups>(k, g, [&](int64_t place) {
+            add(*reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2),
+                p.part_o + (place * RM + r) * D + lane * PER);
+        });
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s_x[j][g][lane * PER + i] = acc[i];
+    if (lane == 0) s_ml[j][g] = make_float2(top, l);
+    __syncthreads();
+    if (g != 0 || !live) return;
+#pragma unroll
+    for (int o = 1; o < kJoinGroups; ++o) add(s_ml[j][o], &s_x[j][o][lane * PER]);
     const float inv = 1.0f / l;
     uint32_t w[PER / 2];
 #pragma unroll
@@ -487,23 +503,53 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_
         *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
-// results by columns: a thread has kJoinCols columns of a row, a warp 32 rows
+// results by columns: a warp has kJoinCols columns of 32 rows; a block CG such sets
+constexpr int kJoinCols = 16;
+template <int D, int RM>
+struct JoinCfg {
+    static constexpr int PG = RM == 128 ? 4 : 1;  // units of 128 rows have long axes
+    static constexpr int CG = PG == 4 ? 2 : D / kJoinCols;
+    static constexpr int kThreads = 32 * PG * CG;
+    static constexpr int kBlocks = (RM / 32) * (D / (CG * kJoinCols));
+};
 template <typename T, int D, int RM>
-__global__ void __launch_bounds__(RM) attend_join_columns_kernel(const __grid_constant__ AttendArgs p) {
+__global__ void __launch_bounds__(JoinCfg<D, RM>::kThreads)
+    attend_join_columns_kernel(const __grid_constant__ AttendArgs p) {
+    using C = JoinCfg<D, RM>;
+    __shared__ float s_x[C::PG][C::CG][kJoinCols][32];
+    __shared__ float2 s_ml[C::PG][C::CG][32];
     Cut k;
     if (!join_unit(p, k)) return;
-    const int r = threadIdx.x, c0 = blockIdx.y * kJoinCols;
-    if (r >= k.n * p.group - k.rt * RM) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = warp % C::PG, cg = warp / C::PG;
+    const int r = blockIdx.y % (RM / 32) * 32 + lane;
+    const int c0 = (blockIdx.y / (RM / 32) * C::CG + cg) * kJoinCols;
+    const bool live = r < k.n * p.group - k.rt * RM;
     float top = -INFINITY, l = 0.0f, acc[kJoinCols];
 #pragma unroll
     for (int i = 0; i < kJoinCols; ++i) acc[i] = 0.0f;
-    join_each(k, [&](int64_t place) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
-        float x[kJoinCols];
+    if (live)
+        join_each<C::PG>(k, g, [&](int64_t place) {
+            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (place * RM + r) * 2);
+            float x[kJoinCols];
 #pragma unroll
-        for (int i = 0; i < kJoinCols; ++i) x[i] = p.part_o[(place * D + c0 + i) * RM + r];
-        join_add(top, l, acc, ml.x, ml.y, x);
-    });
+            for (int i = 0; i < kJoinCols; ++i) x[i] = p.part_o[(place * D + c0 + i) * RM + r];
+            join_add(top, l, acc, ml.x, ml.y, x);
+        });
+    if constexpr (C::PG > 1) {
+#pragma unroll
+        for (int i = 0; i < kJoinCols; ++i) s_x[g][cg][i][lane] = acc[i];
+        s_ml[g][cg][lane] = make_float2(top, l);
+        __syncthreads();
+        if (g != 0) return;
+#pragma unroll
+        for (int o = 1; o < C::PG; ++o) {
+            float x[kJoinCols];
+#pragma unroll
+            for (int i = 0; i < kJoinCols; ++i) x[i] = s_x[o][cg][i][lane];
+            join_add(top, l, acc, s_ml[o][cg][lane].x, s_ml[o][cg][lane].y, x);
+        }
+    }
+    if (!live) return;
     const float inv = 1.0f / l;
     uint32_t w[kJoinCols / 2];
 #pragma unroll
@@ -518,9 +564,15 @@ cudaError_t launch_rows(const AttendArgs& p, cudaStream_t s) {
     constexpr int bytes = RowsCfg<D, MT>::kSmem;
     CUtensorMap km, vm;
     if (!encode_pages(&km, &vm, p, kBlk, D / 64)) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<T, D, MT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> ready{0};  // devices whose kernel has its shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load() >> dev & 1)) {
+        e = cudaFuncSetAttribute(attend_rows_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev);
+    }
     attend_rows_kernel<T, D, MT><<<p.ctas, kAThreads, bytes, s>>>(p, km, vm);
     return cudaGetLastError();
 }
@@ -534,12 +586,12 @@ cudaError_t launch_join(const AttendArgs& p, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if constexpr (RM >= 128) {
-        cfg.blockDim = dim3(RM);
-        cfg.gridDim = dim3((unsigned)p.ctas, D / kJoinCols);
+        cfg.blockDim = dim3(JoinCfg<D, RM>::kThreads);
+        cfg.gridDim = dim3((unsigned)p.ctas, JoinCfg<D, RM>::kBlocks);
         return cudaLaunchKernelEx(&cfg, attend_join_columns_kernel<T, D, RM>, p);
     } else {
-        cfg.blockDim = dim3(kJoinThreads);
-        cfg.gridDim = dim3((unsigned)p.ctas, RM / (kJoinThreads / 32));
+        cfg.blockDim = dim3(32 * kJoinRows * kJoinGroups);
+        cfg.gridDim = dim3((unsigned)p.ctas, RM / kJoinRows);
         return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, RM>, p);
     }
 }

@@ -22,7 +22,7 @@
 //
 // Every wait has a limit.  When one runs out, the CTA writes NaN for what is left of its
 // part, sets SV_ROW_INTERNAL, lets its copies and products finish (with a limit) and ends.
-#include <mutex>
+#include <atomic>
 #include <type_traits>
 
 #include "sv_async.cuh"
@@ -665,21 +665,17 @@ cudaError_t launch_tiles(const AttendArgs& p, cudaStream_t s) {
     CUtensorMap km, vm;
     if (!encode_pages(&km, &vm, p, ta.box, 1)) return cudaErrorInvalidValue;
     // once a device: room in shared memory, and proof that the register split fits the launch
-    static std::mutex mu;
-    static bool ready[64];
+    static std::atomic<uint64_t> ready{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (dev < 0 || dev >= 64 || !ready[dev]) {
-            cudaFuncAttributes at;
-            if ((e = cudaFuncGetAttributes(&at, attend_tiles_kernel<T, D, SPLIT>)) != cudaSuccess) return e;
-            if (at.numRegs * kTThreads < 256 * kSoftRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
-            e = cudaFuncSetAttribute(attend_tiles_kernel<T, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-            if (e != cudaSuccess) return e;
-            if (dev >= 0 && dev < 64) ready[dev] = true;
-        }
+    if (dev >= 64 || !(ready.load() >> dev & 1)) {
+        cudaFuncAttributes at;
+        if ((e = cudaFuncGetAttributes(&at, attend_tiles_kernel<T, D, SPLIT>)) != cudaSuccess) return e;
+        if (at.numRegs * kTThreads < 256 * kSoftRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(attend_tiles_kernel<T, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev);
     }
     attend_tiles_kernel<T, D, SPLIT><<<p.ctas, kTThreads, bytes, s>>>(ta, km, vm);
     return cudaGetLastError();

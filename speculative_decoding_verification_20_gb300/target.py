@@ -42,10 +42,25 @@ _ROTATE = struct.Struct("<Q4Q6q12qQ3q" + _CACHE + "Q")
 _ATTENTION = struct.Struct("<Q2Q6q6qd2q" + _CACHE + "QqQQ")
 
 
-def _api():
-    from . import _check, load_library
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_lib = None
 
-    return load_library(), _check
+
+def _library():
+    global _lib
+    if _lib is None:
+        from . import load_library
+
+        _lib = load_library()
+    return _lib
+
+
+def _check(status: int) -> None:
+    if status:
+        from . import SpecVerifyError, strerror
+
+        raise SpecVerifyError(status, strerror(status))
 
 
 def _p(t: Optional[torch.Tensor]) -> int:
@@ -56,18 +71,18 @@ def _vec(x, B: int, dtype: torch.dtype, device, name: str) -> Optional[torch.Ten
     """A per-sequence parameter as a contiguous device vector of B entries."""
     if x is None:
         return None
-    if torch.is_tensor(x) and x.dtype == dtype and x.device == device and x.dim() == 1 and x.numel() == B and \
-            x.is_contiguous():
+    if isinstance(x, torch.Tensor) and x.dtype == dtype and x.device == device and x.dim() == 1 and \
+            x.shape[0] == B and x.is_contiguous():
         return x
     from . import _dev_vec
 
     return _dev_vec(x, B, dtype, device, name)
 
 
-def _table(x: torch.Tensor, shape, device, name: str) -> torch.Tensor:
-    """An int32 device matrix whose rows are contiguous."""
-    if not torch.is_tensor(x) or x.dim() != 2 or x.shape[0] != shape[0] or x.shape[1] < shape[1]:
-        raise ValueError(f"{name} must be [{shape[0]}, >= {shape[1]}]")
+def _table(x: torch.Tensor, rows: int, cols: int, device, name: str) -> torch.Tensor:
+    """An int32 device matrix of so many rows and at least so many columns, rows contiguous."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[0] != rows or x.shape[1] < cols:
+        raise ValueError(f"{name} must be [{rows}, >= {cols}]")
     if x.dtype != torch.int32 or x.device != device:
         x = x.to(device=device, dtype=torch.int32)
     return x if x.stride(1) == 1 or x.shape[1] == 1 else x.contiguous()
@@ -80,36 +95,36 @@ def _status(row_status, B, device):
     return row_status
 
 
-class _On:
-    """Device and stream of one call: work and allocations go to ``stream`` when it is given, and the
-    tensors of the call are kept for it."""
+def _elsewhere(device: torch.device, stream, fn, args, kwargs):
+    """The call on another stream than torch's current one (what it allocates belongs to that stream, what it is
+    given is kept for it), or on another device than the current one."""
+    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(device):
+        if stream is not None and torch.cuda.current_device() != device.index:
+            raise ValueError(f"the stream is not one of {device}")
+        res = fn(*args, **kwargs)
+        if stream is not None:
+            for t in (*args, *kwargs.values()):
+                for u in t if isinstance(t, (tuple, list)) else \
+                        (t.k, t.v) if isinstance(t, PagedCache) else \
+                        (t.seen, t.counts) if isinstance(t, TokenHistory) else (t,):
+                    if isinstance(u, torch.Tensor) and u.is_cuda:
+                        u.record_stream(stream)
+    return res
 
-    __slots__ = ("device", "stream", "ctx")
 
-    def __init__(self, device: torch.device, stream):
-        self.device, self.stream, self.ctx = device, stream, None
+_workspaces: dict = {}
 
-    def __enter__(self):
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-            self.ctx.__enter__()
-        elif torch.cuda.current_device() != self.device.index:
-            self.ctx = torch.cuda.device(self.device)
-            self.ctx.__enter__()
-        return self
 
-    def handle(self) -> int:
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
-
-    def keep(self, *tensors) -> None:
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _workspace(nbytes: int, device: torch.device, raw: int) -> torch.Tensor:
+    """Scratch of the calls on one stream, which follow one another; a call that is captured into a graph gets its own
+    from the graph's memory, since replays may overlap with the stream's later calls."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    key = (device.index, raw)
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws
 
 
 # ---------------------------------------------------------------------------
@@ -134,23 +149,23 @@ class TokenHistory:
         if not self.counts.is_cuda:
             raise ValueError("the history must be on a CUDA device")
         dev = self.counts.device
-        with _On(dev, stream) as on:
-            if not torch.is_tensor(tokens):
-                tokens = torch.as_tensor(tokens, dtype=torch.int32)
-            if tokens.dim() != 2:
-                raise ValueError("tokens must be [B, L]")
-            B, L = tokens.shape
-            tokens = _table(tokens, (B, L), dev, "tokens")
-            slot_of = _vec(slots, B, torch.int32, dev, "slots")
-            if slot_of is None and B > self.slots:
-                raise ValueError(f"{B} rows but only {self.slots} slots")
-            pl = _vec(prompt_lens, B, torch.int32, dev, "prompt_lens")
-            tl = _vec(total_lens, B, torch.int32, dev, "total_lens")
-            lib, check = _api()
-            check(lib.spec_verify_history_add(_HISTORY.pack(
-                _HISTORY.size, _p(self.seen), _p(self.counts), self.slots, self.words, self.vocab,
-                _p(slot_of), _p(tokens), B, L, tokens.stride(0), _p(pl), _p(tl), int(clear)), on.handle()))
-            on.keep(tokens, slot_of, pl, tl, self.seen, self.counts)
+        if stream is not None or _current_device() != dev.index:
+            return _elsewhere(dev, stream, TokenHistory._call, (self, tokens, prompt_lens, total_lens, slots, clear, None),
+                              {})
+        if not isinstance(tokens, torch.Tensor):
+            tokens = torch.as_tensor(tokens, dtype=torch.int32)
+        if tokens.dim() != 2:
+            raise ValueError("tokens must be [B, L]")
+        B, L = tokens.shape
+        tokens = _table(tokens, B, L, dev, "tokens")
+        slot_of = _vec(slots, B, torch.int32, dev, "slots")
+        if slot_of is None and B > self.slots:
+            raise ValueError(f"{B} rows but only {self.slots} slots")
+        pl = _vec(prompt_lens, B, torch.int32, dev, "prompt_lens")
+        tl = _vec(total_lens, B, torch.int32, dev, "total_lens")
+        _check(_library().spec_verify_history_add(_HISTORY.pack(
+            _HISTORY.size, _p(self.seen), _p(self.counts), self.slots, self.words, self.vocab,
+            _p(slot_of), _p(tokens), B, L, tokens.stride(0), _p(pl), _p(tl), int(clear)), _raw_stream(dev.index)))
 
     def load(self, tokens, prompt_lens=None, total_lens=None, slots=None, *, stream=None) -> None:
         """New sequences take their slots: of row b of tokens [B, L] the first prompt_lens[b] (default: none) are
@@ -175,63 +190,68 @@ def process_logits(logits: torch.Tensor, *, history: Optional[TokenHistory] = No
     mask: int32 [B, N, W] or [B, W], W >= ceil(V / 32), 1 = allowed: bit t % 32 of word t // 32 is token t's.
     out: where to write (may be ``logits``); by default a new tensor.  Returns it.
     """
-    if not torch.is_tensor(logits) or not logits.is_cuda or logits.dim() != 3:
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3:
         raise ValueError("logits must be a CUDA tensor [B, N, V]")
+    dev = logits.device
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(dev, stream, process_logits, (logits,), dict(
+            history=history, slots=slots, draft_tokens=draft_tokens, repetition=repetition, frequency=frequency,
+            presence=presence, bias=bias, mask=mask, out=out, row_status=row_status))
     code = _DTYPE.get(logits.dtype)
     if code not in (0, 1):
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     B, N, V = logits.shape
-    dev = logits.device
-    with _On(dev, stream) as on:
-        x = logits if logits.stride(2) == 1 or V == 1 else logits.contiguous()
-        if out is None:
-            out = torch.empty((B, N, V), dtype=logits.dtype, device=dev)
-        elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev or \
-                (V > 1 and out.stride(2) != 1):
-            raise ValueError("out must have the logits' shape, type and device, and a contiguous vocabulary")
-        seen = counts = slot_of = None
-        nslots = words = 0
-        if history is not None:
-            if history.vocab != V or history.counts.device != dev:
-                raise ValueError(f"the history is of {history.vocab} tokens on {history.counts.device}")
-            seen, counts = history.seen, history.counts
-            nslots, words = history.slots, history.words
-            slot_of = _vec(slots, B, torch.int32, dev, "slots")
-            if slot_of is None and B > nslots:
-                raise ValueError(f"{B} rows but only {nslots} slots")
-        toks = None if draft_tokens is None or N == 1 else _table(draft_tokens, (B, N - 1), dev, "draft_tokens")
-        rep = _vec(repetition, B, torch.float32, dev, "repetition")
-        freq = _vec(frequency, B, torch.float32, dev, "frequency")
-        pres = _vec(presence, B, torch.float32, dev, "presence")
-        ids = vals = offs = None
-        if bias is not None:
-            ids, vals, offs = bias
-            ids, vals = (_vec(ids, len(ids), torch.int32, dev, "bias ids"),
-                         _vec(vals, len(vals), torch.float32, dev, "bias values"))
-            offs = _vec(offs, B + 1, torch.int32, dev, "bias offsets")
-            if ids.numel() != vals.numel():
-                raise ValueError("bias ids and values differ in length")
-            if ids.numel() == 0:
-                ids = vals = offs = None
-        msb = msn = 0
-        if mask is not None:
-            if mask.dtype != torch.int32 or mask.device != dev:
-                raise ValueError("mask must be an int32 CUDA tensor")
-            if mask.dim() not in (2, 3) or mask.shape[0] != B or (mask.dim() == 3 and mask.shape[1] != N) or \
-                    32 * mask.shape[-1] < V:
-                raise ValueError("mask must be [B, N, W] or [B, W] with W >= ceil(V / 32)")
-            if mask.stride(-1) != 1 and mask.shape[-1] > 1:
-                mask = mask.contiguous()
-            msb, msn = mask.stride(0), (mask.stride(1) if mask.dim() == 3 else 0)
-        st = _status(row_status, B, dev)
-        lib, check = _api()
-        check(lib.spec_verify_process_logits(_LOGITS.pack(
-            _LOGITS.size, _p(x), _p(out), code, B, N, V, x.stride(0), x.stride(1), out.stride(0), out.stride(1),
-            _p(seen), _p(counts), nslots, words, _p(slot_of),
-            _p(toks), 0 if toks is None else toks.stride(0), 0 if toks is None else toks.shape[1],
-            _p(rep), _p(freq), _p(pres), _p(ids), _p(vals), _p(offs), 0 if ids is None else ids.numel(),
-            _p(mask), msb, msn, _p(st)), on.handle()))
-        on.keep(x, out, seen, counts, slot_of, toks, rep, freq, pres, ids, vals, offs, mask, st)
+    x = logits if logits.stride(2) == 1 or V == 1 else logits.contiguous()
+    if out is None:
+        out = torch.empty((B, N, V), dtype=logits.dtype, device=dev)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev or (V > 1 and out.stride(2) != 1):
+        raise ValueError("out must have the logits' shape, type and device, and a contiguous vocabulary")
+    seen = counts = slot_of = 0
+    nslots = words = 0
+    if history is not None:
+        if history.vocab != V or history.counts.device != dev:
+            raise ValueError(f"the history is of {history.vocab} tokens on {history.counts.device}")
+        seen, counts = history.seen.data_ptr(), history.counts.data_ptr()
+        nslots, words = history.slots, history.words
+        slots = _vec(slots, B, torch.int32, dev, "slots")
+        if slots is None and B > nslots:
+            raise ValueError(f"{B} rows but only {nslots} slots")
+        slot_of = _p(slots)
+    toks = tstride = tlen = 0
+    if draft_tokens is not None and N > 1:
+        draft_tokens = _table(draft_tokens, B, N - 1, dev, "draft_tokens")
+        toks, tstride, tlen = draft_tokens.data_ptr(), draft_tokens.stride(0), draft_tokens.shape[1]
+    rep = _vec(repetition, B, torch.float32, dev, "repetition")
+    freq = _vec(frequency, B, torch.float32, dev, "frequency")
+    pres = _vec(presence, B, torch.float32, dev, "presence")
+    ids = vals = offs = None
+    nbias = 0
+    if bias is not None:
+        ids, vals, offs = bias
+        nbias = len(ids)
+        ids = _vec(ids, nbias, torch.int32, dev, "bias ids")
+        vals = _vec(vals, len(vals), torch.float32, dev, "bias values")
+        offs = _vec(offs, B + 1, torch.int32, dev, "bias offsets")
+        if vals.shape[0] != nbias:
+            raise ValueError("bias ids and values differ in length")
+        if nbias == 0:
+            ids = vals = offs = None
+    msb = msn = 0
+    if mask is not None:
+        if mask.dtype != torch.int32 or mask.device != dev:
+            raise ValueError("mask must be an int32 CUDA tensor")
+        dims = mask.dim()
+        if dims not in (2, 3) or mask.shape[0] != B or (dims == 3 and mask.shape[1] != N) or 32 * mask.shape[-1] < V:
+            raise ValueError("mask must be [B, N, W] or [B, W] with W >= ceil(V / 32)")
+        if mask.stride(-1) != 1 and mask.shape[-1] > 1:
+            mask = mask.contiguous()
+        msb, msn = mask.stride(0), (mask.stride(1) if dims == 3 else 0)
+    _status(row_status, B, dev)
+    xs, os = x.stride(), out.stride()
+    _check(_library().spec_verify_process_logits(_LOGITS.pack(
+        _LOGITS.size, x.data_ptr(), out.data_ptr(), code, B, N, V, xs[0], xs[1], os[0], os[1], seen, counts, nslots, words,
+        slot_of, toks, tstride, tlen, _p(rep), _p(freq), _p(pres), _p(ids), _p(vals), _p(offs), nbias, _p(mask), msb, msn,
+        _p(row_status)), _raw_stream(dev.index)))
     return out
 
 
@@ -271,8 +291,6 @@ class PagedCache:
         self.dtype, self.device = k.dtype, k.device
         self._fields = (k.data_ptr(), v.data_ptr(), self.pages, self.page_size, *k.stride()[:3], *v.stride()[:3])
 
-    def _pack(self, page_table, lens, new):
-        return self._fields + (_p(page_table), page_table.stride(0), page_table.shape[1], _p(lens), _p(new))
 
 
 def rotary_table(length: int, rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] = None,
@@ -323,10 +341,10 @@ def rotary_table(length: int, rotary_dim: int, base: float = 10000.0, scaling: O
     return torch.stack(((angle.cos() * mscale).float(), (angle.sin() * mscale).float()), 1)
 
 
-def _rows(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
+def _rows(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
     """[B, N, heads, dim] with contiguous, 16-byte aligned heads; a copy if it has not."""
-    if not torch.is_tensor(t) or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape) if torch.is_tensor(t) else type(t)}")
+    if not isinstance(t, torch.Tensor) or t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
     if t.dtype != dtype or t.device != device:
         raise TypeError(f"{name} must be {dtype} on {device} like the cache, got {t.dtype} on {t.device}")
     s = t.stride()
@@ -337,13 +355,11 @@ def _rows(t: torch.Tensor, shape, dtype, device, name: str) -> torch.Tensor:
     return t
 
 
-def _out_rows(out, q, name="out"):
-    if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+def _out_rows(out, shape, dtype, device):
     s = out.stride()
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or s[3] != 1 or \
+    if out.shape != shape or out.dtype != dtype or out.device != device or s[3] != 1 or \
             (s[0] | s[1] | s[2]) & 7 or out.data_ptr() & 15:
-        raise ValueError(f"{name} must have q's shape, type and device, with contiguous, 16-byte aligned heads")
+        raise ValueError("out must have q's shape, type and device, with contiguous, 16-byte aligned heads")
     return out
 
 
@@ -358,39 +374,42 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
     (a multiple of 16) may be less than dim.  Pairs are (j, j + rotary_dim / 2), or (2j, 2j + 1) with
     interleaved.  Returns the rotated q (``out``, which may be q; rows past num_new are zeros).
     """
-    if not torch.is_tensor(q) or not q.is_cuda or q.dim() != 4:
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, N, q_heads, dim]")
-    B, N, Hq, D = q.shape
-    dev = q.device
+    dev, dtype, shape = q.device, cache.dtype, q.shape
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(dev, stream, rotate_append, (q, k, v, table, cache, page_table, cache_lens, num_new), dict(
+            interleaved=interleaved, out=out, row_status=row_status))
+    B, N, Hq, D = shape
     if D != cache.head_dim or dev != cache.device:
         raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
     if table.dim() != 3 or table.shape[1] != 2 or table.dtype != torch.float32 or table.device != dev or \
             not table.is_contiguous():
         raise ValueError("table must be a contiguous float32 CUDA tensor [length, 2, rotary_dim / 2]")
-    rot = 2 * table.shape[2]
-    if rot % 16 or rot > D or rot < 16:
-        raise ValueError(f"rotary_dim must be a multiple of 16 and at most {D}, got {rot}")
-    with _On(dev, stream) as on:
-        x = _rows(q, (B, N, Hq, D), cache.dtype, dev, "q")
-        k = _rows(k, (B, N, cache.kv_heads, D), cache.dtype, dev, "k")
-        v = _rows(v, (B, N, cache.kv_heads, D), cache.dtype, dev, "v")
-        o = _out_rows(out, q)
-        pt = _table(page_table, (B, 1), dev, "page_table")
-        lens = _vec(cache_lens, B, torch.int32, dev, "cache_lens")
-        new = _vec(num_new, B, torch.int32, dev, "num_new")
-        st = _status(row_status, B, dev)
-        lib, check = _api()
-        check(lib.spec_verify_rotate_append(_ROTATE.pack(
-            _ROTATE.size, _p(x), _p(o), _p(k), _p(v), _DTYPE[cache.dtype], B, N, Hq, cache.kv_heads, D,
-            *x.stride()[:3], *o.stride()[:3], *k.stride()[:3], *v.stride()[:3], _p(table), table.shape[0], rot,
-            int(bool(interleaved)), *cache._pack(pt, lens, new), _p(st)), on.handle()))
-        on.keep(x, o, k, v, table, cache.k, cache.v, pt, lens, new, st)
+    tlen, _, half = table.shape
+    if half % 8 or 2 * half > D or half < 8:
+        raise ValueError(f"rotary_dim must be a multiple of 16 and at most {D}, got {2 * half}")
+    kv = (B, N, cache.kv_heads, D)
+    x = _rows(q, "q", shape, dtype, dev)
+    k = _rows(k, "k", kv, dtype, dev)
+    v = _rows(v, "v", kv, dtype, dev)
+    o = torch.empty(shape, dtype=dtype, device=dev) if out is None else _out_rows(out, shape, dtype, dev)
+    pt = _table(page_table, B, 1, dev, "page_table")
+    lens = _vec(cache_lens, B, torch.int32, dev, "cache_lens")
+    new = _vec(num_new, B, torch.int32, dev, "num_new")
+    _status(row_status, B, dev)
+    xs, os, ks, vs = x.stride(), o.stride(), k.stride(), v.stride()
+    _check(_library().spec_verify_rotate_append(_ROTATE.pack(
+        _ROTATE.size, x.data_ptr(), o.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPE[dtype], B, N, Hq, cache.kv_heads, D,
+        xs[0], xs[1], xs[2], os[0], os[1], os[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], table.data_ptr(), tlen,
+        2 * half, 1 if interleaved else 0, *cache._fields, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(),
+        _p(new), _p(row_status)), _raw_stream(dev.index)))
     return o
 
 
 def attention_workspace_size(B: int, N: int, q_heads: int, kv_heads: int, dim: int) -> int:
     """Bytes of workspace that one paged_attention call of this shape needs (0 for a shape it does not take)."""
-    return int(_api()[0].spec_verify_attention_workspace_size(B, N, q_heads, kv_heads, dim))
+    return int(_library().spec_verify_attention_workspace_size(B, N, q_heads, kv_heads, dim))
 
 
 def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, cache_lens: torch.Tensor,
@@ -403,32 +422,37 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     Token i of sequence b sees the positions up to cache_lens[b] + i, with window > 0 only the last ``window``
     of them.  scale: default 1 / sqrt(dim).  max_context: the host's upper bound of cache_lens + num_new
     (default: the page table's width); it only sizes the launch.  Rows past num_new are zeros.
-    workspace: uint8 of attention_workspace_size() bytes (default: from torch's allocator, per call).
+    workspace: uint8 of attention_workspace_size() bytes; calls on one must not overlap (default: one kept for each
+    stream, or the graph's own memory while a graph is captured).
     """
-    if not torch.is_tensor(q) or not q.is_cuda or q.dim() != 4:
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, N, q_heads, dim]")
-    B, N, Hq, D = q.shape
-    dev = q.device
+    dev, dtype, shape = q.device, cache.dtype, q.shape
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(dev, stream, paged_attention, (q, cache, page_table, cache_lens, num_new), dict(
+            scale=scale, window=window, max_context=max_context, out=out, row_status=row_status, workspace=workspace,
+            wait_limit_ns=wait_limit_ns))
+    B, N, Hq, D = shape
+    Hkv = cache.kv_heads
     if D != cache.head_dim or dev != cache.device:
         raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
-    if Hq % cache.kv_heads:
-        raise ValueError(f"{Hq} query heads cannot share {cache.kv_heads} cache heads evenly")
+    if Hq % Hkv:
+        raise ValueError(f"{Hq} query heads cannot share {Hkv} cache heads evenly")
     if window < 0:
         raise ValueError("window must be 0 (none) or positive")
-    lib, check = _api()
-    with _On(dev, stream) as on:
-        x = _rows(q, (B, N, Hq, D), cache.dtype, dev, "q")
-        o = _out_rows(out, q)
-        pt = _table(page_table, (B, 1), dev, "page_table")
-        lens = _vec(cache_lens, B, torch.int32, dev, "cache_lens")
-        new = _vec(num_new, B, torch.int32, dev, "num_new")
-        st = _status(row_status, B, dev)
-        if workspace is None:
-            workspace = torch.empty(lib.spec_verify_attention_workspace_size(B, N, Hq, cache.kv_heads, D),
-                                    dtype=torch.uint8, device=dev)
-        check(lib.spec_verify_attention(_ATTENTION.pack(
-            _ATTENTION.size, _p(x), _p(o), _DTYPE[cache.dtype], B, N, Hq, cache.kv_heads, D, *x.stride()[:3],
-            *o.stride()[:3], 1.0 / math.sqrt(D) if scale is None else float(scale), window, max_context or 0,
-            *cache._pack(pt, lens, new), _p(workspace), workspace.numel(), _p(st), int(wait_limit_ns)), on.handle()))
-        on.keep(x, o, cache.k, cache.v, pt, lens, new, st, workspace)
+    x = _rows(q, "q", shape, dtype, dev)
+    o = torch.empty(shape, dtype=dtype, device=dev) if out is None else _out_rows(out, shape, dtype, dev)
+    pt = _table(page_table, B, 1, dev, "page_table")
+    lens = _vec(cache_lens, B, torch.int32, dev, "cache_lens")
+    new = _vec(num_new, B, torch.int32, dev, "num_new")
+    _status(row_status, B, dev)
+    lib, raw = _library(), _raw_stream(dev.index)
+    if workspace is None:
+        workspace = _workspace(lib.spec_verify_attention_workspace_size(B, N, Hq, Hkv, D), dev, raw)
+    xs, os = x.stride(), o.stride()
+    _check(lib.spec_verify_attention(_ATTENTION.pack(
+        _ATTENTION.size, x.data_ptr(), o.data_ptr(), _DTYPE[dtype], B, N, Hq, Hkv, D, xs[0], xs[1], xs[2],
+        os[0], os[1], os[2], 1.0 / math.sqrt(D) if scale is None else float(scale), window, max_context or 0,
+        *cache._fields, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(), _p(new), workspace.data_ptr(),
+        workspace.numel(), _p(row_status), wait_limit_ns), raw))
     return o
