@@ -12,6 +12,8 @@
 
 #include <cuda.h>
 
+#include <utility>
+
 #include "sv_internal.cuh"
 #include "sv_paged.cuh"
 
@@ -99,82 +101,120 @@ __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
     __shared__ long long s_warp[NT / 32];
     __shared__ long long s_before;
     __shared__ int s_seq;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = (int)p.a.B;
-    // key tiles of one head of sequence b0 + t: by a thread alone, or where a sequence has
-    // many row tiles by a warp
-    auto head_tiles = [&](int b0) -> int {
-        if (p.max_row_tiles <= 4) {
-            if (b0 + t >= B) return 0;
-            const SeqLens s = seq_lens(p.a.cache, b0 + t, (int)p.a.N, p.capacity);
-            int c = 0;
-            for (int rt = row_tiles<RM>(p, s.n); rt-- > 0;) c += tile_count<RM>(p, s.past, s.n, rt);
-            return c;
-        }
-        __syncthreads();
-        for (int i = warp; i < NT && b0 + i < B; i += NT / 32) {
-            const SeqLens s = seq_lens(p.a.cache, b0 + i, (int)p.a.N, p.capacity);
-            int c = 0;
-            for (int rt = lane; rt < row_tiles<RM>(p, s.n); rt += 32) c += tile_count<RM>(p, s.past, s.n, rt);
-            c = warp_sum(c);
-            if (lane == 0) s_tiles[i] = c;
-        }
-        __syncthreads();
-        return b0 + t < B ? s_tiles[t] : 0;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = (int)p.a.B, c = blockIdx.x;
+    const int Hkv = (int)p.a.kv_heads;
+    // key tiles of one head of sequence b, by a thread alone or by a warp
+    auto alone = [&](int b) -> int {
+        const SeqLens s = seq_lens(p.a.cache, b, (int)p.a.N, p.capacity);
+        int n = 0;
+        for (int rt = row_tiles<RM>(p, s.n); rt-- > 0;) n += tile_count<RM>(p, s.past, s.n, rt);
+        return n;
     };
-    long long total = 0;
-    int mine = 0;
-    for (int b0 = 0; b0 < B; b0 += NT) {
-        mine = head_tiles(b0);
-        total += (long long)mine * p.a.kv_heads;
-    }
-    total = warp_sum(total);
-    if (lane == 0) s_warp[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) total += s_warp[w];
-    __syncthreads();
-    const int c = blockIdx.x, ctas = total < p.ctas ? (int)total : p.ctas;
-    part.todo = 0;
-    if (c >= ctas) {
-        if (t == 0) p.cut[c].ctas = 0;
-        return;
-    }
-    const long long per = total >> 31 ? total / ctas : (long long)((uint32_t)total / (uint32_t)ctas);
-    const int more = (int)(total - per * ctas);
-    const long long begin = per * c + min(c, more);
-    part.todo = (int)per + (c < more ? 1 : 0);
-    long long base = 0;
-    for (int b0 = 0; b0 < B; b0 += NT) {
-        if (B > NT) mine = head_tiles(b0);
-        const long long own = (long long)mine * p.a.kv_heads;
+    auto by_warp = [&](int b) -> int {
+        const SeqLens s = seq_lens(p.a.cache, b, (int)p.a.N, p.capacity);
+        int n = 0;
+        for (int rt = lane; rt < row_tiles<RM>(p, s.n); rt += 32) n += tile_count<RM>(p, s.past, s.n, rt);
+        return warp_sum(n);
+    };
+    auto scan = [&](long long own) -> long long {  // inclusive, over the warp
         long long x = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) s_warp[warp] = x;
-        __syncthreads();
-        long long before = base + x - own;
-        for (int w = 0; w < warp; ++w) before += s_warp[w];
-        if (begin >= before && begin < before + own) {
-            s_seq = b0 + t;
-            s_before = before;
-            s_tiles[0] = mine;
+        return x;
+    };
+    // the CTA's share of `total` tiles
+    long long begin = 0, per = 0;
+    int more = 0, ctas = 0;
+    auto share = [&](long long total) -> bool {
+        ctas = total < p.ctas ? (int)total : p.ctas;
+        part.todo = 0;
+        if (c >= ctas) {
+            if (t == 0) p.cut[c].ctas = 0;
+            return false;
         }
-        for (int w = 0; w < NT / 32; ++w) base += s_warp[w];
+        per = total >> 31 ? total / ctas : (long long)((uint32_t)total / (uint32_t)ctas);
+        more = (int)(total - per * ctas);
+        begin = per * c + min(c, more);
+        part.todo = (int)per + (c < more ? 1 : 0);
+        return true;
+    };
+    int seq = 0, per_head = 0;
+    long long before_seq = 0;
+    const bool many_rows = p.max_row_tiles > 4;
+    if (many_rows ? B * ((p.max_row_tiles + 31) / 32) <= 16 : B <= 32) {
+        // a small batch: every warp by itself, with no barrier
+        int mine = 0;
+        if (many_rows) {
+            for (int b = 0; b < B; ++b) {
+                const int n = by_warp(b);
+                if (lane == b) mine = n;
+            }
+        } else {
+            mine = alone(min(lane, B - 1));  // by every lane: the warp stays together for the scan
+            if (lane >= B) mine = 0;
+        }
+        __syncwarp();
+        const long long own = (long long)mine * Hkv, upto = scan(own);
+        if (!share(__shfl_sync(0xFFFFFFFFu, upto, 31))) return;
+        seq = __ffs(__ballot_sync(0xFFFFFFFFu, upto > begin)) - 1;
+        before_seq = __shfl_sync(0xFFFFFFFFu, upto - own, seq);
+        per_head = __shfl_sync(0xFFFFFFFFu, mine, seq);
+    } else {
+        auto head_tiles = [&](int b0) -> int {  // of sequence b0 + t
+            if (!many_rows) return b0 + t < B ? alone(b0 + t) : 0;
+            __syncthreads();
+            for (int i = warp; i < NT && b0 + i < B; i += NT / 32) {
+                const int n = by_warp(b0 + i);
+                if (lane == 0) s_tiles[i] = n;
+            }
+            __syncthreads();
+            return b0 + t < B ? s_tiles[t] : 0;
+        };
+        long long total = 0;
+        int mine = 0;
+        for (int b0 = 0; b0 < B; b0 += NT) {
+            mine = head_tiles(b0);
+            total += (long long)mine * Hkv;
+        }
+        total = warp_sum(total);
+        if (lane == 0) s_warp[warp] = total;
         __syncthreads();
-        if (base > begin) break;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) total += s_warp[w];
+        __syncthreads();
+        if (!share(total)) return;
+        long long base = 0;
+        for (int b0 = 0; b0 < B; b0 += NT) {
+            if (B > NT) mine = head_tiles(b0);
+            const long long own = (long long)mine * Hkv, x = scan(own);
+            if (lane == 31) s_warp[warp] = x;
+            __syncthreads();
+            long long before = base + x - own;
+            for (int w = 0; w < warp; ++w) before += s_warp[w];
+            if (begin >= before && begin < before + own) {
+                s_seq = b0 + t;
+                s_before = before;
+                s_tiles[0] = mine;
+            }
+            for (int w = 0; w < NT / 32; ++w) base += s_warp[w];
+            __syncthreads();
+            if (base > begin) break;
+        }
+        seq = s_seq;
+        before_seq = s_before;
+        per_head = s_tiles[0];
     }
     // then the head and the row tile
     Unit& u = part.u;
-    u.b = s_seq;
+    u.b = seq;
     const SeqLens s = seq_lens(p.a.cache, u.b, (int)p.a.N, p.capacity);
     u.past = s.past;
     u.n = s.n;
-    const int per_head = s_tiles[0];
-    const long long off = begin - s_before;
+    const long long off = begin - before_seq;
     u.h = off >> 31 ? (int)(off / per_head) : (int)((uint32_t)off / (uint32_t)per_head);
     int at = (int)(off - (long long)u.h * per_head);
     for (int rt0 = 0;; rt0 += 32) {  // (at < per_head: a row tile holds it)
@@ -261,6 +301,23 @@ __device__ __forceinline__ float fast_exp2(float x) {  // 2^x; 2^-inf = 0
 // tensor maps of the pages, a head's rows in parts of 64 elements (128 bytes, swizzled):
 // boxes of `box` rows and `parts` parts
 bool encode_pages(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, int parts);
+
+// Launch whose start may overlap with the end of the kernel before it on the stream; the
+// kernels wait for that one with grid_dependency_wait() before they read anything.
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 // the two kernels' launchers (RM rows a tile) and the join of the cut units
 cudaError_t launch_attend_rows(int dtype, int dim, int mt, const AttendArgs& p, cudaStream_t s);

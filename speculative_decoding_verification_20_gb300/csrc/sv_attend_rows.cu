@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
+    grid_dependency_wait();
     fill_idle_rows<T, kAThreads>(p);
     Part part;
     find_part<RM, kAThreads>(p, part, reinterpret_cast<int*>(s_join));
@@ -422,6 +423,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
 // unit joins it.  Of a long axis there are many partial results to a row: PG warps take
 // every PG-th each, and their sums meet in shared memory.
 __device__ __forceinline__ bool join_unit(const AttendArgs& p, Cut& k) {
+    grid_dependents_go();
     grid_dependency_wait();
     k = p.cut[blockIdx.x];
     const long long c = blockIdx.x;
@@ -573,26 +575,17 @@ cudaError_t launch_rows(const AttendArgs& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev);
     }
-    attend_rows_kernel<T, D, MT><<<p.ctas, kAThreads, bytes, s>>>(p, km, vm);
-    return cudaGetLastError();
+    return launch_early(attend_rows_kernel<T, D, MT>, dim3((unsigned)p.ctas), dim3(kAThreads), bytes, s, p, km, vm);
 }
 template <typename T, int D, int RM>
 cudaError_t launch_join(const AttendArgs& p, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     if constexpr (RM >= 128) {
-        cfg.blockDim = dim3(JoinCfg<D, RM>::kThreads);
-        cfg.gridDim = dim3((unsigned)p.ctas, JoinCfg<D, RM>::kBlocks);
-        return cudaLaunchKernelEx(&cfg, attend_join_columns_kernel<T, D, RM>, p);
+        using C = JoinCfg<D, RM>;
+        return launch_early(attend_join_columns_kernel<T, D, RM>, dim3((unsigned)p.ctas, C::kBlocks), dim3(C::kThreads), 0,
+                            s, p);
     } else {
-        cfg.blockDim = dim3(32 * kJoinRows * kJoinGroups);
-        cfg.gridDim = dim3((unsigned)p.ctas, RM / kJoinRows);
-        return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, RM>, p);
+        return launch_early(attend_join_kernel<T, D, RM>, dim3((unsigned)p.ctas, RM / kJoinRows),
+                            dim3(32 * kJoinRows * kJoinGroups), 0, s, p);
     }
 }
 

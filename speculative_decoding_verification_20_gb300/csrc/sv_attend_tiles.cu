@@ -9,6 +9,7 @@
 //   warps 8, 10     issue the products of one row tile each: S = Q K^T from shared memory,
 //                   O += P V with P from tensor memory
 //   warp 9          loads keys and values by TMA, page by page, into a ring
+//   warp 11         loads the next unit's queries while this one's ends
 // While one tile's softmax runs, the products of the other fill the tensor cores:
 // PV and the next S of tile A, then those of tile B.  The output stays in tensor memory
 // over all keys; the running maximum it refers to is only raised when a row's scores
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t s_full[C::kStages], s_empty[C::kStages];  // ring of key and value tiles
     __shared__ uint64_t s_q[2], s_scores[2], s_weights[2][2], s_out[2];  // per half (weights: in two parts)
+    __shared__ uint64_t s_q_free[2];  // per place of the queries
     __shared__ uint64_t s_last, s_second, s_joined;
     __shared__ float2 s_ml[SPLIT ? 128 : 1];  // the second half's maximum and sum
     __shared__ uint32_t s_tmem;
@@ -196,7 +198,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
             bar_init(&s_empty[s], 2);  // both halves, whether or not they read the stage
         }
         for (int x = 0; x < 2; ++x) {
-            bar_init(&s_q[x], 128);
+            bar_init(&s_q[x], 1);
+            bar_init(&s_q_free[x], SPLIT ? 2 : 1);
             bar_init(&s_scores[x], 1);
             bar_init(&s_weights[x][0], 128);
             bar_init(&s_weights[x][1], 128);
@@ -215,6 +218,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    grid_dependency_wait();
     fill_idle_rows<T, kTThreads>(p);
     Part part;
     find_part<RM, kTThreads>(p, part, reinterpret_cast<int*>(smem_p));
@@ -240,32 +244,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
         uint32_t n_scores = 0, n_out = 0;  // phases seen
         bool alive = true;
 
-        // the rows of unit w (the index-th) into shared memory, swizzled as the products
-        // read them; SPLIT: by the first half, in two places in turn
-        auto load_q = [&](const Unit& w, int index) {
-            const int rows = w.n * p.group;
-            if (SPLIT ? x != 0 : w.rt * RM + x0 >= rows) return;
-            unsigned char* dst = smem_p + (SPLIT ? index & 1 : x) * 128 * D * 2;
-            constexpr int RC = D / 8, RS = 32 / RC;  // 16-byte pieces of a row, rows a step
-            const int c = lane % RC, r0 = w.rt * RM + x0, i0 = (row & ~31) + lane / RC;
-            constexpr int AHEAD = 8;
-#pragma unroll 1
-            for (int i = i0; i < i0 + 32; i += AHEAD * RS) {
-                uint4 v[AHEAD];
-#pragma unroll
-                for (int k = 0; k < AHEAD; ++k)
-                    v[k] = __ldg(reinterpret_cast<const uint4*>(
-                                     q_row<T>(p, w.b, w.h, min(r0 + i + k * RS, rows - 1))) + c);
-#pragma unroll
-                for (int k = 0; k < AHEAD; ++k) {
-                    const int j = i + k * RS;  // (rows past the last are computed and dropped)
-                    *reinterpret_cast<uint4*>(dst + (c / 8) * C::kHalfBytes + j * 128 + (((c & 7) ^ (j & 7)) << 4)) = v[k];
-                }
-            }
-            fence_async_smem();
-            bar_arrive(&s_q[SPLIT ? index & 1 : x]);
-        };
-        load_q(u, 0);
         while (left > 0) {
             const int rows = u.n * p.group, r = u.rt * RM + x0 + row;
             const int end = min(u.t1, first + left);
@@ -357,9 +335,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     add[0] = add2(add[0], add[1]);
                     sum += add[0].x + add[0].y;
                 }
-                // all scores of the unit are through: its queries make room for the next
                 if (left > 0) next_unit<RM>(p, next);
-                if (alive && left > 0) load_q(next, index + 1);
                 if (alive && start < end) {
                     alive = bar_wait(&s_out[x], n_out & 1, limit, dead);
                     ++n_out;
@@ -429,7 +405,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 }
             } else if (left > 0) {
                 next_unit<RM>(p, next);
-                if (alive) load_q(next, index + 1);
             }
             if (!alive && lane == 0 && p.a.row_status) atomicOr(p.a.row_status + u.b, SV_ROW_INTERNAL);
             u = next;
@@ -471,8 +446,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 }
                 return bar_wait(&s_full[stage], turn, limit, dead);
             };
-            // S of the keys in the place that was reached
-            auto scores = [&](uint32_t q_desc) {
+            // S of the keys in the place that was reached; the unit's last frees its queries' place
+            auto scores = [&](uint32_t q_desc, bool last, int place) {
                 const uint32_t b = uniform(desc_keys(ring_s + stage * C::kTileBytes));
                 fence_after();
                 if (elect()) {
@@ -483,6 +458,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     }
                     mma_commit(&s_scores[x]);
                     mma_commit(&s_empty[stage]);
+                    if (last) mma_commit(&s_q_free[place]);
                 }
                 __syncwarp();
                 next_place();
@@ -490,19 +466,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
             while (alive && left > 0) {
                 const int end = min(u.t1, first + left);
                 const uint32_t last = at + 2 * (end - first);  // the place after the unit's
+                const int q_place = SPLIT ? index & 1 : x;
                 if (SPLIT || u.rt * RM + x * 128 < u.n * p.group) {
                     const int start = first + (SPLIT ? x : 0);
                     int lo, hi;
                     tile_keys<RM>(p, u.past, u.n, u.rt, lo, hi);
                     const int vend = u.past + u.n;
-                    const uint32_t q_desc = uniform(desc_keys(q_s + (SPLIT ? index & 1 : x) * 128 * D * 2));
+                    const uint32_t q_desc = uniform(desc_keys(q_s + q_place * 128 * D * 2));
                     uint32_t i = at + 2 * (start - first);
                     if (start < end) {
-                        // SPLIT: the place of the queries is not written again before this half is
-                        // through with the unit, so the unit's count gives the phase
-                        alive = bar_wait(&s_q[SPLIT ? index & 1 : x], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
+                        // SPLIT: a place of the queries is written again when both halves have
+                        // freed it, so the unit's count gives the phase
+                        alive = bar_wait(&s_q[q_place], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
                         alive = alive && reach(i);
-                        if (alive) scores(q_desc);
+                        if (alive) scores(q_desc, start + STEP >= end, q_place);
+                    } else if (lane == 0) {
+                        bar_arrive(&s_q_free[q_place]);
                     }
                     for (int tile = start; alive && tile < end; tile += STEP, i += 2 * STEP) {
                         const bool more = tile + STEP < end;
@@ -548,7 +527,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         ++n_w;
                         if (more) {
                             if (SPLIT) alive = reach(i + 2 * STEP);
-                            if (alive) scores(q_desc);
+                            if (alive) scores(q_desc, tile + 2 * STEP >= end, q_place);
                         }
                     }
                 }
@@ -649,6 +628,46 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 if (stage == C::kStages - 1) turn ^= 1;
                 while (!bar_try(&s_full[stage], turn) && now_ns() - t0 < kWaitLimitNs) {}
             }
+        } else {
+            // ---------------------------------------------------------- queries
+            // A unit's rows into shared memory, swizzled as the products read them: 128 rows
+            // for each half, or (SPLIT) for both, in two places in turn.  A place is free when
+            // the last scores of what it held are through.
+            Unit u = part.u;
+            int first = part.tile, left = part.todo, index = 0;
+            uint32_t n_free[2] = {0, 0};
+            bool alive = true;
+            constexpr int RC = D / 8, RS = 32 / RC;  // 16-byte pieces of a row, rows a step
+            const int c = lane % RC, sub = lane / RC;
+            while (alive && left > 0) {
+                const int rows = u.n * p.group;
+                for (int x = 0; alive && x < (SPLIT ? 1 : 2); ++x) {
+                    const int r0 = u.rt * RM + x * 128, place = SPLIT ? index & 1 : x;
+                    if (r0 >= rows) break;
+                    if (n_free[place]++ > 0) alive = bar_wait(&s_q_free[place], n_free[place] & 1, limit, dead);
+                    if (!alive) break;
+                    const uint32_t dst = q_s + place * 128 * D * 2 + (c >> 3) * C::kHalfBytes;
+#pragma unroll 4
+                    for (int i = sub; i < 128; i += RS) {  // (rows past the last are computed and dropped)
+                        const T* src = q_row<T>(p, u.b, u.h, min(r0 + i, rows - 1)) + c * 8;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
+                                     "l"(src)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&s_q[place]);
+                }
+                const int end = min(u.t1, first + left);
+                left -= end - first;
+                ++index;
+                if (left > 0) {
+                    next_unit<RM>(p, u);
+                    first = u.t0;
+                }
+            }
         }
     }
     __syncthreads();
@@ -677,8 +696,7 @@ cudaError_t launch_tiles(const AttendArgs& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev);
     }
-    attend_tiles_kernel<T, D, SPLIT><<<p.ctas, kTThreads, bytes, s>>>(ta, km, vm);
-    return cudaGetLastError();
+    return launch_early(attend_tiles_kernel<T, D, SPLIT>, dim3((unsigned)p.ctas), dim3(kTThreads), bytes, s, ta, km, vm);
 }
 
 template <typename T>
