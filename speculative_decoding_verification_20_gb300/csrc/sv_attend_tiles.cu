@@ -33,8 +33,6 @@ namespace sv {
 namespace {
 
 constexpr int kTThreads = 384;
-// registers a thread: softmax warps, the others; their sum has to fit the launch's share
-constexpr int kSoftRegs = 216, kOtherRegs = 72;
 constexpr int kBadSlots = 16;  // units that the loader can be ahead by, and more
 
 template <int D>
@@ -112,43 +110,32 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 #define SV_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), \
                     "=r"(a[i + 6]), "=r"(a[i + 7])
+#define SV_RW8(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3]), "+r"(a[i + 4]), "+r"(a[i + 5]), \
+                     "+r"(a[i + 6]), "+r"(a[i + 7])
 #define SV_I8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), \
                     "r"(a[i + 6]), "r"(a[i + 7])
-// 32 columns of the thread's row; the values are there when this returns
-__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* r) {
+// 16 columns of the thread's row; the values are there when this returns
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
         "tcgen05.wait::ld.sync.aligned;"
-        : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24)
+        : SV_R8(r, 0), SV_R8(r, 8)
         : "r"(addr)
         : "memory");
 }
-// 128 columns
-__device__ __forceinline__ void tmem_load128(uint32_t addr, uint32_t* r) {
+// 64 columns, not waited for
+__device__ __forceinline__ void tmem_start64(uint32_t addr, uint32_t* r) {
     asm volatile(
-        "{\n.reg .b32 a1, a2, a3;\nadd.u32 a1, %128, 32;\nadd.u32 a2, %128, 64;\nadd.u32 a3, %128, 96;\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,"
-        "%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [a1];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,"
-        "%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [a2];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,"
-        "%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [a3];\n"
-        "tcgen05.wait::ld.sync.aligned;\n}\n"
-        : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24), SV_R8(r, 32), SV_R8(r, 40), SV_R8(r, 48), SV_R8(r, 56),
-          SV_R8(r, 64), SV_R8(r, 72), SV_R8(r, 80), SV_R8(r, 88), SV_R8(r, 96), SV_R8(r, 104), SV_R8(r, 112),
-          SV_R8(r, 120)
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : SV_R8(r, 0), SV_R8(r, 8), SV_R8(r, 16), SV_R8(r, 24), SV_R8(r, 32), SV_R8(r, 40), SV_R8(r, 48), SV_R8(r, 56)
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        SV_I8(r, 0), SV_I8(r, 8), SV_I8(r, 16), SV_I8(r, 24)
-        : "memory");
+// waits for the loads so far; the registers pass through it, so that nothing reads them before
+__device__ __forceinline__ void tmem_wait64(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : SV_RW8(r, 0), SV_RW8(r, 8), SV_RW8(r, 16), SV_RW8(r, 24), SV_RW8(r, 32), SV_RW8(r, 40), SV_RW8(r, 48),
+                   SV_RW8(r, 56)::"memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
     asm volatile(
@@ -233,7 +220,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
         // nothing to do
     } else if (warp < 8) {
         // ---------------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int x = warp >> 2;              // half of the CTA
         const int row = t & 127;              // row of its tile
         const int x0 = SPLIT ? 0 : x * 128;   // the tile's first row in the unit
@@ -272,23 +258,36 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         bar_arrive(&s_weights[x][1]);
                         continue;
                     }
-                    float s[kKeyTile];
-                    tmem_load128(tS, reinterpret_cast<uint32_t*>(s));
+                    // The scores of 128 keys, as two halves.  The second is read for the maximum, and
+                    // again when the first has become weights: held through, it costs spills.
+                    float s0[64], s1[64];
+                    uint32_t *w0 = reinterpret_cast<uint32_t*>(s0), *w1 = reinterpret_cast<uint32_t*>(s1);
+                    tmem_start64(tS + 64, w1);
+                    tmem_start64(tS, w0);
+                    tmem_wait64(w1);
+                    tmem_wait64(w0);
                     const int k0 = tile * kKeyTile;
-                    if (k0 + kKeyTile - 1 > pos0 || (p.a.window > 0 && k0 <= (int64_t)pos1 - p.a.window)) {
-                        const int64_t from = p.a.window > 0 ? pos - p.a.window + 1 : 0;
-                        const int a = (int)max(from - k0, (int64_t)0), b = pos - k0;  // visible: [a, b]
+                    const bool cut = k0 + kKeyTile - 1 > pos0 || (p.a.window > 0 && k0 <= (int64_t)pos1 - p.a.window);
+                    // visible: keys [seen0, seen1] of the tile
+                    const int seen0 = p.a.window > 0 ? (int)max((int64_t)pos - p.a.window + 1 - k0, (int64_t)0) : 0;
+                    const int seen1 = pos - k0;
+                    if (cut) {
 #pragma unroll
-                        for (int j = 0; j < kKeyTile; ++j)
-                            if (j < a || j > b) s[j] = -INFINITY;
+                        for (int j = 0; j < 64; ++j) {
+                            if (j < seen0 || j > seen1) s0[j] = -INFINITY;
+                            if (j + 64 < seen0 || j + 64 > seen1) s1[j] = -INFINITY;
+                        }
                     }
-                    float top[4] = {s[0], s[1], s[2], s[3]};
+                    float top[4] = {s0[0], s0[1], s1[0], s1[1]};
 #pragma unroll
-                    for (int j = 4; j < kKeyTile - 4; j += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], s[j + 2 * e]), s[j + 2 * e + 1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[kKeyTile - 4 + e]);
+                    for (int j = 2; j < 62; j += 4) {
+                        top[0] = fmaxf(fmaxf(top[0], s0[j]), s0[j + 1]);
+                        top[1] = fmaxf(fmaxf(top[1], s0[j + 2]), s0[j + 3]);
+                        top[2] = fmaxf(fmaxf(top[2], s1[j]), s1[j + 1]);
+                        top[3] = fmaxf(fmaxf(top[3], s1[j + 2]), s1[j + 3]);
+                    }
+                    top[0] = fmaxf(fmaxf(top[0], s0[62]), s0[63]);
+                    top[2] = fmaxf(fmaxf(top[2], s1[62]), s1[63]);
                     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.qscale;
                     if (tile == start) {
                         ref = m;
@@ -299,13 +298,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         alive = bar_wait(&s_out[x], n_out & 1, limit, dead);  // the product before this one
                         if (!alive) break;
                         fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float o[16];
+                            tmem_load16(tO + c, reinterpret_cast<uint32_t*>(o));
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_load32(tO + c, reinterpret_cast<uint32_t*>(o));
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= f;
-                            tmem_store32(tO + c, reinterpret_cast<const uint32_t*>(o));
+                            for (int j = 0; j < 16; ++j) o[j] *= f;
+                            tmem_store16(tO + c, reinterpret_cast<const uint32_t*>(o));
                         }
                         sum *= f;
                         ref = now;
@@ -314,24 +313,35 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     const float base = ref == -INFINITY ? 0.0f : ref;  // nothing visible yet: weights 0
                     const float2 qs = make_float2(p.qscale, p.qscale), mb = make_float2(-base, -base);
                     float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    auto weigh = [&](const float* x, int c) {  // 32 keys, the c-th such set of the tile
                         uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            float2 e = fma2(make_float2(s[c * 32 + 2 * j], s[c * 32 + 2 * j + 1]), qs, mb);
+                            float2 e = fma2(make_float2(x[2 * j], x[2 * j + 1]), qs, mb);
                             e.x = fast_exp2(e.x);
                             e.y = fast_exp2(e.y);
                             add[j & 1] = add2(add[j & 1], e);
                             w[j] = Pair<T>::pack(e.x, e.y);  // 16 bits into the product, as the values
                         }
                         tmem_store16(tS + c * 16, w);
-                        if (c & 1) {  // half of the keys: their product can start
-                            tmem_store_wait();
-                            fence_before();
-                            bar_arrive(&s_weights[x][c >> 1]);
-                        }
+                    };
+                    weigh(s0, 0);
+                    tmem_start64(tS + 64, w1);
+                    weigh(s0 + 32, 1);
+                    tmem_wait64(w1);
+                    tmem_store_wait();  // half of the weights: their product can start
+                    fence_before();
+                    bar_arrive(&s_weights[x][0]);
+                    if (cut) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (j + 64 < seen0 || j + 64 > seen1) s1[j] = -INFINITY;
                     }
+                    weigh(s1, 2);
+                    weigh(s1 + 32, 3);
+                    tmem_store_wait();
+                    fence_before();
+                    bar_arrive(&s_weights[x][1]);
                     add[0] = add2(add[0], add[1]);
                     sum += add[0].x + add[0].y;
                 }
@@ -368,27 +378,28 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     if (!whole && r < rows)
                         *reinterpret_cast<float2*>(p.part_ml + ((int64_t)place * RM + x0 + row) * 2) =
                             make_float2(alive ? ref : -INFINITY, l);
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
                         __syncwarp();  // tensor memory is read by whole warps
                         if (alive) {
-                            tmem_load32(tO + c, reinterpret_cast<uint32_t*>(o));
+                            tmem_load16(tO + c, reinterpret_cast<uint32_t*>(o));
                             if (SPLIT) {
                                 if (end - first > 1) {
-                                    float o1[32];
-                                    tmem_load32(tO + D + c, reinterpret_cast<uint32_t*>(o1));
+                                    float o1[16];
+                                    tmem_load16(tO + D + c, reinterpret_cast<uint32_t*>(o1));
 #pragma unroll
-                                    for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + o1[j] * f1;
+                                    for (int j = 0; j < 16; ++j) o[j] = o[j] * f0 + o1[j] * f1;
                                 }
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+                            for (int j = 0; j < 16; ++j) o[j] = 0.0f;
                         }
                         if (r < rows) {
                             if (whole) {
 #pragma unroll
-                                for (int j = 0; j < 32; j += 8)
+                                for (int j = 0; j < 16; j += 8)
                                     *reinterpret_cast<uint4*>(dst + c + j) =
                                         make_uint4(Pair<T>::pack(o[j] * inv, o[j + 1] * inv),
                                                    Pair<T>::pack(o[j + 2] * inv, o[j + 3] * inv),
@@ -396,7 +407,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                                                    Pair<T>::pack(o[j + 6] * inv, o[j + 7] * inv));
                             } else {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) part_o[(int64_t)(c + j) * RM] = o[j];
+                                for (int j = 0; j < 16; ++j) part_o[(int64_t)(c + j) * RM] = o[j];
                             }
                         }
                     }
@@ -412,7 +423,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
             ++index;
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8 || warp == 10) {
             // ------------------------------------------------------------ products
             // of one half each.  (One warp for both left the tensor cores idle between its
@@ -683,15 +693,12 @@ cudaError_t launch_tiles(const AttendArgs& p, cudaStream_t s) {
     while (ta.box < kKeyTile && p.a.cache.page_size % (2 * ta.box) == 0) ta.box *= 2;
     CUtensorMap km, vm;
     if (!encode_pages(&km, &vm, p, ta.box, 1)) return cudaErrorInvalidValue;
-    // once a device: room in shared memory, and proof that the register split fits the launch
+    // once a device: room in shared memory
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load() >> dev & 1)) {
-        cudaFuncAttributes at;
-        if ((e = cudaFuncGetAttributes(&at, attend_tiles_kernel<T, D, SPLIT>)) != cudaSuccess) return e;
-        if (at.numRegs * kTThreads < 256 * kSoftRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(attend_tiles_kernel<T, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev);
