@@ -63,7 +63,7 @@ __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? l
 // the first pass, the few such tokens of a row cost each of their warps the whole
 // arithmetic: that form took 886 us for [256, 8, 128256] bf16.
 template <typename T, int WORDS>
-__global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int chunks) {
+__global__ void __launch_bounds__(kLThreads, 8) logits_kernel(sv_logits_args a, int chunks) {
     constexpr int VEC = 16 / (int)sizeof(T);
     constexpr int CHUNK = WORDS * 32;
     constexpr int U = CHUNK / (kLThreads * VEC);
@@ -113,46 +113,35 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int
         bhi = clampi(a.bias_offsets[b + 1], blo, (int)a.bias_total);
     }
     const bool special = nprefix > 0 || bhi > blo;
+    // each warp takes a contiguous part of the bias list and keeps its order; what it needs
+    // first is asked for before the barrier
+    const int bias_per = (bhi - blo + kLWarps - 1) / kLWarps;
+    const int bias_lo = blo + warp * bias_per, bias_hi = min(bias_lo + bias_per, bhi);
+    int bias_x = bias_lo + lane < bias_hi ? a.bias_ids[bias_lo + lane] : -1;
+    const int draft_x = t < nprefix ? a.draft_tokens[b * a.draft_stride + t] : -1;
 
-    uint32_t ok = 0xFFFFFFFFu, seen = 0u;
     if (t < WORDS) {
-        if (mask) ok = plane_word(mask, first + 32 * t, V);
-        if (a.seen) seen = plane_word(a.seen + slot * a.words, first + 32 * t, V);
-        s_ok[t] = ok;
-        s_seen[t] = seen;
+        s_ok[t] = mask ? plane_word(mask, first + 32 * t, V) : 0xFFFFFFFFu;
+        s_seen[t] = a.seen ? plane_word(a.seen + slot * a.words, first + 32 * t, V) : 0u;
         s_special[t] = 0u;
     }
     if (t == 0) s_count = 0;
     __syncthreads();
 
-    // the logits that the mask leaves; a vector that it hides whole is not read
-    uint4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int at = (u * kLThreads + t) * VEC, e0 = first + at;
-        const uint32_t m = (s_ok[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (m && vec && e0 >= 0 && e0 + VEC <= V) raw[u] = *reinterpret_cast<const uint4*>(in + e0);
-    }
-
     // the tokens that need more
     bool overflow = false;
     if (special) {
         if (t < nprefix) {
-            const int x = a.draft_tokens[b * a.draft_stride + t];
-            s_draft[t] = x;
-            const int at = x - first;
-            if (x >= 0 && x < V && at >= 0 && at < CHUNK) atomicOr(&s_special[at >> 5], 1u << (at & 31));
+            s_draft[t] = draft_x;
+            const int at = draft_x - first;
+            if (draft_x >= 0 && draft_x < V && at >= 0 && at < CHUNK) atomicOr(&s_special[at >> 5], 1u << (at & 31));
         }
-        // each warp takes a contiguous part of the bias list and keeps its order
-        const int per = (bhi - blo + kLWarps - 1) / kLWarps;
-        const int lo = blo + warp * per, hi = min(lo + per, bhi);
         int n = 0;
-        for (int j0 = lo; j0 < hi; j0 += 32) {
+        for (int j0 = bias_lo; j0 < bias_hi; j0 += 32) {
             const int j = j0 + lane;
-            const int x = j < hi ? a.bias_ids[j] : -1;
-            const int at = x - first;
-            const bool hit = x >= 0 && x < V && at >= 0 && at < CHUNK;
+            if (j0 != bias_lo) bias_x = j < bias_hi ? a.bias_ids[j] : -1;
+            const int at = bias_x - first;
+            const bool hit = bias_x >= 0 && bias_x < V && at >= 0 && at < CHUNK;
             const unsigned m = __ballot_sync(0xFFFFFFFFu, hit);
             if (hit) {
                 atomicOr(&s_special[at >> 5], 1u << (at & 31));
@@ -170,7 +159,7 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int
     if (special || a.seen) {
         // (the list's order differs from run to run; what is done to a token does not depend on it)
         if (t < WORDS) {
-            uint32_t w = (seen | s_special[t]) & ok;
+            uint32_t w = (s_seen[t] | s_special[t]) & s_ok[t];
             if (w) {
                 int k = atomicAdd(&s_count, __popc(w));
                 for (; w; w &= w - 1) s_list[k++] = (uint16_t)(32 * t + __ffs(w) - 1);
@@ -178,6 +167,15 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int
         }
     }
 
+    // the copy; a vector that the mask hides whole is not read
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int at = (u * kLThreads + t) * VEC, e0 = first + at;
+        const uint32_t m = (s_ok[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (m && vec && e0 >= 0 && e0 + VEC <= V) raw[u] = *reinterpret_cast<const uint4*>(in + e0);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int at = (u * kLThreads + t) * VEC, e0 = first + at;
@@ -185,7 +183,7 @@ __global__ void __launch_bounds__(kLThreads) logits_kernel(sv_logits_args a, int
         if (vec && e0 >= 0 && e0 + VEC <= V) {
             *reinterpret_cast<uint4*>(out + e0) = hide(raw[u], m, in);
         } else {
-#pragma unroll
+#pragma unroll 1
             for (int v = 0; v < VEC; ++v) {
                 const int e = e0 + v;
                 if (e >= 0 && e < V) {
@@ -323,6 +321,6 @@ extern "C" int spec_verify_process_logits(const sv_logits_args* args, void* stre
     if (a.dtype == SV_BF16)
         e = wide ? sv::launch_logits<__nv_bfloat16, 256>(a, s) : sv::launch_logits<__nv_bfloat16, 64>(a, s);
     else
-        e = wide ? sv::launch_logits<float, 256>(a, s) : sv::launch_logits<float, 64>(a, s);
+        e = wide ? sv::launch_logits<float, 128>(a, s) : sv::launch_logits<float, 64>(a, s);
     return e == cudaSuccess ? SV_OK : SV_ECUDA;
 }
