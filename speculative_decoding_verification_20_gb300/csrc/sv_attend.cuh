@@ -258,21 +258,24 @@ __device__ __forceinline__ void next_unit(const AttendArgs& p, Unit& u) {
     unit_tiles<RM>(p, u);
 }
 
-// rows that no unit covers: zeros past a sequence's new tokens, NaN for a sequence
-// whose lengths are bad
-template <typename T, int NT>
+// Rows that no unit covers: zeros past a sequence's new tokens, NaN for a sequence whose
+// lengths are bad.  A sequence's rows are shared by the CTAs c, c + B, ..., a warp a token.
+template <typename T, int D, int NT>
 __device__ void fill_idle_rows(const AttendArgs& p) {
-    const int vecs = (int)p.a.dim / 8, Hq = (int)p.a.q_heads;
-    for (int b = blockIdx.x; b < p.a.B; b += gridDim.x) {
+    constexpr int VECS = D / 8;
+    const int B = (int)p.a.B, ctas = (int)gridDim.x, lane = threadIdx.x & 31;
+    const int parts = max(1, ctas / B), part = (int)blockIdx.x / B;
+    if (part >= parts) return;
+    for (int b = (int)blockIdx.x % B; b < B; b += ctas) {
         const SeqLens s = seq_lens(p.a.cache, b, (int)p.a.N, p.capacity);
-        if (s.bad && threadIdx.x == 0 && p.a.row_status) atomicOr(p.a.row_status + b, SV_ROW_BAD_LENGTH);
+        if (s.bad && part == 0 && threadIdx.x == 0 && p.a.row_status)
+            atomicOr(p.a.row_status + b, SV_ROW_BAD_LENGTH);
         const uint32_t w = s.bad ? Pair<T>::pack(NAN, NAN) : 0u;
-        const int64_t idle = (int64_t)(p.a.N - s.n) * Hq * vecs;
-        for (int64_t x = threadIdx.x; x < idle; x += NT) {
-            const int64_t row = x / vecs;
-            T* o = (T*)p.a.out + b * p.a.o_stride_b + (s.n + row / Hq) * p.a.o_stride_n +
-                   (row % Hq) * p.a.o_stride_h + (x % vecs) * 8;
-            *reinterpret_cast<uint4*>(o) = make_uint4(w, w, w, w);
+        for (int i = s.n + part * (NT / 32) + (int)threadIdx.x / 32; i < p.a.N; i += parts * (NT / 32)) {
+            T* o = (T*)p.a.out + (int64_t)b * p.a.o_stride_b + (int64_t)i * p.a.o_stride_n;
+            for (int x = lane; x < (int)p.a.q_heads * VECS; x += 32)
+                *reinterpret_cast<uint4*>(o + (int64_t)(x / VECS) * p.a.o_stride_h + x % VECS * 8) =
+                    make_uint4(w, w, w, w);
         }
     }
 }

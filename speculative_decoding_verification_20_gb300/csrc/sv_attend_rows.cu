@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         fence_async_smem();
     }
     grid_dependency_wait();
-    fill_idle_rows<T, kAThreads>(p);
+    fill_idle_rows<T, D, kAThreads>(p);
     Part part;
     find_part<RM, kAThreads>(p, part, reinterpret_cast<int*>(s_join));
     __syncthreads();

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     grid_dependency_wait();
-    fill_idle_rows<T, kTThreads>(p);
+    fill_idle_rows<T, D, kTThreads>(p);
     Part part;
     find_part<RM, kTThreads>(p, part, reinterpret_cast<int*>(smem_p));
     fence_before();
