@@ -200,12 +200,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
+    grid_dependency_wait();
+    // (tensor memory is taken only now: the kernel before this one may need it to end)
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    grid_dependency_wait();
     fill_idle_rows<T, D, kTThreads>(p);
     Part part;
     find_part<RM, kTThreads>(p, part, reinterpret_cast<int*>(smem_p));
@@ -252,10 +253,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     ++n_scores;
                     fence_after();
                     if (wr0 >= rows) {  // no rows: their lanes' products go nowhere
-                        if (tile != start) ++n_out;
                         fence_before();
                         bar_arrive(&s_weights[x][0]);
                         bar_arrive(&s_weights[x][1]);
+                        if (tile != start) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
                         continue;
                     }
                     // The scores of 128 keys, as two halves.  The second is read for the maximum, and
@@ -289,14 +290,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     top[0] = fmaxf(fmaxf(top[0], s0[62]), s0[63]);
                     top[2] = fmaxf(fmaxf(top[2], s1[62]), s1[63]);
                     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.qscale;
+                    bool out_seen = tile == start;
                     if (tile == start) {
                         ref = m;
                     } else if (__any_sync(0xFFFFFFFFu, m > ref + 8.0f)) {
                         // raise the reference; the output so far shrinks by as much
                         const float now = fmaxf(ref, m);
                         const float f = now == -INFINITY ? 1.0f : fast_exp2(ref - now);
-                        alive = bar_wait(&s_out[x], n_out & 1, limit, dead);  // the product before this one
+                        alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);  // the product before this one
                         if (!alive) break;
+                        out_seen = true;
                         fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
@@ -309,7 +312,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         sum *= f;
                         ref = now;
                     }
-                    if (tile != start) ++n_out;
                     const float base = ref == -INFINITY ? 0.0f : ref;  // nothing visible yet: weights 0
                     const float2 qs = make_float2(p.qscale, p.qscale), mb = make_float2(-base, -base);
                     float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -344,12 +346,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     bar_arrive(&s_weights[x][1]);
                     add[0] = add2(add[0], add[1]);
                     sum += add[0].x + add[0].y;
+                    // (every phase is waited for, in order: a parity does not tell the one before last)
+                    if (!out_seen) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
                 }
                 if (left > 0) next_unit<RM>(p, next);
-                if (alive && start < end) {
-                    alive = bar_wait(&s_out[x], n_out & 1, limit, dead);
-                    ++n_out;
-                }
+                if (alive && start < end) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
                 if (SPLIT && x == 1) {
                     s_ml[row] = make_float2(ref, sum);
                     fence_before();
