@@ -38,12 +38,14 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// -inf where the bit of a vector's element is 0
+// -inf where the bit of a vector's element is 0.  bf16: bits 2i and 2i + 1 are spread to
+// bits 0 and 16, and a product makes each a 16-bit mask.
 __device__ __forceinline__ uint4 hide(uint4 r, uint32_t ok, const __nv_bfloat16*) {
     uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    const uint32_t spread = ok | (ok << 15);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t keep = (ok >> (2 * i) & 1u ? 0x0000FFFFu : 0u) | (ok >> (2 * i + 1) & 1u ? 0xFFFF0000u : 0u);
+        const uint32_t keep = ((spread >> (2 * i)) & 0x00010001u) * 0xFFFFu;
         w[i] = (w[i] & keep) | (0xFF80FF80u & ~keep);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -77,16 +79,15 @@ __global__ void __launch_bounds__(kLThreads, 8) logits_kernel(sv_logits_args a, 
     __shared__ int s_draft[SV_MAX_GAMMA];
 
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t row = blockIdx.x / (unsigned)chunks;
-    const int chunk = (int)(blockIdx.x % (unsigned)chunks);
-    const int V = (int)a.V, b = (int)(row / a.N), i = (int)(row % a.N);
+    const unsigned row = blockIdx.x / (unsigned)chunks, chunk = blockIdx.x - row * (unsigned)chunks;
+    const int V = (int)a.V, b = (int)(row / (unsigned)a.N), i = (int)(row - (unsigned)b * (unsigned)a.N);
     const T* in = (const T*)a.logits + b * a.logits_stride_b + i * a.logits_stride_n;
     T* out = (T*)a.out + b * a.out_stride_b + i * a.out_stride_n;
     // vectors lie on 16-byte boundaries of the row's memory: the chunk begins up to a
     // vector before its place
     const int skew = (int)(((uintptr_t)in & 15u) / sizeof(T));
     const bool vec = (((uintptr_t)in ^ (uintptr_t)out) & 15u) == 0;
-    const int first = chunk * CHUNK - skew;
+    const int first = (int)chunk * CHUNK - skew;
     if (first >= V) return;
 
     // the sequence's parameters; bad ones give NaN rows
@@ -168,21 +169,31 @@ __global__ void __launch_bounds__(kLThreads, 8) logits_kernel(sv_logits_args a, 
     }
 
     // the copy; a vector that the mask hides whole is not read
-    uint4 raw[U];
+    if (vec && first >= 0 && first + CHUNK <= V) {
+        const uint4* src = reinterpret_cast<const uint4*>(in + first) + t;
+        uint4* dst = reinterpret_cast<uint4*>(out + first) + t;
+        uint4 raw[U];
+        uint32_t m[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int at = (u * kLThreads + t) * VEC, e0 = first + at;
-        const uint32_t m = (s_ok[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (m && vec && e0 >= 0 && e0 + VEC <= V) raw[u] = *reinterpret_cast<const uint4*>(in + e0);
-    }
+        for (int u = 0; u < U; ++u) {
+            const int at = (u * kLThreads + t) * VEC;
+            m[u] = (s_ok[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (m[u]) raw[u] = src[u * kLThreads];
+        }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int at = (u * kLThreads + t) * VEC, e0 = first + at;
-        const uint32_t m = (s_ok[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
-        if (vec && e0 >= 0 && e0 + VEC <= V) {
-            *reinterpret_cast<uint4*>(out + e0) = hide(raw[u], m, in);
-        } else {
+        for (int u = 0; u < U; ++u) dst[u * kLThreads] = hide(raw[u], m[u], in);
+    } else {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+            const int at = (u * kLThreads + t) * VEC, e0 = first + at;
+            const uint32_t m = (s_ok[at >> 5] >> (at & 31)) & ((1u << VEC) - 1u);
+            if (vec && e0 >= 0 && e0 + VEC <= V) {
+                uint4 raw = make_uint4(0, 0, 0, 0);
+                if (m) raw = *reinterpret_cast<const uint4*>(in + e0);
+                *reinterpret_cast<uint4*>(out + e0) = hide(raw, m, in);
+                continue;
+            }
 #pragma unroll 1
             for (int v = 0; v < VEC; ++v) {
                 const int e = e0 + v;
