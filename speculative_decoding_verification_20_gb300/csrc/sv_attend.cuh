@@ -299,6 +299,12 @@ __device__ __forceinline__ float fast_exp2(float x) {  // 2^x; 2^-inf = 0
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 #endif  // __CUDACC__
 
 // tensor maps of the pages, a head's rows in parts of 64 elements (128 bytes, swizzled):

@@ -21,6 +21,14 @@
 // scores are masked, and its values add nothing.  Rows of a box past the sequence's end
 // are zeroed in shared memory before their product, since they may hold anything.
 //
+// Two chunks of 2048 tokens behind 4-6k keys (32 / 8 heads of 128, bf16): 331 us, 1200
+// TFLOP/s.  What bounds it is the round of one tile: scores -> softmax (about 1650 cycles, of
+// which 512 are the exponential unit's) -> weights -> PV and the next S (780 cycles of
+// products) -> scores, 3400 cycles in all with the hand-overs, while the two tiles' products
+// fill 2080 of them.  Tried and slower: steps of 64 keys with the scores two steps ahead (365
+// us: the step's fixed costs double), two threads a row (376 us), registers moved from the
+// other warps to the softmax (340 us: the warps that issue products then spill).
+//
 // Every wait has a limit.  When one runs out, the CTA writes NaN for what is left of its
 // part, sets SV_ROW_INTERNAL, lets its copies and products finish (with a limit) and ends.
 #include <atomic>
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         fence_before();
                         bar_arrive(&s_weights[x][0]);
                         bar_arrive(&s_weights[x][1]);
-                        if (tile != start) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
+                        if (tile != start) ++n_out;
                         continue;
                     }
                     // The scores of 128 keys, as two halves.  The second is read for the maximum, and
@@ -282,13 +290,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     float top[4] = {s0[0], s0[1], s1[0], s1[1]};
 #pragma unroll
                     for (int j = 2; j < 62; j += 4) {
-                        top[0] = fmaxf(fmaxf(top[0], s0[j]), s0[j + 1]);
-                        top[1] = fmaxf(fmaxf(top[1], s0[j + 2]), s0[j + 3]);
-                        top[2] = fmaxf(fmaxf(top[2], s1[j]), s1[j + 1]);
-                        top[3] = fmaxf(fmaxf(top[3], s1[j + 2]), s1[j + 3]);
+                        top[0] = max3(top[0], s0[j], s0[j + 1]);
+                        top[1] = max3(top[1], s0[j + 2], s0[j + 3]);
+                        top[2] = max3(top[2], s1[j], s1[j + 1]);
+                        top[3] = max3(top[3], s1[j + 2], s1[j + 3]);
                     }
-                    top[0] = fmaxf(fmaxf(top[0], s0[62]), s0[63]);
-                    top[2] = fmaxf(fmaxf(top[2], s1[62]), s1[63]);
+                    top[0] = max3(top[0], s0[62], s0[63]);
+                    top[2] = max3(top[2], s1[62], s1[63]);
                     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.qscale;
                     bool out_seen = tile == start;
                     if (tile == start) {
@@ -346,8 +354,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     bar_arrive(&s_weights[x][1]);
                     add[0] = add2(add[0], add[1]);
                     sum += add[0].x + add[0].y;
-                    // (every phase is waited for, in order: a parity does not tell the one before last)
-                    if (!out_seen) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
+                    // These scores came after the product before them, in one warp's order, so that
+                    // phase of s_out is over: the wait at the unit's end is for the one after it.
+                    // (Waiting for every phase here costs 2%.)
+                    if (!out_seen) ++n_out;
                 }
                 if (left > 0) next_unit<RM>(p, next);
                 if (alive && start < end) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);

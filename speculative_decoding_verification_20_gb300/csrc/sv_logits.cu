@@ -63,7 +63,10 @@ __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? l
 // gathered into a list from their bit planes, one word of 32 tokens a thread, and the
 // second pass takes them one a thread, reading the logit again.  Left to the threads of
 // the first pass, the few such tokens of a row cost each of their warps the whole
-// arithmetic: that form took 886 us for [256, 8, 128256] bf16.
+// arithmetic: that form took 886 us for [256, 8, 128256] bf16; this one takes 177 us (6.2
+// TB/s of logits, counting those that the masks spare).  A CTA is a chain of short waits
+// (parameters, bit planes, logits, listed tokens), so eight of them share an SM: at 32
+// registers a thread it takes 180 us, at 40 registers 211 us.
 template <typename T, int WORDS>
 __global__ void __launch_bounds__(kLThreads, 8) logits_kernel(sv_logits_args a, int chunks) {
     constexpr int VEC = 16 / (int)sizeof(T);
@@ -326,8 +329,10 @@ extern "C" int spec_verify_process_logits(const sv_logits_args* args, void* stre
     if (a.mask && (a.mask_stride_b < 0 || a.mask_stride_n < 0)) return SV_EINVAL;
     if (a.B * a.N * ((a.V + 7) / 2048 + 1) > 0x7FFFFFFF) return SV_ETOO_LARGE;
     cudaStream_t s = (cudaStream_t)stream;
-    // chunks of 8192 tokens where that still leaves every SM several CTAs, else of 2048
-    const bool wide = a.B * a.N * ((a.V + 8191) / 8192) >= 2048;
+    // 16 KB of logits a CTA where that makes two CTAs a SM or more, else 4 or 8 KB: 64 rows of
+    // 128256 bf16 logits (1024 CTAs of 16 KB) take 9.9 us by 16 KB and 16.9 us by 4 KB, 8 rows
+    // (128 CTAs) 7.1 and 5.9 us; at 256 CTAs either may win
+    const bool wide = a.B * a.N * ((a.V * (int64_t)es + 16383) / 16384) >= 304;
     cudaError_t e;
     if (a.dtype == SV_BF16)
         e = wide ? sv::launch_logits<__nv_bfloat16, 256>(a, s) : sv::launch_logits<__nv_bfloat16, 64>(a, s);
