@@ -1,14 +1,16 @@
 """In-tree build of the CUDA library (sm_103a only).
 
 Compiles ``csrc/*.cu`` with nvcc into ``libspec_verify.so`` next to this file,
-one translation unit per process, in parallel.  Object files go to
-``_build/`` at the repository root.
+one translation unit per process, in parallel, and ``csrc/sv_bind.cpp`` with the
+host compiler against torch's headers into the Python module ``_bind.so``.
+Object files go to ``_build/`` at the repository root.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libspec_verify.so")
+BIND = os.path.join(PKG, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "sv_bind.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC,
@@ -47,8 +51,32 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def build_bind(force: bool = False) -> str:
+    """The Python module of the short calls (csrc/sv_bind.cpp)."""
+    deps = [BIND_SRC, os.path.abspath(__file__)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
+    if not force and os.path.exists(BIND) and all(os.path.getmtime(d) <= os.path.getmtime(BIND) for d in deps):
+        return BIND
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + INCLUDE, "-I" + os.path.join(root, "include"),
+           "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I" + os.path.join(cuda, "include"), "-I" + sysconfig.get_paths()["include"], BIND_SRC, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     if not force and up_to_date():
+        build_bind()
         return LIB
     nvcc = _nvcc()
     os.makedirs(OBJDIR, exist_ok=True)
@@ -67,8 +95,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        bind = ex.submit(build_bind, force)
         objs = list(ex.map(compile_one, srcs))
+        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

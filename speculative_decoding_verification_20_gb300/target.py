@@ -19,6 +19,7 @@ then reports as ROW_NONFINITE.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 import struct
 from typing import Optional, Tuple
@@ -54,6 +55,32 @@ def _library():
 
         _lib = load_library()
     return _lib
+
+
+class _Short:
+    """The calls in csrc/sv_bind.cpp, which serve tensors that need no conversion and answer None for others; loaded
+    at the first use."""
+
+    __slots__ = ()
+
+    def __getattr__(self, name):
+        global _short
+        from . import _build
+
+        lib = _library()
+        try:
+            from . import _bind
+        except ImportError as e:
+            raise RuntimeError(f"{_build.BIND} is missing or of another torch: build it with "
+                               "__graft_entry__.build()") from e
+        address = lambda fn: ctypes.cast(fn, ctypes.c_void_p).value
+        _bind.setup(address(lib.spec_verify_process_logits), address(lib.spec_verify_rotate_append),
+                    address(lib.spec_verify_attention), address(lib.spec_verify_attention_workspace_size), _check)
+        _short = _bind
+        return getattr(_bind, name)
+
+
+_short = _Short()
 
 
 def _check(status: int) -> None:
@@ -190,6 +217,13 @@ def process_logits(logits: torch.Tensor, *, history: Optional[TokenHistory] = No
     mask: int32 [B, N, W] or [B, W], W >= ceil(V / 32), 1 = allowed: bit t % 32 of word t // 32 is token t's.
     out: where to write (may be ``logits``); by default a new tensor.  Returns it.
     """
+    if stream is None:
+        seen, counts = (None, None) if history is None else (history.seen, history.counts)
+        ids, vals, offs = (None, None, None) if bias is None else bias
+        res = _short.logits(logits, seen, counts, slots, draft_tokens, repetition, frequency, presence, ids, vals, offs,
+                            mask, out, row_status)
+        if res is not None:
+            return res
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3:
         raise ValueError("logits must be a CUDA tensor [B, N, V]")
     dev = logits.device
@@ -290,7 +324,8 @@ class PagedCache:
         self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.dtype, self.device = k.dtype, k.device
         self._fields = (k.data_ptr(), v.data_ptr(), self.pages, self.page_size, *k.stride()[:3], *v.stride()[:3])
-
+        self._record = struct.pack("<2Q8q4q", *self._fields, self.kv_heads, self.head_dim, _DTYPE[k.dtype],
+                                   k.device.index if k.is_cuda else -1)
 
 
 def rotary_table(length: int, rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] = None,
@@ -374,6 +409,10 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
     (a multiple of 16) may be less than dim.  Pairs are (j, j + rotary_dim / 2), or (2j, 2j + 1) with
     interleaved.  Returns the rotated q (``out``, which may be q; rows past num_new are zeros).
     """
+    if stream is None:
+        res = _short.rotate(q, k, v, table, cache._record, page_table, cache_lens, num_new, interleaved, out, row_status)
+        if res is not None:
+            return res
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, N, q_heads, dim]")
     dev, dtype, shape = q.device, cache.dtype, q.shape
@@ -425,6 +464,11 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     workspace: uint8 of attention_workspace_size() bytes; calls on one must not overlap (default: one kept for each
     stream, or the graph's own memory while a graph is captured).
     """
+    if stream is None and workspace is None:
+        res = _short.attention(q, cache._record, page_table, cache_lens, num_new, scale, window, max_context, out,
+                               row_status, wait_limit_ns)
+        if res is not None:
+            return res
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, N, q_heads, dim]")
     dev, dtype, shape = q.device, cache.dtype, q.shape

@@ -1,6 +1,7 @@
 """The target-step operators on a GPU against their 64-bit forms (tests/target_ref.py)."""
 import math
 import random
+import struct
 
 import pytest
 import torch
@@ -542,3 +543,89 @@ def test_one_round_together():
         lens += res["accepted_len"] + 1
         keys = [ref.gather(cache.k, pt[b], int(lens[b]), page) for b in range(B)]
     assert int(history.counts.sum()) == int(lens.sum())
+
+
+def test_short_calls_and_converted_calls_agree(monkeypatch):
+    """Tensors that need no conversion go straight to the C entry points, and give what the general way gives."""
+    from speculative_decoding_verification_20_gb300 import target as tg
+
+    class General:
+        logits = rotate = attention = staticmethod(lambda *a: None)
+
+    class Direct:
+        def __getattr__(self, name):
+            def call(*a):
+                res = getattr(short, name)(*a)
+                assert res is not None, f"{name} was not served directly"
+                return res
+            return call
+
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))
+    B, N, Hq, Hkv, D, V = 3, 5, 8, 2, 128, 1000
+    past, new = [40, 0, 77], [5, 3, 1]
+    s = paged(B, N, Hq, Hkv, D, BF, 32, past, new, seed=8)
+    k = torch.randn(B, N, Hkv, D, device="cuda").to(BF)
+    table = sv.rotary_table(200, 64)
+    d = logit_case(B, N, V, BF, seed=9)
+    h = history_of(d, V, slots=4, of=[3, 0, 2])
+    f32 = lambda x: torch.tensor(x, dtype=F32, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    x, mask, bias = d["logits"].cuda(), ref.planes_of(d["mask"]).cuda(), bias_of(d)
+
+    def calls(st):
+        kw = dict(row_status=st)
+        cache = sv.PagedCache.from_tensors(s["cache"].k.clone(), s["cache"].v.clone())
+        q = sv.rotate_append(s["q"], k, k, table, cache, s["table"], s["lens"], s["new"], interleaved=True, **kw)
+        o = sv.paged_attention(q, cache, s["table"], s["lens"], s["new"], window=50, scale=0.1, max_context=90, **kw)
+        o2 = sv.paged_attention(s["q"], s["cache"], s["table"], s["lens"], s["new"], out=torch.empty_like(o))
+        z = sv.process_logits(x, history=h, slots=i32([3, 0, 2]), draft_tokens=i32(d["draft"]), repetition=f32(d["rep"]),
+                              frequency=f32(d["freq"]), presence=f32(d["pres"]), bias=bias, mask=mask, **kw)
+        z2 = sv.process_logits(x[:, :1].contiguous(), slots=i32([9, 9, 9]))  # no history: its slots are not read
+        return q, cache.k, o, o2, z, z2
+
+    short = tg._short if not isinstance(tg._short, tg._Short) else None
+    if short is None:
+        tg._short.attention
+        short = tg._short
+    st = [torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2)]
+    monkeypatch.setattr(tg, "_short", Direct())
+    a = calls(st[0])
+    monkeypatch.setattr(tg, "_short", General())
+    b = calls(st[1])
+    assert all(same(p, r) for p, r in zip(a, b))
+    assert torch.equal(st[0], st[1]) and not st[0].any()
+
+
+def test_refusals_name_the_argument():
+    s = paged(2, 3, 4, 2, 64, BF, 16, [20, 5], [3, 3], seed=2)
+    host = sv.PagedCache.from_tensors(s["cache"].k.cpu(), s["cache"].v.cpu())
+    k = torch.ones(2, 3, 2, 64, dtype=BF, device="cuda")
+    table = sv.rotary_table(64, 64)
+    at = lambda **kw: sv.paged_attention(**{**dict(q=s["q"], cache=s["cache"], page_table=s["table"],
+                                                   cache_lens=s["lens"]), **kw})
+    ro = lambda **kw: sv.rotate_append(**{**dict(q=s["q"], k=k, v=k, table=table, cache=s["cache"],
+                                                 page_table=s["table"], cache_lens=s["lens"]), **kw})
+    for call in (at, ro):
+        for kw, error in ((dict(cache=host), ValueError), (dict(q=s["q"].to(HF)), TypeError),
+                          (dict(q=s["q"][:1]), ValueError), (dict(page_table=s["table"][:1]), ValueError),
+                          (dict(out=torch.empty(2, 3, 4, 64, device="cuda")), ValueError),
+                          (dict(row_status=torch.zeros(2, device="cuda")), ValueError)):
+            with pytest.raises(error):
+                call(**kw)
+    for kw in (dict(window=-1), dict(window="a"), dict(window=1.5), dict(scale="a"), dict(scale=math.nan),
+               dict(q=s["q"][:, :, :3])):
+        with pytest.raises((ValueError, TypeError, struct.error, sv.SpecVerifyError)):
+            at(**kw)
+    with pytest.raises(TypeError):
+        ro(v=k.to(HF))
+    with pytest.raises(ValueError):
+        ro(table=table.double())
+    x = torch.zeros(2, 3, 100, device="cuda")
+    h = sv.TokenHistory(2, 99)
+    for kw in (dict(history=h), dict(mask=torch.zeros(2, 3, device="cuda")), dict(out=x.to(BF)),
+               dict(mask=torch.zeros(2, 2, 4, dtype=torch.int32, device="cuda")),
+               dict(draft_tokens=torch.zeros(2, 1, dtype=torch.int32, device="cuda")),
+               dict(row_status=torch.zeros(3, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            sv.process_logits(x, **kw)
+    torch.cuda.synchronize()
