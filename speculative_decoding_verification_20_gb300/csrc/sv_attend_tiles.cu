@@ -43,15 +43,16 @@ namespace {
 constexpr int kTThreads = 384;
 constexpr int kBadSlots = 16;  // units that the loader can be ahead by, and more
 
-template <int D>
+template <int D, bool SPLIT>
 struct TilesCfg {
     static constexpr int kTileBytes = kKeyTile * D * 2;
     static constexpr int kQBytes = 256 * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kWBytes = SPLIT ? 0 : 2 * 128 * kKeyTile * 2;  // weights of the two tiles
+    static constexpr int kStages = D == 64 ? 8 : SPLIT ? 5 : 3;
     static constexpr int kHalves = D / 64;                // 128-byte columns of a tile
     static constexpr int kHalfBytes = kKeyTile * 128;     // 128 rows of one
-    static constexpr int kSmem = kQBytes + kStages * kTileBytes + 1024;  // and room to align
-    // tensor memory columns: scores (and weights) of the two tiles, then their outputs
+    static constexpr int kSmem = kQBytes + kWBytes + kStages * kTileBytes + 1024;  // and room to align
+    // tensor memory columns: scores (SPLIT: and weights) of the two tiles, then their outputs
     static constexpr int kS = 0, kO = 256;
 };
 
@@ -168,7 +169,7 @@ template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(kTThreads, 1)
     attend_tiles_kernel(const __grid_constant__ TilesArgs ta, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
-    using C = TilesCfg<D>;
+    using C = TilesCfg<D, SPLIT>;
     constexpr int RM = SPLIT ? 128 : 256;
     constexpr int STEP = SPLIT ? 2 : 1;  // key tiles from one of a half's to the next
     const AttendArgs& p = ta.p;
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     // swizzled tiles start on 1024-byte boundaries
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* smem_p = smem_raw + (smem - smem_u32(smem_raw));
-    const uint32_t q_s = smem, ring_s = smem + C::kQBytes;
+    const uint32_t q_s = smem, w_s = smem + C::kQBytes, ring_s = w_s + C::kWBytes;
     if (t == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             bar_init(&s_full[s], 1);
@@ -261,10 +262,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     ++n_scores;
                     fence_after();
                     if (wr0 >= rows) {  // no rows: their lanes' products go nowhere
+                        // (not SPLIT: these scores can be there before the others' weights of the
+                        // tile before, whose phase this warp must not enter twice)
+                        if (tile != start) {
+                            if (!SPLIT) alive = bar_wait(&s_out[x], n_out & 1, limit, dead);
+                            ++n_out;
+                        }
                         fence_before();
                         bar_arrive(&s_weights[x][0]);
                         bar_arrive(&s_weights[x][1]);
-                        if (tile != start) ++n_out;
                         continue;
                     }
                     // The scores of 128 keys, as two halves.  The second is read for the maximum, and
@@ -299,16 +305,24 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     top[2] = max3(top[2], s1[62], s1[63]);
                     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.qscale;
                     bool out_seen = tile == start;
+                    if (!SPLIT && tile != start) {  // the product before this one has read its weights
+                        alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
+                        if (!alive) break;
+                        out_seen = true;
+                        fence_after();
+                    }
                     if (tile == start) {
                         ref = m;
                     } else if (__any_sync(0xFFFFFFFFu, m > ref + 8.0f)) {
                         // raise the reference; the output so far shrinks by as much
                         const float now = fmaxf(ref, m);
                         const float f = now == -INFINITY ? 1.0f : fast_exp2(ref - now);
-                        alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);  // the product before this one
-                        if (!alive) break;
-                        out_seen = true;
-                        fence_after();
+                        if (SPLIT) {
+                            alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);  // the product before this one
+                            if (!alive) break;
+                            out_seen = true;
+                            fence_after();
+                        }
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float o[16];
@@ -317,31 +331,47 @@ __global__ void __launch_bounds__(kTThreads, 1)
                             for (int j = 0; j < 16; ++j) o[j] *= f;
                             tmem_store16(tO + c, reinterpret_cast<const uint32_t*>(o));
                         }
+                        if (!SPLIT) tmem_store_wait();
                         sum *= f;
                         ref = now;
                     }
                     const float base = ref == -INFINITY ? 0.0f : ref;  // nothing visible yet: weights 0
                     const float2 qs = make_float2(p.qscale, p.qscale), mb = make_float2(-base, -base);
                     float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    auto weigh = [&](const float* x, int c) {  // 32 keys, the c-th such set of the tile
+                    auto weigh = [&](const float* v, int c) {  // 32 keys, the c-th such set of the tile
                         uint32_t w[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            float2 e = fma2(make_float2(x[2 * j], x[2 * j + 1]), qs, mb);
+                            float2 e = fma2(make_float2(v[2 * j], v[2 * j + 1]), qs, mb);
                             e.x = fast_exp2(e.x);
                             e.y = fast_exp2(e.y);
                             add[j & 1] = add2(add[j & 1], e);
                             w[j] = Pair<T>::pack(e.x, e.y);  // 16 bits into the product, as the values
                         }
-                        tmem_store16(tS + c * 16, w);
+                        if constexpr (SPLIT) {
+                            tmem_store16(tS + c * 16, w);
+                        } else {
+                            unsigned char* dst =
+                                smem_p + C::kQBytes + x * (C::kWBytes / 2) + (c >> 1) * (128 * 128) + row * 128;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                *reinterpret_cast<uint4*>(dst + ((((c & 1) * 4 + j) ^ (row & 7)) << 4)) =
+                                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                        }
+                    };
+                    auto handed = [&](uint64_t* bar) {  // the weights so far are where their product reads them
+                        if constexpr (SPLIT)
+                            tmem_store_wait();
+                        else
+                            fence_async_smem();
+                        fence_before();
+                        bar_arrive(bar);
                     };
                     weigh(s0, 0);
                     tmem_start64(tS + 64, w1);
                     weigh(s0 + 32, 1);
                     tmem_wait64(w1);
-                    tmem_store_wait();  // half of the weights: their product can start
-                    fence_before();
-                    bar_arrive(&s_weights[x][0]);
+                    handed(&s_weights[x][0]);  // their product can start, and the scores may be written over
                     if (cut) {
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
@@ -349,15 +379,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     }
                     weigh(s1, 2);
                     weigh(s1 + 32, 3);
-                    tmem_store_wait();
-                    fence_before();
-                    bar_arrive(&s_weights[x][1]);
+                    handed(&s_weights[x][1]);
                     add[0] = add2(add[0], add[1]);
                     sum += add[0].x + add[0].y;
                     // These scores came after the product before them, in one warp's order, so that
                     // phase of s_out is over: the wait at the unit's end is for the one after it.
                     // (Waiting for every phase here costs 2%.)
-                    if (!out_seen) ++n_out;
+                    if (SPLIT && !out_seen) ++n_out;
                 }
                 if (left > 0) next_unit<RM>(p, next);
                 if (alive && start < end) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
@@ -506,7 +534,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     }
                     for (int tile = start; alive && tile < end; tile += STEP, i += 2 * STEP) {
                         const bool more = tile + STEP < end;
-                        alive = reach(i + 1);
+                        if (!SPLIT) {
+                            // the next scores, as soon as these are read: they are there when the
+                            // softmax ends
+                            if (more) alive = bar_wait(&s_full[stage], turn, limit, dead);
+                            alive = alive && bar_wait(&s_weights[x][0], n_w & 1, limit, dead);
+                            if (alive && more) scores(q_desc, tile + 2 >= end, q_place);
+                            alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
+                        } else {
+                            alive = reach(i + 1);
+                        }
                         if (!alive) break;
                         const uint32_t vstage = stage, vs = ring_s + stage * C::kTileBytes;
                         next_place();
@@ -526,17 +563,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
                             fence_async_smem();
                             __syncwarp();
                         }
-                        if (!SPLIT && more) alive = reach(i + 2);  // the next keys, while the softmax runs
                         const uint32_t v_desc = uniform(desc_values(vs, C::kHalfBytes));
+                        const uint32_t w_desc = uniform(desc_keys(w_s + x * (C::kWBytes / 2)));
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
-                            alive = alive && bar_wait(&s_weights[x][half], n_w & 1, limit, dead);
+                            if (SPLIT || half) alive = alive && bar_wait(&s_weights[x][half], n_w & 1, limit, dead);
                             if (!alive) break;
                             fence_after();
                             if (elect()) {
 #pragma unroll
-                                for (int k = half * 4; k < half * 4 + 4; ++k)
-                                    mma_ts(tO, tS + k * 8, v_desc + k * (16 * 128 >> 4), i_o, tile > start || k > 0);
+                                for (int k = half * 4; k < half * 4 + 4; ++k) {
+                                    const uint32_t b = v_desc + k * (16 * 128 >> 4);
+                                    const bool add = tile > start || k > 0;
+                                    if constexpr (SPLIT)
+                                        mma_ts(tO, tS + k * 8, b, i_o, add);
+                                    else
+                                        mma_ss(tO, w_desc + (((k / 4) * (128 * 128) + (k % 4) * 32) >> 4), b, i_o, add);
+                                }
                                 if (half) {
                                     mma_commit(&s_out[x]);
                                     mma_commit(&s_empty[vstage]);
@@ -546,8 +589,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         }
                         if (!alive) break;
                         ++n_w;
-                        if (more) {
-                            if (SPLIT) alive = reach(i + 2 * STEP);
+                        if (SPLIT && more) {
+                            alive = reach(i + 2 * STEP);
                             if (alive) scores(q_desc, tile + 2 * STEP >= end, q_place);
                         }
                     }
@@ -611,31 +654,53 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 }
                 return false;
             };
+            auto mark = [&](bool bad) {  // a tile with a bad page
+                if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) {
+                    *(volatile int*)&s_bad[index % kBadSlots] = 1;
+                    if (p.a.row_status) atomicOr(p.a.row_status + u.b, SV_ROW_BAD_PAGE);
+                    __threadfence_block();
+                }
+            };
             int page, in_page;
             bool bad = find(u, tile, page, in_page);
             while (alive && left > 0) {
                 const int end = min(u.t1, tile + left);
+                left -= end - tile;
                 if (lane == 0) s_bad[index % kBadSlots] = 0;
                 __syncwarp();
                 Unit next = u;
-                if (left > end - tile) next_unit<RM>(p, next);
-                for (; alive && tile < end; ++tile, --left) {
-                    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) {
-                        *(volatile int*)&s_bad[index % kBadSlots] = 1;
-                        if (p.a.row_status) atomicOr(p.a.row_status + u.b, SV_ROW_BAD_PAGE);
-                        __threadfence_block();
-                    }
-                    // the next tile's pages are looked up while this one's copies run
-                    int page1 = no_page, in_page1 = 0;
-                    bad = false;
+                if (left > 0) next_unit<RM>(p, next);
+                // the next tiles' pages are looked up while this one's copies run
+                int page1 = no_page, in_page1 = 0;
+                bool bad1 = false;
+                if (!SPLIT) {  // keys are one tile ahead of the values
+                    mark(bad);
                     put(&kmap, u.h, page, in_page);
-                    if (tile + 1 < end)
-                        bad = find(u, tile + 1, page1, in_page1);
-                    else if (left > 1)
-                        bad = find(next, next.t0, page1, in_page1);
+                    if (tile + 1 < end) bad1 = find(u, tile + 1, page1, in_page1);
+                }
+                for (; alive && tile < end; ++tile) {
+                    int page2 = no_page, in_page2 = 0;
+                    bool bad2 = false;
+                    if (!SPLIT && tile + 1 < end) {
+                        mark(bad1);
+                        put(&kmap, u.h, page1, in_page1);
+                    }
+                    if (SPLIT) {
+                        mark(bad);
+                        put(&kmap, u.h, page, in_page);
+                    }
+                    const int ahead = tile + (SPLIT ? 1 : 2);
+                    if (ahead < end)
+                        bad2 = find(u, ahead, page2, in_page2);
+                    else if (left > 0 && tile + 1 == end)
+                        bad2 = find(next, next.t0, page2, in_page2);
                     put(&vmap, u.h, page, in_page);
-                    page = page1;
-                    in_page = in_page1;
+                    if (!SPLIT && tile + 1 < end) {
+                        page = page1, in_page = in_page1;
+                        page1 = page2, in_page1 = in_page2, bad1 = bad2;
+                    } else {
+                        page = page2, in_page = in_page2, bad = bad2;
+                    }
                 }
                 ++index;
                 u = next;
@@ -697,7 +762,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
 template <typename T, int D, bool SPLIT>
 cudaError_t launch_tiles(const AttendArgs& p, cudaStream_t s) {
-    constexpr int bytes = TilesCfg<D>::kSmem;
+    constexpr int bytes = TilesCfg<D, SPLIT>::kSmem;
     TilesArgs ta;
     ta.p = p;
     ta.box = 16;
