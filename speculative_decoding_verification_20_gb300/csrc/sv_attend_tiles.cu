@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
             bar_init(&s_empty[s], 2);  // both halves, whether or not they read the stage
         }
         for (int x = 0; x < 2; ++x) {
-            bar_init(&s_q[x], 1);
-            bar_init(&s_q_free[x], SPLIT ? 2 : 1);
+            bar_init(&s_q[x], SPLIT ? 1 : 128);
+            bar_init(&s_q_free[x], 2);
             bar_init(&s_scores[x], 1);
             bar_init(&s_weights[x][0], 128);
             bar_init(&s_weights[x][1], 128);
@@ -239,6 +239,27 @@ __global__ void __launch_bounds__(kTThreads, 1)
         int first = part.tile, left = part.todo, index = 0;
         uint32_t n_scores = 0, n_out = 0;  // phases seen
         bool alive = true;
+        // !SPLIT: the warp's 32 query rows of a unit, into shared memory as the products read them.  (One warp for
+        // all 256 rows took 5000 cycles a half; here a unit's rows come while its predecessor ends.)
+        bool q_there = false;
+        auto load_q = [&](const Unit& w) {
+            constexpr int RC = D / 8, RS = 32 / RC;  // 16-byte pieces of a row, rows a step
+            const int c = lane % RC, r0 = (warp & 3) * 32, count = w.n * p.group;
+            const uint32_t dst = q_s + x * 128 * D * 2 + (c >> 3) * C::kHalfBytes;
+#pragma unroll 4
+            for (int i = r0 + lane / RC; i < r0 + 32; i += RS) {  // (rows past the last are computed and dropped)
+                const T* src = q_row<T>(p, w.b, w.h, min(w.rt * RM + x0 + i, count - 1)) + c * 8;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
+                             "l"(src)
+                             : "memory");
+            }
+            q_there = true;
+        };
+        auto hand_q = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            bar_arrive(&s_q[x]);
+        };
 
         while (left > 0) {
             const int rows = u.n * p.group, r = u.rt * RM + x0 + row;
@@ -246,7 +267,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const bool whole = first == u.t0 && end == u.t1;
             left -= end - first;
             Unit next = u;
+            bool ahead = false;  // next is the next unit
             if (SPLIT || u.rt * RM + x0 < rows) {  // the tile has rows
+                if (!SPLIT && !q_there) {
+                    load_q(u);
+                    hand_q();
+                }
+                q_there = false;
                 const int start = first + (SPLIT ? x : 0);
                 const int pos = u.past + by_group(p, min(r, rows - 1));
                 // of the warp's rows: the least and the greatest position; or there is none
@@ -261,6 +288,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     if (!alive) break;
                     ++n_scores;
                     fence_after();
+                    if (!SPLIT && tile + 1 == end && left > 0) {  // the unit's last scores: its queries are read
+                        next_unit<RM>(p, next);
+                        ahead = true;
+                        if (next.rt * RM + x0 < next.n * p.group) load_q(next);
+                    }
                     if (wr0 >= rows) {  // no rows: their lanes' products go nowhere
                         // (not SPLIT: these scores can be there before the others' weights of the
                         // tile before, whose phase this warp must not enter twice)
@@ -387,7 +419,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     // (Waiting for every phase here costs 2%.)
                     if (SPLIT && !out_seen) ++n_out;
                 }
-                if (left > 0) next_unit<RM>(p, next);
+                if (q_there) hand_q();
+                if (left > 0 && !ahead) next_unit<RM>(p, next);
                 if (alive && start < end) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
                 if (SPLIT && x == 1) {
                     s_ml[row] = make_float2(ref, sum);
@@ -507,7 +540,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     }
                     mma_commit(&s_scores[x]);
                     mma_commit(&s_empty[stage]);
-                    if (last) mma_commit(&s_q_free[place]);
+                    if (SPLIT && last) mma_commit(&s_q_free[place]);
                 }
                 __syncwarp();
                 next_place();
@@ -529,7 +562,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         alive = bar_wait(&s_q[q_place], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
                         alive = alive && reach(i);
                         if (alive) scores(q_desc, start + STEP >= end, q_place);
-                    } else if (lane == 0) {
+                    } else if (SPLIT && lane == 0) {
                         bar_arrive(&s_q_free[q_place]);
                     }
                     for (int tile = start; alive && tile < end; tile += STEP, i += 2 * STEP) {
@@ -714,11 +747,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 if (stage == C::kStages - 1) turn ^= 1;
                 while (!bar_try(&s_full[stage], turn) && now_ns() - t0 < kWaitLimitNs) {}
             }
-        } else {
+        } else if (SPLIT) {
             // ---------------------------------------------------------- queries
-            // A unit's rows into shared memory, swizzled as the products read them: 128 rows
-            // for each half, or (SPLIT) for both, in two places in turn.  A place is free when
-            // the last scores of what it held are through.
+            // A unit's 128 rows into shared memory, swizzled as the products read them, in two
+            // places in turn.  A place is free when the last scores of what it held are through.
             Unit u = part.u;
             int first = part.tile, left = part.todo, index = 0;
             uint32_t n_free[2] = {0, 0};
@@ -727,25 +759,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const int c = lane % RC, sub = lane / RC;
             while (alive && left > 0) {
                 const int rows = u.n * p.group;
-                for (int x = 0; alive && x < (SPLIT ? 1 : 2); ++x) {
-                    const int r0 = u.rt * RM + x * 128, place = SPLIT ? index & 1 : x;
-                    if (r0 >= rows) break;
-                    if (n_free[place]++ > 0) alive = bar_wait(&s_q_free[place], n_free[place] & 1, limit, dead);
-                    if (!alive) break;
-                    const uint32_t dst = q_s + place * 128 * D * 2 + (c >> 3) * C::kHalfBytes;
+                const int r0 = u.rt * RM, place = index & 1;
+                if (n_free[place]++ > 0) alive = bar_wait(&s_q_free[place], n_free[place] & 1, limit, dead);
+                if (!alive) break;
+                const uint32_t dst = q_s + place * 128 * D * 2 + (c >> 3) * C::kHalfBytes;
 #pragma unroll 4
-                    for (int i = sub; i < 128; i += RS) {  // (rows past the last are computed and dropped)
-                        const T* src = q_row<T>(p, u.b, u.h, min(r0 + i, rows - 1)) + c * 8;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                         dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
-                                     "l"(src)
-                                     : "memory");
-                    }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(&s_q[place]);
+                for (int i = sub; i < 128; i += RS) {  // (rows past the last are computed and dropped)
+                    const T* src = q_row<T>(p, u.b, u.h, min(r0 + i, rows - 1)) + c * 8;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     dst + i * 128 + (((c & 7) ^ (i & 7)) << 4)),
+                                 "l"(src)
+                                 : "memory");
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&s_q[place]);
                 const int end = min(u.t1, first + left);
                 left -= end - first;
                 ++index;
