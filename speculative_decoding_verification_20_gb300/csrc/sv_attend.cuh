@@ -104,18 +104,17 @@ __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = (int)p.a.B, c = blockIdx.x;
     const int Hkv = (int)p.a.kv_heads;
     // key tiles of one head of sequence b, by a thread alone or by a warp
-    auto alone = [&](int b) -> int {
-        const SeqLens s = seq_lens(p.a.cache, b, (int)p.a.N, p.capacity);
+    auto alone = [&](const SeqLens s) -> int {
         int n = 0;
         for (int rt = row_tiles<RM>(p, s.n); rt-- > 0;) n += tile_count<RM>(p, s.past, s.n, rt);
         return n;
     };
-    auto by_warp = [&](int b) -> int {
-        const SeqLens s = seq_lens(p.a.cache, b, (int)p.a.N, p.capacity);
+    auto by_warp = [&](const SeqLens s) -> int {
         int n = 0;
         for (int rt = lane; rt < row_tiles<RM>(p, s.n); rt += 32) n += tile_count<RM>(p, s.past, s.n, rt);
         return warp_sum(n);
     };
+    auto lens = [&](int b) -> SeqLens { return seq_lens(p.a.cache, b, (int)p.a.N, p.capacity); };
     auto scan = [&](long long own) -> long long {  // inclusive, over the warp
         long long x = own;
 #pragma unroll
@@ -144,16 +143,25 @@ __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
     int seq = 0, per_head = 0;
     long long before_seq = 0;
     const bool many_rows = p.max_row_tiles > 4;
+    SeqLens s;  // of the first unit's sequence
     if (many_rows ? B * ((p.max_row_tiles + 31) / 32) <= 16 : B <= 32) {
         // a small batch: every warp by itself, with no barrier
+        // (a lane a sequence: the lengths of all come in one wait)
+        const SeqLens held = lens(min(lane, B - 1));
+        auto of = [&](int b) -> SeqLens {
+            SeqLens x = held;
+            x.past = __shfl_sync(0xFFFFFFFFu, held.past, b);
+            x.n = __shfl_sync(0xFFFFFFFFu, held.n, b);
+            return x;
+        };
         int mine = 0;
         if (many_rows) {
             for (int b = 0; b < B; ++b) {
-                const int n = by_warp(b);
+                const int n = by_warp(of(b));
                 if (lane == b) mine = n;
             }
         } else {
-            mine = alone(min(lane, B - 1));  // by every lane: the warp stays together for the scan
+            mine = alone(held);  // by every lane: the warp stays together for the scan
             if (lane >= B) mine = 0;
         }
         __syncwarp();
@@ -162,12 +170,13 @@ __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
         seq = __ffs(__ballot_sync(0xFFFFFFFFu, upto > begin)) - 1;
         before_seq = __shfl_sync(0xFFFFFFFFu, upto - own, seq);
         per_head = __shfl_sync(0xFFFFFFFFu, mine, seq);
+        s = of(seq);
     } else {
         auto head_tiles = [&](int b0) -> int {  // of sequence b0 + t
-            if (!many_rows) return b0 + t < B ? alone(b0 + t) : 0;
+            if (!many_rows) return b0 + t < B ? alone(lens(b0 + t)) : 0;
             __syncthreads();
             for (int i = warp; i < NT && b0 + i < B; i += NT / 32) {
-                const int n = by_warp(b0 + i);
+                const int n = by_warp(lens(b0 + i));
                 if (lane == 0) s_tiles[i] = n;
             }
             __syncthreads();
@@ -207,11 +216,11 @@ __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
         seq = s_seq;
         before_seq = s_before;
         per_head = s_tiles[0];
+        s = lens(seq);
     }
     // then the head and the row tile
     Unit& u = part.u;
     u.b = seq;
-    const SeqLens s = seq_lens(p.a.cache, u.b, (int)p.a.N, p.capacity);
     u.past = s.past;
     u.n = s.n;
     const long long off = begin - before_seq;
