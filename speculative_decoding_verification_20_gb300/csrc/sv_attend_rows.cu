@@ -11,7 +11,7 @@
 // pass over the keys) and its own output in registers.  The ring runs on over the borders
 // of units; at the end of a unit the groups' results are joined in shared memory.
 //
-// 64 sequences of 1.5-8k keys, 8 tokens each (32 / 8 heads of 128, bf16): 236 us, 5.5 TB/s
+// 64 sequences of 1.5-8k keys, 8 tokens each (32 / 8 heads of 128, bf16): 234 us, 5.5 TB/s
 // of keys and values, 0.82 of the copy rate; the rest is the units' ends and the start.
 // (Warps that filled their own rings by 16-byte copies spent 885 instructions on a block,
 // half of them on addresses, and reached 3.7 TB/s; with one loading warp it was 3.4 TB/s.)

@@ -5,29 +5,35 @@
 // (tcgen05): a unit is 256 query rows, two tiles of 128 that share every key tile of 128
 // keys.  Twelve warps, one job each:
 //   warps 0-3, 4-7  the softmax of one row tile each, a thread a row: scores from tensor
-//                   memory, weights back to it (in place of the scores), output rows at the end
-//   warps 8, 10     issue the products of one row tile each: S = Q K^T from shared memory,
-//                   O += P V with P from tensor memory
+//                   memory, weights to shared memory, output rows at the end; and the
+//                   queries of the next unit, fetched behind the last scores of this one
+//   warps 8, 10     issue the products of one row tile each: S = Q K^T and O += P V, operands
+//                   in shared memory
 //   warp 9          loads keys and values by TMA, page by page, into a ring
-//   warp 11         loads the next unit's queries while this one's ends
-// While one tile's softmax runs, the products of the other fill the tensor cores:
-// PV and the next S of tile A, then those of tile B.  The output stays in tensor memory
+// The scores are read by the time half of the weights are there; then the next S is issued,
+// so that it is done when the softmax ends, and the output's product needs the tensor cores
+// only while the next softmax looks for its maximum.  The output stays in tensor memory
 // over all keys; the running maximum it refers to is only raised when a row's scores
 // outgrow it by 2^8, so that rescaling the output is rare.  Weights of up to 2^8 lose
 // nothing in the 16-bit types' relative step, and sums are 32-bit.
+//
+// Up to 128 rows (SPLIT) the loads bound the call, and the room goes to the ring: the
+// weights lie over their scores in tensor memory, and warp 11 loads the queries.
 //
 // Pages become boxes of gcd(page_size, 128) keys x 64 elements.  A box with no visible
 // key, or on a bad page, is loaded from past the last page, where TMA gives zeros: its
 // scores are masked, and its values add nothing.  Rows of a box past the sequence's end
 // are zeroed in shared memory before their product, since they may hold anything.
 //
-// Two chunks of 2048 tokens behind 4-6k keys (32 / 8 heads of 128, bf16): 331 us, 1200
-// TFLOP/s.  What bounds it is the round of one tile: scores -> softmax (about 1650 cycles, of
-// which 512 are the exponential unit's) -> weights -> PV and the next S (780 cycles of
-// products) -> scores, 3400 cycles in all with the hand-overs, while the two tiles' products
-// fill 2080 of them.  Tried and slower: steps of 64 keys with the scores two steps ahead (365
-// us: the step's fixed costs double), two threads a row (376 us), registers moved from the
-// other warps to the softmax (340 us: the warps that issue products then spill).
+// Two chunks of 2048 tokens behind 4-6k keys (32 / 8 heads of 128, bf16): 305 us, 1310
+// TFLOP/s, 0.69 of the measured rate.  What bounds it is the softmax: some 2900 cycles for
+// two tiles of 128 x 128 (2600 with heads of 64), of which the exponential unit fills 1024
+// and the tiles' products 2080; it waits for nothing else.  The start and the units' ends
+// are a tenth.  Tried and slower: weights over the scores for these units too (337 us: the
+// next S waits for the output's product), room for the weights of 64 keys and one more stage
+// (308 us, and 403 with the next S ahead of the output's product), steps of 64 keys (365 us
+// of then 331), two threads a row (376), registers moved from the other warps to the softmax
+// (340: the warps that issue products then spill).
 //
 // Every wait has a limit.  When one runs out, the CTA writes NaN for what is left of its
 // part, sets SV_ROW_INTERNAL, lets its copies and products finish (with a limit) and ends.
