@@ -10,7 +10,13 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
 
-// rows of a cache head's tile: 16, 32 or 128 where that holds a sequence's rows, else 256
+// Rows of a cache head's tile: 16, 32 or 128 where that holds a sequence's rows, else 256.
+// A tile too small reads the cache once more, one too large computes rows that are not
+// there.  64 sequences behind 4096 (8 cache heads of 128), us with tiles of 16 / 32 / 128 / 256:
+//    16 rows   175 /  180 / 199 / 204        36 rows   490 / 349 / 211 / 217
+//    20 rows   331 /  186 / 199 / 204       128 rows  1278 / 697 / 224 / 228
+//    32 rows   333 /  190 / 201 / 204       132 rows  1437 / 859 / 398 / 239
+// (Of calls of some 20 us, 36 rows take 14.7 us in tiles of 32 and 18.0 in one of 128.)
 int row_tile(int64_t N, int64_t group) {
     const int64_t rows = N * group;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
