@@ -31,9 +31,10 @@
 // and the tiles' products 2080; it waits for nothing else.  The start and the units' ends
 // are a tenth.  Tried and slower: weights over the scores for these units too (337 us: the
 // next S waits for the output's product), room for the weights of 64 keys and one more stage
-// (308 us, and 403 with the next S ahead of the output's product), steps of 64 keys (365 us
-// of then 331), two threads a row (376), registers moved from the other warps to the softmax
-// (340: the warps that issue products then spill).
+// (308 us, and 403 with the next S ahead of the output's product), two threads a row (451: the output's
+// product then stands between one softmax and the next), and before that steps of 64 keys (365
+// us of then 331), and registers moved from the other warps to the softmax (340: the warps
+// that issue products then spill).
 //
 // Every wait has a limit.  When one runs out, the CTA writes NaN for what is left of its
 // part, sets SV_ROW_INTERNAL, lets its copies and products finish (with a limit) and ends.
