@@ -31,9 +31,9 @@
 // and the tiles' products 2080; it waits for nothing else.  The start and the units' ends
 // are a tenth.  Tried and slower: weights over the scores for these units too (337 us: the
 // next S waits for the output's product), room for the weights of 64 keys and one more stage
-// (308 us, and 403 with the next S ahead of the output's product), two threads a row (451: the output's
-// product then stands between one softmax and the next), and before that steps of 64 keys (365
-// us of then 331), and registers moved from the other warps to the softmax (340: the warps
+// (308 us, and 403 with the next S ahead of the output's product), two threads a row (451: the
+// output's product then stands between one softmax and the next), and before that steps of
+// 64 keys (365 us of then 331) and registers moved from the other warps to the softmax (340: the warps
 // that issue products then spill).
 //
 // Every wait has a limit.  When one runs out, the CTA writes NaN for what is left of its
@@ -421,9 +421,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     handed(&s_weights[x][1]);
                     add[0] = add2(add[0], add[1]);
                     sum += add[0].x + add[0].y;
-                    // These scores came after the product before them, in one warp's order, so that
-                    // phase of s_out is over: the wait at the unit's end is for the one after it.
-                    // (Waiting for every phase here costs 2%.)
+                    // SPLIT: these scores came after the product before them, in one warp's order, so
+                    // that phase of s_out is over: the wait at the unit's end is for the one after it.
                     if (SPLIT && !out_seen) ++n_out;
                 }
                 if (q_there) hand_q();
