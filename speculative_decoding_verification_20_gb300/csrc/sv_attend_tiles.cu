@@ -562,13 +562,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     const int vend = u.past + u.n;
                     const uint32_t q_desc = uniform(desc_keys(q_s + q_place * 128 * D * 2));
                     uint32_t i = at + 2 * (start - first);
+                    // SPLIT: a half waits for the queries of every unit, also of one whose single
+                    // tile is the other's, and frees their place only then.  So nobody frees a place
+                    // twice while the other half has yet to read it, and nobody is a phase of s_q
+                    // ahead: a parity only tells a barrier's last two phases apart.  The place is
+                    // written again when both have freed it, so the unit's count gives the phase.
+                    alive = bar_wait(&s_q[q_place], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
                     if (start < end) {
-                        // SPLIT: a place of the queries is written again when both halves have
-                        // freed it, so the unit's count gives the phase
-                        alive = bar_wait(&s_q[q_place], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
                         alive = alive && reach(i);
                         if (alive) scores(q_desc, start + STEP >= end, q_place);
-                    } else if (SPLIT && lane == 0) {
+                    } else if (SPLIT && alive && lane == 0) {
                         bar_arrive(&s_q_free[q_place]);
                     }
                     for (int tile = start; alive && tile < end; tile += STEP, i += 2 * STEP) {
