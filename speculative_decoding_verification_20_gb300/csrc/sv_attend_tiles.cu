@@ -100,6 +100,8 @@ __device__ __forceinline__ bool elect() {
     return one;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+// (a warp that gives up says so before it arrives anywhere)
+__device__ __forceinline__ bool none_gave_up(volatile int* dead) { return !__any_sync(0xFFFFFFFFu, *dead); }
 // two 32-bit operations in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -288,8 +290,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 const int pos0 = u.past + by_group(p, min(wr0, rows - 1));
                 const int pos1 = u.past + by_group(p, min(wr0 + 31, rows - 1));
                 float ref = -INFINITY, sum = 0.0f;
-                // the first half has to be through with what the second left of the unit before
-                if (SPLIT && x == 1 && index > 0) alive = alive && bar_wait(&s_joined, (index - 1) & 1, limit, dead);
+                // The first half has to be through with what the second left of the unit before.
+                // Warps that gave up a wait still arrive, here and on s_second, for every unit that
+                // is left, so after these two waits a warp looks whether one has: a phase of theirs
+                // alone may be over before the others have done their part of it.
+                if (SPLIT && x == 1 && index > 0)
+                    alive = alive && bar_wait(&s_joined, (index - 1) & 1, limit, dead) && none_gave_up(dead);
                 for (int tile = start; alive && tile < end; tile += STEP) {
                     alive = bar_wait(&s_scores[x], n_scores & 1, limit, dead);
                     if (!alive) break;
@@ -429,13 +435,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 if (left > 0 && !ahead) next_unit<RM>(p, next);
                 if (alive && start < end) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
                 if (SPLIT && x == 1) {
-                    s_ml[row] = make_float2(ref, sum);
+                    if (alive) s_ml[row] = make_float2(ref, sum);  // (else the unit before may be read from it yet)
                     fence_before();
                     bar_arrive(&s_second);
                 } else {
                     float f0 = 1.0f, f1 = 0.0f;  // of the two halves' outputs
                     if (SPLIT) {
-                        alive = alive && bar_wait(&s_second, index & 1, limit, dead);
+                        alive = alive && bar_wait(&s_second, index & 1, limit, dead) && none_gave_up(dead);
                         if (alive) {
                             const float2 ml = s_ml[row];
                             const float now = fmaxf(ref, ml.x);

@@ -1,8 +1,8 @@
-"""A model of the barriers between the warps of the attention kernel for up to 128 rows
+"""Models of the barriers between the warps of the attention kernel for up to 128 rows
 (csrc/sv_attend_tiles.cu, SPLIT), run over random lists of units and random speeds of the warps.
 
 A unit's key tiles go to two halves in turn, so that of a unit with one tile the second half has
-none.  The model checks that every product of scores reads its own unit's queries and that the
+none.  The first model checks that every product of scores reads its own unit's queries and that the
 warps come to their end."""
 import random
 
@@ -187,3 +187,72 @@ def test_the_model_finds_a_half_that_does_not_wait(stages):
     # units of two tiles and more are not concerned
     rng = random.Random(1)
     assert all(Cta([rng.randint(2, 5) for _ in range(10)], stages, rng, False).run() == 0 for _ in range(50))
+
+
+class Ends:
+    """The ends of units, where the first half's four softmax warps join what the second half's left, with one warp
+    that gives up a wait somewhere.  A warp that gave up goes on through its units without waiting, and arrives."""
+
+    def __init__(self, units, rng, looks, careful):
+        # looks: after the waits for the other half, whether a warp has given up; careful: what a warp that has gives
+        # to the other half is not written
+        self.units, self.rng, self.looks, self.careful = units, rng, looks, careful
+        self.done = [Bar(4), Bar(4)]  # the weights of a half, and with them its product
+        self.second, self.joined = Bar(4), Bar(4)
+        self.left = [None] * 4        # per warp: the unit whose maximum and sum the second half left
+        self.dead = False
+        self.wrong = 0
+
+    def warp(self, x, w, gives_up):
+        alive = True
+
+        def wait(bar, parity):
+            nonlocal alive
+            if alive and not bar.over(parity):
+                yield lambda: bar.over(parity) or self.dead
+                alive = bar.over(parity)
+                self.dead |= not alive
+
+        for j in range(self.units):
+            if x == 1 and j > 0:
+                yield from wait(self.joined, j - 1)
+                alive = alive and not (self.looks and self.dead)
+            yield None
+            if j == gives_up and alive:
+                alive, self.dead = False, True
+            if alive:
+                self.done[x].arrive()
+            yield from wait(self.done[x], j)
+            if x == 1:
+                if alive or not self.careful:
+                    self.left[w] = j
+                self.second.arrive()
+                continue
+            yield from wait(self.second, j)
+            alive = alive and not (self.looks and self.dead)
+            for _ in range(3 if alive else 0):  # reads it, for a while
+                self.wrong += alive and self.left[w] != j
+                yield None
+            self.joined.arrive()
+
+    def run(self):
+        one = (self.rng.randrange(2), self.rng.randrange(4))
+        at = self.rng.randrange(self.units)
+        live = {self.warp(x, w, at if (x, w) == one else None): None for x in range(2) for w in range(4)}
+        speed = {w: self.rng.choice([1.0, 0.1, 0.01]) for w in live}
+        while live:
+            ready = [w for w, wait in live.items() if wait is None or wait()]
+            w = self.rng.choices(ready, [speed[w] for w in ready])[0]
+            step = next(w, False)
+            if step is False:
+                del live[w]
+            else:
+                live[w] = step
+        return self.wrong
+
+
+def test_a_wait_given_up_leaves_no_wrong_row():
+    rng = random.Random(5)
+    wrong = lambda looks, careful: sum(Ends(rng.randint(1, 10), rng, looks, careful).run() for _ in range(600))
+    assert wrong(True, True) == 0
+    assert wrong(False, True) > 0 and wrong(True, False) > 0  # both are needed
