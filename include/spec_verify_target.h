@@ -41,8 +41,8 @@ extern "C" {
 
 /*
  * Token history.  Per slot (a sequence's place in the server): seen [slots, words], a
- * bit plane, token t at bit t & 31 of word t >> 5, words >= ceil(V / 32); counts
- * [slots, V].  A token of the prompt or the output sets its bit; one of the output
+ * bit plane, token t at bit t & 31 of word t >> 5, words >= ceil(V / 32) (bits from V on
+ * are ignored); counts [slots, V].  A token of the prompt or the output sets its bit; one of the output
  * adds 1 to its count.
  *
  * tokens [B, L] (row stride tokens_stride); of row b the first prompt_lens[b]

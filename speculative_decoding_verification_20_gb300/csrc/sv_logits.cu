@@ -21,8 +21,8 @@ constexpr int kLWarps = kLThreads / 32;
 // biases of one chunk that each warp can hold; a chunk with more re-reads the list
 constexpr int kLBiasCap = 64;
 
-// 32 bits of a bit plane from token e0 on (e0 may be negative or run past the end;
-// those bits are 0)
+// 32 bits of a bit plane from token e0 on (e0 may be negative or run past V; those bits
+// are 0, whatever the plane's last word holds there: the listed tokens come from here)
 __device__ __forceinline__ uint32_t plane_word(const uint32_t* __restrict__ p, int e0, int V) {
     const int i = e0 >> 5, sh = e0 & 31, last = (V - 1) >> 5;
     uint32_t w = (i >= 0 && i <= last) ? __ldg(p + i) : 0u;
@@ -30,6 +30,7 @@ __device__ __forceinline__ uint32_t plane_word(const uint32_t* __restrict__ p, i
         const uint32_t hi = (i + 1 >= 0 && i + 1 <= last) ? __ldg(p + i + 1) : 0u;
         w = __funnelshift_r(w, hi, sh);
     }
+    if (e0 + 32 > V) w = e0 < V ? w & (0xFFFFFFFFu >> (e0 + 32 - V)) : 0u;
     return w;
 }
 
