@@ -183,7 +183,9 @@ int spec_verify_rotate_append(const sv_rotate_args* args, void* stream);
  * max_context: an upper bound of cache_lens + num_new known to the host, or 0 (the
  * page table's width); it only sizes the launch.
  * workspace: spec_verify_attention_workspace_size() bytes, 256-byte aligned, needs
- * no initialisation; calls on one workspace must not overlap.
+ * no initialisation; calls on one workspace must not overlap.  A call enqueues two
+ * kernels that hand over through it: threads that share a workspace (and a stream) must
+ * not be in this function at the same time.
  * wait_limit_ns: limit of a device-side wait (0: 2 s); a call in which one runs
  * out sets SV_ROW_INTERNAL and gives NaN for the rows concerned.
  * A sequence with bad lengths gets NaN rows; so do the rows of a tile that meets a bad

@@ -22,6 +22,7 @@ from __future__ import annotations
 import ctypes
 import math
 import struct
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -140,6 +141,9 @@ def _elsewhere(device: torch.device, stream, fn, args, kwargs):
 
 
 _workspaces: dict = {}
+# A call of spec_verify_attention enqueues two kernels, the second of which joins what the first left in the workspace,
+# and ctypes lets other threads run meanwhile: none may enqueue its own between them.
+_attend_lock = threading.Lock()
 
 
 def _workspace(nbytes: int, device: torch.device, raw: int) -> torch.Tensor:
@@ -461,8 +465,8 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     Token i of sequence b sees the positions up to cache_lens[b] + i, with window > 0 only the last ``window``
     of them.  scale: default 1 / sqrt(dim).  max_context: the host's upper bound of cache_lens + num_new
     (default: the page table's width); it only sizes the launch.  Rows past num_new are zeros.
-    workspace: uint8 of attention_workspace_size() bytes; calls on one must not overlap (default: one kept for each
-    stream, or the graph's own memory while a graph is captured).
+    workspace: uint8 of attention_workspace_size() bytes; calls on one must not overlap on the GPU (default: one kept
+    for each stream, or the graph's own memory while a graph is captured).  Threads may share a stream.
     """
     if stream is None and workspace is None:
         res = _short.attention(q, cache._record, page_table, cache_lens, num_new, scale, window, max_context, out,
@@ -491,12 +495,14 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     new = _vec(num_new, B, torch.int32, dev, "num_new")
     _status(row_status, B, dev)
     lib, raw = _library(), _raw_stream(dev.index)
-    if workspace is None:
-        workspace = _workspace(lib.spec_verify_attention_workspace_size(B, N, Hq, Hkv, D), dev, raw)
     xs, os = x.stride(), o.stride()
-    _check(lib.spec_verify_attention(_ATTENTION.pack(
-        _ATTENTION.size, x.data_ptr(), o.data_ptr(), _DTYPE[dtype], B, N, Hq, Hkv, D, xs[0], xs[1], xs[2],
-        os[0], os[1], os[2], 1.0 / math.sqrt(D) if scale is None else float(scale), window, max_context or 0,
-        *cache._fields, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(), _p(new), workspace.data_ptr(),
-        workspace.numel(), _p(row_status), wait_limit_ns), raw))
+    with _attend_lock:
+        if workspace is None:
+            workspace = _workspace(lib.spec_verify_attention_workspace_size(B, N, Hq, Hkv, D), dev, raw)
+        status = lib.spec_verify_attention(_ATTENTION.pack(
+            _ATTENTION.size, x.data_ptr(), o.data_ptr(), _DTYPE[dtype], B, N, Hq, Hkv, D, xs[0], xs[1], xs[2],
+            os[0], os[1], os[2], 1.0 / math.sqrt(D) if scale is None else float(scale), window, max_context or 0,
+            *cache._fields, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(), _p(new), workspace.data_ptr(),
+            workspace.numel(), _p(row_status), wait_limit_ns), raw)
+    _check(status)
     return o
