@@ -15,7 +15,6 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
-#include <cstddef>
 #include <cstring>
 #include <map>
 #include <utility>
@@ -80,28 +79,27 @@ inline PyObject* done(int status, const at::Tensor& out) {
     return THPVariable_Wrap(out);
 }
 
-// what a PagedCache packs when it is made: the head of sv_paged_cache, then its heads, type and device
-struct cache_record {
-    unsigned char head[80];
-    int64_t kv_heads, dim, code, device;
-};
-static_assert(offsetof(sv_paged_cache, page_table) == sizeof(cache_record::head), "the head of the cache's description");
-
-// false: not such a record, or of another device
-inline bool record(PyObject* o, const at::Device& d, cache_record* r) {
-    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != (Py_ssize_t)sizeof *r) return false;
-    std::memcpy(r, PyBytes_AS_STRING(o), sizeof *r);
-    return r->device == d.index();
+// a PagedCache's keys and values, as they are at this call: [pages, heads, page_size, dim]
+inline bool pages(PyObject* ko, PyObject* vo, const at::Device& d, const at::Tensor** k, const at::Tensor** v) {
+    if (!tensor(ko, k) || !tensor(vo, v)) return false;
+    const at::Tensor &x = **k, &y = **v;
+    const at::ScalarType s = x.scalar_type();
+    return (s == at::kBFloat16 || s == at::kHalf) && on(x, d, s) && on(y, d, s) && x.dim() == 4 && x.sizes() == y.sizes() &&
+           x.size(2) >= 16 && x.size(2) % 16 == 0 && rows(x) && rows(y);
 }
-inline at::ScalarType type_of(const cache_record& r) { return r.code == SV_BF16 ? at::kBFloat16 : at::kHalf; }
-inline void fill(sv_paged_cache* c, const cache_record& r, const at::Tensor& pt, const void* lens, const void* fresh) {
-    std::memcpy(c, r.head, sizeof r.head);
+inline void fill(sv_paged_cache* c, const at::Tensor& k, const at::Tensor& v, const at::Tensor& pt, const void* lens,
+                 const void* fresh) {
+    c->k_pages = k.data_ptr(), c->v_pages = v.data_ptr();
+    c->pages = k.size(0), c->page_size = k.size(2);
+    c->k_stride_page = k.stride(0), c->k_stride_head = k.stride(1), c->k_stride_slot = k.stride(2);
+    c->v_stride_page = v.stride(0), c->v_stride_head = v.stride(1), c->v_stride_slot = v.stride(2);
     c->page_table = pt.data_ptr<int32_t>();
     c->page_table_stride = pt.stride(0);
     c->pages_per_seq = pt.size(1);
     c->cache_lens = (const int32_t*)lens;
     c->num_new = (const int32_t*)fresh;
 }
+inline int64_t code(at::ScalarType s) { return s == at::kBFloat16 ? SV_BF16 : SV_F16; }
 
 // scratch of the calls on one stream, which follow one another
 at::Tensor& scratch(const at::Device& d, void* stream, int64_t bytes) {
@@ -111,32 +109,31 @@ at::Tensor& scratch(const at::Device& d, void* stream, int64_t bytes) {
     return t;
 }
 
-// attention(q, cache record, page_table, cache_lens, num_new, scale (None: the default), window, max_context, out,
+// attention(q, cache's k, v, page_table, cache_lens, num_new, scale (None: the default), window, max_context, out,
 //           row_status, wait_limit_ns)
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    const at::Tensor *q, *pt, *given = nullptr;
-    if (n != 11 || !tensor(a[0], &q) || q->dim() != 4) SV_NONE;
+    const at::Tensor *q, *ck, *cv, *pt, *given = nullptr;
+    if (n != 12 || !tensor(a[0], &q) || q->dim() != 4) SV_NONE;
     const at::Device d = q->device();
     const int64_t B = q->size(0), N = q->size(1), Hq = q->size(2), D = q->size(3);
-    cache_record r;
-    if (!current(d) || !record(a[1], d, &r)) SV_NONE;
-    const int64_t Hkv = r.kv_heads;
-    const at::ScalarType s = type_of(r);
-    if (q->scalar_type() != s || D != r.dim || !rows(*q) || Hkv < 1 || Hq % Hkv || B == 0) SV_NONE;
+    if (!current(d) || !pages(a[1], a[2], d, &ck, &cv)) SV_NONE;
+    const int64_t Hkv = ck->size(1);
+    const at::ScalarType s = ck->scalar_type();
+    if (q->scalar_type() != s || D != ck->size(3) || !rows(*q) || Hkv < 1 || Hq % Hkv || B == 0) SV_NONE;
     const void *lens, *fresh, *status;
-    if (!table(a[2], d, B, 1, &pt) || !vec(a[3], d, at::kInt, B, &lens) || !lens || !vec(a[4], d, at::kInt, B, &fresh) ||
-        !vec(a[9], d, at::kInt, B, &status))
+    if (!table(a[3], d, B, 1, &pt) || !vec(a[4], d, at::kInt, B, &lens) || !lens || !vec(a[5], d, at::kInt, B, &fresh) ||
+        !vec(a[10], d, at::kInt, B, &status))
         SV_NONE;
-    if (a[8] != Py_None && (!tensor(a[8], &given) || !same_rows(*given, d, s, B, N, Hq, D))) SV_NONE;
+    if (a[9] != Py_None && (!tensor(a[9], &given) || !same_rows(*given, d, s, B, N, Hq, D))) SV_NONE;
     if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) SV_NONE;
     sv_attention_args g;
     std::memset(&g, 0, sizeof g);
-    fill(&g.cache, r, *pt, lens, fresh);
-    g.scale = a[5] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AsDouble(a[5]);
-    g.window = PyLong_AsLongLong(a[6]);
-    g.max_context = a[7] == Py_None ? 0 : PyLong_AsLongLong(a[7]);
-    g.wait_limit_ns = PyLong_AsUnsignedLongLong(a[10]);
+    fill(&g.cache, *ck, *cv, *pt, lens, fresh);
+    g.scale = a[6] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AsDouble(a[6]);
+    g.window = PyLong_AsLongLong(a[7]);
+    g.max_context = a[8] == Py_None ? 0 : PyLong_AsLongLong(a[8]);
+    g.wait_limit_ns = PyLong_AsUnsignedLongLong(a[11]);
     if (PyErr_Occurred() || g.window < 0) SV_NONE;
     void* stream = at::cuda::getCurrentCUDAStream(d.index()).stream();
     const size_t bytes = g_attention_ws(B, N, Hq, Hkv, D);
@@ -146,7 +143,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.struct_size = sizeof g;
     g.q = q->data_ptr();
     g.out = out.data_ptr();
-    g.dtype = r.code;
+    g.dtype = code(s);
     g.B = B, g.N = N, g.q_heads = Hq, g.kv_heads = Hkv, g.dim = D;
     g.q_stride_b = q->stride(0), g.q_stride_n = q->stride(1), g.q_stride_h = q->stride(2);
     g.o_stride_b = out.stride(0), g.o_stride_n = out.stride(1), g.o_stride_h = out.stride(2);
@@ -157,33 +154,32 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// rotate(q, k, v, table, cache record, page_table, cache_lens, num_new, interleaved, out, row_status)
+// rotate(q, k, v, table, cache's k, v, page_table, cache_lens, num_new, interleaved, out, row_status)
 PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    const at::Tensor *q, *k, *v, *tab, *pt, *given = nullptr;
-    if (n != 11 || !tensor(a[0], &q) || !tensor(a[1], &k) || !tensor(a[2], &v) || !tensor(a[3], &tab) || q->dim() != 4)
+    const at::Tensor *q, *k, *v, *tab, *ck, *cv, *pt, *given = nullptr;
+    if (n != 12 || !tensor(a[0], &q) || !tensor(a[1], &k) || !tensor(a[2], &v) || !tensor(a[3], &tab) || q->dim() != 4)
         SV_NONE;
     const at::Device d = q->device();
     const int64_t B = q->size(0), N = q->size(1), Hq = q->size(2), D = q->size(3);
-    cache_record r;
-    if (!current(d) || !record(a[4], d, &r)) SV_NONE;
-    const int64_t Hkv = r.kv_heads;
-    const at::ScalarType s = type_of(r);
-    if (q->scalar_type() != s || D != r.dim || !rows(*q) || B == 0 || !same_rows(*k, d, s, B, N, Hkv, D) ||
+    if (!current(d) || !pages(a[4], a[5], d, &ck, &cv)) SV_NONE;
+    const int64_t Hkv = ck->size(1);
+    const at::ScalarType s = ck->scalar_type();
+    if (q->scalar_type() != s || D != ck->size(3) || !rows(*q) || B == 0 || !same_rows(*k, d, s, B, N, Hkv, D) ||
         !same_rows(*v, d, s, B, N, Hkv, D))
         SV_NONE;
     if (!on(*tab, d, at::kFloat) || tab->dim() != 3 || tab->size(1) != 2 || !tab->is_contiguous() || tab->size(2) < 8 ||
         tab->size(2) % 8 || 2 * tab->size(2) > D)
         SV_NONE;
     const void *lens, *fresh, *status;
-    if (!table(a[5], d, B, 1, &pt) || !vec(a[6], d, at::kInt, B, &lens) || !lens || !vec(a[7], d, at::kInt, B, &fresh) ||
-        !vec(a[10], d, at::kInt, B, &status))
+    if (!table(a[6], d, B, 1, &pt) || !vec(a[7], d, at::kInt, B, &lens) || !lens || !vec(a[8], d, at::kInt, B, &fresh) ||
+        !vec(a[11], d, at::kInt, B, &status))
         SV_NONE;
-    if (a[9] != Py_None && (!tensor(a[9], &given) || !same_rows(*given, d, s, B, N, Hq, D))) SV_NONE;
+    if (a[10] != Py_None && (!tensor(a[10], &given) || !same_rows(*given, d, s, B, N, Hq, D))) SV_NONE;
     sv_rotate_args g;
     std::memset(&g, 0, sizeof g);
-    fill(&g.cache, r, *pt, lens, fresh);
-    const int turn = PyObject_IsTrue(a[8]);
+    fill(&g.cache, *ck, *cv, *pt, lens, fresh);
+    const int turn = PyObject_IsTrue(a[9]);
     if (turn < 0) SV_NONE;
     at::Tensor out = given ? *given : at::empty(q->sizes(), q->options());
     g.struct_size = sizeof g;
@@ -191,7 +187,7 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.q_out = out.data_ptr();
     g.k = k->data_ptr();
     g.v = v->data_ptr();
-    g.dtype = r.code;
+    g.dtype = code(s);
     g.B = B, g.N = N, g.q_heads = Hq, g.kv_heads = Hkv, g.dim = D;
     g.q_stride_b = q->stride(0), g.q_stride_n = q->stride(1), g.q_stride_h = q->stride(2);
     g.o_stride_b = out.stride(0), g.o_stride_n = out.stride(1), g.o_stride_h = out.stride(2);

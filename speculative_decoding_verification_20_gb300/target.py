@@ -299,37 +299,46 @@ def process_logits(logits: torch.Tensor, *, history: Optional[TokenHistory] = No
 class PagedCache:
     """Keys and values of one layer in pages: k, v [pages, kv_heads, page_size, head_dim], bfloat16 or float16.
 
-    Position j of a sequence is row j % page_size of the page that its page table names at j // page_size.
+    Position j of a sequence is row j % page_size of the page that its page table names at j // page_size.  The calls
+    read k and v as they are then.
     """
 
     def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
         shape = (pages, kv_heads, page_size, head_dim)
-        self._set(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+        self.k, self.v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
+        _pages(self)
 
     @classmethod
     def from_tensors(cls, k: torch.Tensor, v: torch.Tensor) -> "PagedCache":
         """A cache over the caller's memory; any order of page, head and row in memory (views are fine), as long
         as the head dimension is contiguous and every row starts on a 16-byte boundary."""
         self = cls.__new__(cls)
-        self._set(k, v)
+        self.k, self.v = k, v
+        _pages(self)
         return self
 
-    def _set(self, k, v):
-        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
-            raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim] of one shape, type and device")
-        if k.dtype not in (torch.bfloat16, torch.float16):
-            raise TypeError(f"the cache must be bfloat16 or float16, got {k.dtype}")
-        if k.shape[2] < 16 or k.shape[2] % 16:
-            raise ValueError(f"page_size must be a multiple of 16, got {k.shape[2]}")
-        for t in (k, v):
-            if t.stride(3) != 1 or t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:3]):
-                raise ValueError("rows of the cache must be contiguous and start on 16-byte boundaries")
-        self.k, self.v = k, v
-        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
-        self.dtype, self.device = k.dtype, k.device
-        self._fields = (k.data_ptr(), v.data_ptr(), self.pages, self.page_size, *k.stride()[:3], *v.stride()[:3])
-        self._record = struct.pack("<2Q8q4q", *self._fields, self.kv_heads, self.head_dim, _DTYPE[k.dtype],
-                                   k.device.index if k.is_cuda else -1)
+    # k and v may be replaced: nothing is kept of them but the tensors
+    pages = property(lambda self: self.k.shape[0])
+    kv_heads = property(lambda self: self.k.shape[1])
+    page_size = property(lambda self: self.k.shape[2])
+    head_dim = property(lambda self: self.k.shape[3])
+    dtype = property(lambda self: self.k.dtype)
+    device = property(lambda self: self.k.device)
+
+
+def _pages(cache: PagedCache) -> tuple:
+    """The head of the C description of a cache: addresses, pages, page size and strides, of what it holds now."""
+    k, v = cache.k, cache.v
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+        raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim] of one shape, type and device")
+    if k.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"the cache must be bfloat16 or float16, got {k.dtype}")
+    if k.shape[2] < 16 or k.shape[2] % 16:
+        raise ValueError(f"page_size must be a multiple of 16, got {k.shape[2]}")
+    for t in (k, v):
+        if t.stride(3) != 1 or t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:3]):
+            raise ValueError("rows of the cache must be contiguous and start on 16-byte boundaries")
+    return (k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], *k.stride()[:3], *v.stride()[:3])
 
 
 def rotary_table(length: int, rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] = None,
@@ -414,16 +423,18 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
     interleaved.  Returns the rotated q (``out``, which may be q; rows past num_new are zeros).
     """
     if stream is None:
-        res = _short.rotate(q, k, v, table, cache._record, page_table, cache_lens, num_new, interleaved, out, row_status)
+        res = _short.rotate(q, k, v, table, cache.k, cache.v, page_table, cache_lens, num_new, interleaved, out,
+                            row_status)
         if res is not None:
             return res
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, N, q_heads, dim]")
-    dev, dtype, shape = q.device, cache.dtype, q.shape
+    dev, shape = q.device, q.shape
     if stream is not None or _current_device() != dev.index:
         return _elsewhere(dev, stream, rotate_append, (q, k, v, table, cache, page_table, cache_lens, num_new), dict(
             interleaved=interleaved, out=out, row_status=row_status))
     B, N, Hq, D = shape
+    pages, dtype = _pages(cache), cache.dtype
     if D != cache.head_dim or dev != cache.device:
         raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
     if table.dim() != 3 or table.shape[1] != 2 or table.dtype != torch.float32 or table.device != dev or \
@@ -445,7 +456,7 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
     _check(_library().spec_verify_rotate_append(_ROTATE.pack(
         _ROTATE.size, x.data_ptr(), o.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPE[dtype], B, N, Hq, cache.kv_heads, D,
         xs[0], xs[1], xs[2], os[0], os[1], os[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], table.data_ptr(), tlen,
-        2 * half, 1 if interleaved else 0, *cache._fields, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(),
+        2 * half, 1 if interleaved else 0, *pages, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(),
         _p(new), _p(row_status)), _raw_stream(dev.index)))
     return o
 
@@ -469,19 +480,19 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     for each stream, or the graph's own memory while a graph is captured).  Threads may share a stream.
     """
     if stream is None and workspace is None:
-        res = _short.attention(q, cache._record, page_table, cache_lens, num_new, scale, window, max_context, out,
+        res = _short.attention(q, cache.k, cache.v, page_table, cache_lens, num_new, scale, window, max_context, out,
                                row_status, wait_limit_ns)
         if res is not None:
             return res
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a CUDA tensor [B, N, q_heads, dim]")
-    dev, dtype, shape = q.device, cache.dtype, q.shape
+    dev, shape = q.device, q.shape
     if stream is not None or _current_device() != dev.index:
         return _elsewhere(dev, stream, paged_attention, (q, cache, page_table, cache_lens, num_new), dict(
             scale=scale, window=window, max_context=max_context, out=out, row_status=row_status, workspace=workspace,
             wait_limit_ns=wait_limit_ns))
     B, N, Hq, D = shape
-    Hkv = cache.kv_heads
+    pages, dtype, Hkv = _pages(cache), cache.dtype, cache.kv_heads
     if D != cache.head_dim or dev != cache.device:
         raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
     if Hq % Hkv:
@@ -502,7 +513,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
         status = lib.spec_verify_attention(_ATTENTION.pack(
             _ATTENTION.size, x.data_ptr(), o.data_ptr(), _DTYPE[dtype], B, N, Hq, Hkv, D, xs[0], xs[1], xs[2],
             os[0], os[1], os[2], 1.0 / math.sqrt(D) if scale is None else float(scale), window, max_context or 0,
-            *cache._fields, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(), _p(new), workspace.data_ptr(),
+            *pages, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(), _p(new), workspace.data_ptr(),
             workspace.numel(), _p(row_status), wait_limit_ns), raw)
     _check(status)
     return o
