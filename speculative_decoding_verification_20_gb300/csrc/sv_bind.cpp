@@ -217,7 +217,8 @@ PyObject* logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     std::memset(&g, 0, sizeof g);
     if (a[1] != Py_None) {
         if (!tensor(a[1], &seen) || !tensor(a[2], &counts) || !on(*seen, d, at::kInt) || !on(*counts, d, at::kInt) ||
-            counts->size(1) != V || (a[3] == Py_None && B > counts->size(0)))
+            seen->dim() != 2 || counts->dim() != 2 || seen->size(0) != counts->size(0) || !seen->is_contiguous() ||
+            !counts->is_contiguous() || 32 * seen->size(1) < V || counts->size(1) != V || (a[3] == Py_None && B > counts->size(0)))
             SV_NONE;
         g.seen = (const uint32_t*)seen->data_ptr();
         g.counts = counts->data_ptr<int32_t>();

@@ -171,10 +171,24 @@ class TokenHistory:
     def __init__(self, slots: int, vocab: int, device="cuda"):
         if slots < 1 or vocab < 1:
             raise ValueError("slots and vocab must be positive")
-        self.slots, self.vocab = slots, vocab
-        self.words = (vocab + 127) // 128 * 4
-        self.seen = torch.zeros((slots, self.words), dtype=torch.int32, device=device)
+        self.seen = torch.zeros((slots, (vocab + 127) // 128 * 4), dtype=torch.int32, device=device)
         self.counts = torch.zeros((slots, vocab), dtype=torch.int32, device=device)
+
+    # seen and counts may be replaced: nothing is kept of them but the tensors
+    slots = property(lambda self: self.counts.shape[0])
+    vocab = property(lambda self: self.counts.shape[1])
+    words = property(lambda self: self.seen.shape[1])
+
+    def _planes(self) -> Tuple[int, int, int, int, int]:
+        """The planes' addresses, slots, words and vocabulary, of what the history holds now."""
+        seen, counts = self.seen, self.counts
+        if seen.dim() != 2 or counts.dim() != 2 or seen.shape[0] != counts.shape[0] or \
+                32 * seen.shape[1] < counts.shape[1] or seen.device != counts.device or \
+                seen.dtype != torch.int32 or counts.dtype != torch.int32 or \
+                not seen.is_contiguous() or not counts.is_contiguous():
+            raise ValueError("seen must be int32 [slots, >= ceil(V / 32)] and counts int32 [slots, V], contiguous, on "
+                             "one device")
+        return seen.data_ptr(), counts.data_ptr(), seen.shape[0], seen.shape[1], counts.shape[1]
 
     def _call(self, tokens, prompt_lens, total_lens, slots, clear, stream):
         if not self.counts.is_cuda:
@@ -188,6 +202,7 @@ class TokenHistory:
         if tokens.dim() != 2:
             raise ValueError("tokens must be [B, L]")
         B, L = tokens.shape
+        planes = self._planes()
         tokens = _table(tokens, B, L, dev, "tokens")
         slot_of = _vec(slots, B, torch.int32, dev, "slots")
         if slot_of is None and B > self.slots:
@@ -195,8 +210,8 @@ class TokenHistory:
         pl = _vec(prompt_lens, B, torch.int32, dev, "prompt_lens")
         tl = _vec(total_lens, B, torch.int32, dev, "total_lens")
         _check(_library().spec_verify_history_add(_HISTORY.pack(
-            _HISTORY.size, _p(self.seen), _p(self.counts), self.slots, self.words, self.vocab,
-            _p(slot_of), _p(tokens), B, L, tokens.stride(0), _p(pl), _p(tl), int(clear)), _raw_stream(dev.index)))
+            _HISTORY.size, *planes, _p(slot_of), _p(tokens), B, L, tokens.stride(0), _p(pl), _p(tl), int(clear)),
+            _raw_stream(dev.index)))
 
     def load(self, tokens, prompt_lens=None, total_lens=None, slots=None, *, stream=None) -> None:
         """New sequences take their slots: of row b of tokens [B, L] the first prompt_lens[b] (default: none) are
@@ -247,10 +262,9 @@ def process_logits(logits: torch.Tensor, *, history: Optional[TokenHistory] = No
     seen = counts = slot_of = 0
     nslots = words = 0
     if history is not None:
-        if history.vocab != V or history.counts.device != dev:
-            raise ValueError(f"the history is of {history.vocab} tokens on {history.counts.device}")
-        seen, counts = history.seen.data_ptr(), history.counts.data_ptr()
-        nslots, words = history.slots, history.words
+        seen, counts, nslots, words, vocab = history._planes()
+        if vocab != V or history.counts.device != dev:
+            raise ValueError(f"the history is of {vocab} tokens on {history.counts.device}")
         slots = _vec(slots, B, torch.int32, dev, "slots")
         if slots is None and B > nslots:
             raise ValueError(f"{B} rows but only {nslots} slots")
