@@ -12,6 +12,7 @@
 
 #include <cuda.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "sv_internal.cuh"
@@ -300,6 +301,19 @@ __device__ __forceinline__ const T* q_row(const AttendArgs& p, int b, int h, int
     const int i = by_group(p, r);
     return (const T*)p.a.q + (int64_t)b * p.a.q_stride_b + (int64_t)i * p.a.q_stride_n +
            (int64_t)(h * p.group + r - i * p.group) * p.a.q_stride_h;
+}
+
+// Weights are 2^(score - reference + lift): at most 2^8, times 2^7 in fp16.  Its steps become
+// coarse below 2^-14 and end at 2^-24, and the many small weights of a long row beside a large
+// one add up: without the lift 16000 weights of 2^-25.2 came to nothing in the product with
+// the values while their sum had them.  A weight is off by at most 2^-11 of itself or
+// by 2^-32 of the row's largest.  The factor falls out of output / sum.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+// what a row's scores are reduced by (nothing visible yet: weights 0)
+template <typename T>
+__device__ __forceinline__ float weight_base(float ref) {
+    return ref == -INFINITY ? 0.0f : ref - kLift<T>;
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {  // 2^x; 2^-inf = 0

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float base = ref[e] == -INFINITY ? 0.0f : ref[e];  // nothing seen yet: weights 0
+                        const float base = weight_base<T>(ref[e]);
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
 #pragma unroll

@@ -15,7 +15,7 @@
 // only while the next softmax looks for its maximum.  The output stays in tensor memory
 // over all keys; the running maximum it refers to is only raised when a row's scores
 // outgrow it by 2^8, so that rescaling the output is rare.  Weights of up to 2^8 lose
-// nothing in the 16-bit types' relative step, and sums are 32-bit.
+// nothing in the 16-bit types' relative step (fp16: see kLift), and sums are 32-bit.
 //
 // Up to 128 rows (SPLIT) the loads bound the call, and the room goes to the ring: the
 // weights lie over their scores in tensor memory, and warp 11 loads the queries.
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         sum *= f;
                         ref = now;
                     }
-                    const float base = ref == -INFINITY ? 0.0f : ref;  // nothing visible yet: weights 0
+                    const float base = weight_base<T>(ref);
                     const float2 qs = make_float2(p.qscale, p.qscale), mb = make_float2(-base, -base);
                     float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     auto weigh = [&](const float* v, int c) {  // 32 keys, the c-th such set of the tile
