@@ -309,10 +309,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     if (wr0 >= rows) {  // no rows: their lanes' products go nowhere
                         // (not SPLIT: these scores can be there before the others' weights of the
                         // tile before, whose phase this warp must not enter twice)
-                        if (tile != start) {
-                            if (!SPLIT) alive = bar_wait(&s_out[x], n_out & 1, limit, dead);
-                            ++n_out;
-                        }
+                        if (!SPLIT && tile != start) alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
                         fence_before();
                         bar_arrive(&s_weights[x][0]);
                         bar_arrive(&s_weights[x][1]);
@@ -349,11 +346,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     top[0] = max3(top[0], s0[62], s0[63]);
                     top[2] = max3(top[2], s1[62], s1[63]);
                     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.qscale;
-                    bool out_seen = tile == start;
-                    if (!SPLIT && tile != start) {  // the product before this one has read its weights
+                    // The product before this one has read its weights.  (SPLIT: it is through when these
+                    // scores are there, for their commit covers what its thread issued before; s_out
+                    // has one phase a unit.)
+                    if (!SPLIT && tile != start) {
                         alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);
                         if (!alive) break;
-                        out_seen = true;
                         fence_after();
                     }
                     if (tile == start) {
@@ -362,12 +360,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
                         // raise the reference; the output so far shrinks by as much
                         const float now = fmaxf(ref, m);
                         const float f = now == -INFINITY ? 1.0f : fast_exp2(ref - now);
-                        if (SPLIT) {
-                            alive = bar_wait(&s_out[x], n_out++ & 1, limit, dead);  // the product before this one
-                            if (!alive) break;
-                            out_seen = true;
-                            fence_after();
-                        }
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float o[16];
@@ -427,9 +419,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
                     handed(&s_weights[x][1]);
                     add[0] = add2(add[0], add[1]);
                     sum += add[0].x + add[0].y;
-                    // SPLIT: these scores came after the product before them, in one warp's order, so
-                    // that phase of s_out is over: the wait at the unit's end is for the one after it.
-                    if (SPLIT && !out_seen) ++n_out;
                 }
                 if (q_there) hand_q();
                 if (left > 0 && !ahead) next_unit<RM>(p, next);
@@ -629,7 +618,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                                         mma_ss(tO, w_desc + (((k / 4) * (128 * 128) + (k % 4) * 32) >> 4), b, i_o, add);
                                 }
                                 if (half) {
-                                    mma_commit(&s_out[x]);
+                                    if (!SPLIT || !more) mma_commit(&s_out[x]);
                                     mma_commit(&s_empty[vstage]);
                                 }
                             }
