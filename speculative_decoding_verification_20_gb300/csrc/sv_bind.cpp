@@ -58,6 +58,10 @@ inline bool table(PyObject* o, const at::Device& d, int64_t rows, int64_t cols, 
     return tensor(o, t) && on(**t, d, at::kInt) && (*t)->dim() == 2 && (*t)->size(0) == rows &&
            (*t)->size(1) >= cols && ((*t)->stride(1) == 1 || (*t)->size(1) == 1);
 }
+// a page table with rows of their own
+inline bool page_table(PyObject* o, const at::Device& d, int64_t B, const at::Tensor** t) {
+    return table(o, d, B, 1, t) && (B < 2 || (*t)->stride(0) >= (*t)->size(1));
+}
 // rows [B, N, heads, dim] as the kernels take them
 inline bool rows(const at::Tensor& t) {
     return t.stride(3) == 1 && !((t.stride(0) | t.stride(1) | t.stride(2)) & 7) && !((uintptr_t)t.data_ptr() & 15);
@@ -122,7 +126,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType s = ck->scalar_type();
     if (q->scalar_type() != s || D != ck->size(3) || !rows(*q) || Hkv < 1 || Hq % Hkv || B == 0) SV_NONE;
     const void *lens, *fresh, *status;
-    if (!table(a[3], d, B, 1, &pt) || !vec(a[4], d, at::kInt, B, &lens) || !lens || !vec(a[5], d, at::kInt, B, &fresh) ||
+    if (!page_table(a[3], d, B, &pt) || !vec(a[4], d, at::kInt, B, &lens) || !lens || !vec(a[5], d, at::kInt, B, &fresh) ||
         !vec(a[10], d, at::kInt, B, &status))
         SV_NONE;
     if (a[9] != Py_None && (!tensor(a[9], &given) || !same_rows(*given, d, s, B, N, Hq, D))) SV_NONE;
@@ -172,7 +176,7 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
         tab->size(2) % 8 || 2 * tab->size(2) > D)
         SV_NONE;
     const void *lens, *fresh, *status;
-    if (!table(a[6], d, B, 1, &pt) || !vec(a[7], d, at::kInt, B, &lens) || !lens || !vec(a[8], d, at::kInt, B, &fresh) ||
+    if (!page_table(a[6], d, B, &pt) || !vec(a[7], d, at::kInt, B, &lens) || !lens || !vec(a[8], d, at::kInt, B, &fresh) ||
         !vec(a[11], d, at::kInt, B, &status))
         SV_NONE;
     if (a[10] != Py_None && (!tensor(a[10], &given) || !same_rows(*given, d, s, B, N, Hq, D))) SV_NONE;

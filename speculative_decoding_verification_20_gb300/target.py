@@ -116,6 +116,12 @@ def _table(x: torch.Tensor, rows: int, cols: int, device, name: str) -> torch.Te
     return x if x.stride(1) == 1 or x.shape[1] == 1 else x.contiguous()
 
 
+def _page_table(x: torch.Tensor, B: int, device) -> torch.Tensor:
+    """A page table with rows of their own: sequences that share one (an expanded row) get a copy each."""
+    x = _table(x, B, 1, device, "page_table")
+    return x if B < 2 or x.stride(0) >= x.shape[1] else x.contiguous()
+
+
 def _status(row_status, B, device):
     if row_status is not None and (row_status.dtype != torch.int32 or row_status.device != device or
                                    tuple(row_status.shape) != (B,) or not row_status.is_contiguous()):
@@ -462,7 +468,7 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
     k = _rows(k, "k", kv, dtype, dev)
     v = _rows(v, "v", kv, dtype, dev)
     o = torch.empty(shape, dtype=dtype, device=dev) if out is None else _out_rows(out, shape, dtype, dev)
-    pt = _table(page_table, B, 1, dev, "page_table")
+    pt = _page_table(page_table, B, dev)
     lens = _vec(cache_lens, B, torch.int32, dev, "cache_lens")
     new = _vec(num_new, B, torch.int32, dev, "num_new")
     _status(row_status, B, dev)
@@ -515,7 +521,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
         raise ValueError("window must be 0 (none) or positive")
     x = _rows(q, "q", shape, dtype, dev)
     o = torch.empty(shape, dtype=dtype, device=dev) if out is None else _out_rows(out, shape, dtype, dev)
-    pt = _table(page_table, B, 1, dev, "page_table")
+    pt = _page_table(page_table, B, dev)
     lens = _vec(cache_lens, B, torch.int32, dev, "cache_lens")
     new = _vec(num_new, B, torch.int32, dev, "num_new")
     _status(row_status, B, dev)

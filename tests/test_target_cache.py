@@ -1,4 +1,4 @@
-"""A PagedCache whose tensors are replaced: the calls read the ones it holds then."""
+"""A PagedCache whose tensors are replaced: the calls read the ones it holds then.  Page tables with shared rows."""
 import pytest
 import torch
 
@@ -83,3 +83,27 @@ def test_replaced_tensors_are_read_and_written(as_list):
     assert torch.equal(got, want) and torch.equal(cache.k, fresh.k) and torch.equal(cache.v, fresh.v)
     assert torch.equal(sv.paged_attention(q, cache, pages, lens), sv.paged_attention(q, fresh, pages, lens))
     assert not old[0].any() and not old[1].any()
+
+
+@pytest.mark.gpu
+def test_sequences_may_share_a_row_of_the_page_table():
+    """Samples of one prompt: an expanded row, and rows that overlap, are read as they are written."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+    B = 3
+    cache = sv.PagedCache.from_tensors(rand(8, 2, 16, 64), rand(8, 2, 16, 64))
+    row = torch.randperm(8, device="cuda").to(torch.int32)
+    lens = torch.full((B,), 40, dtype=torch.int32, device="cuda")
+    q = rand(B, 2, 4, 64)
+    for table in (row[None, :4].expand(B, 4), row.as_strided((B, 4), (2, 1))):
+        want = sv.paged_attention(q, cache, table.contiguous(), lens)
+        assert torch.equal(sv.paged_attention(q, cache, table, lens), want)
+        assert torch.equal(sv.paged_attention(q, cache, table, lens.tolist()), want)
+    new = torch.tensor([1, 0, 0], dtype=torch.int32, device="cuda")  # the first writes, the others read
+    k, t = rand(B, 2, 2, 64), sv.rotary_table(64, 64)
+    other = sv.PagedCache.from_tensors(cache.k.clone(), cache.v.clone())
+    a = sv.rotate_append(q, k, k, t, cache, row[None, :4].expand(B, 4), lens, new)
+    b = sv.rotate_append(q, k, k, t, other, row[None, :4].repeat(B, 1), lens, new)
+    assert torch.equal(a, b) and torch.equal(cache.k, other.k) and torch.equal(cache.v, other.v)
