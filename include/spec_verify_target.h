@@ -79,8 +79,9 @@ int spec_verify_history_add(const sv_history_args* args, void* stream);
  * in 32 bits, rounded once to the logits' type.  The same call serves the target's
  * gamma+1 rows and the drafter's rows (N = 1: the plain decoding step).
  *
- * logits, out      may be the same memory (each element is read by the thread that
- *                  writes it); otherwise they must not overlap
+ * logits, out      may be the same memory (an element is read and written by one block
+ *                  alone, with a barrier between its copy and a second look);
+ *                  otherwise they must not overlap
  * seen .. slot_of  the history, as above; seen = NULL: no history
  * draft_tokens     [B, draft_len] or NULL; ids outside [0, V) are skipped
  * repetition, frequency, presence  [B] float or NULL (1, 0, 0)
@@ -177,9 +178,13 @@ int spec_verify_rotate_append(const sv_rotate_args* args, void* stream);
  * j over the positions of cache head h / (q_heads / kv_heads) with
  * j <= cache_lens[b] + i and, for window > 0, j > cache_lens[b] + i - window.
  * q, out [B, N, q_heads, dim], SV_BF16 or SV_F16 as the cache; dim 64 or 128.
- * Scores, the softmax and the sums are held in 32 bits; its weights enter the
- * product with v in the cache's 16-bit type.  Rows past num_new[b] are zeros.  What
- * the cache holds at positions that no new token sees may be anything (NaN among it).
+ * scale is positive and finite.  Scores, the softmax and the sums are held in 32 bits;
+ * its weights enter the product with v in the cache's 16-bit type (fp16: those below
+ * 2^-21 of the row's largest with a fixed step of 2^-31 of it).  Rows past num_new[b]
+ * are zeros.  What the cache holds at positions that no new token sees may be anything
+ * (NaN among it).  A NaN or infinity among the keys reaches the tokens that see its
+ * position; among the values, where some of the new tokens see its position, it may
+ * reach the others of the sequence as well, as 0 times it.
  * max_context: an upper bound of cache_lens + num_new known to the host, or 0 (the
  * page table's width); it only sizes the launch.
  * workspace: spec_verify_attention_workspace_size() bytes, 256-byte aligned, needs

@@ -18,15 +18,18 @@
 // nothing in the 16-bit types' relative step (fp16: see kLift), and sums are 32-bit.
 //
 // Up to 128 rows (SPLIT) the loads bound the call, and the room goes to the ring: the
-// weights lie over their scores in tensor memory, and warp 11 loads the queries.
+// weights lie over their scores in tensor memory, and warp 11 loads the queries, a unit
+// ahead of the products: 3900 cycles for 128 rows of 128, where a unit of one key tile
+// takes more than 10000 (128 sequences x 8 tokens behind 100, 64 / 8 heads: seven units a CTA,
+// 47 us).
 //
 // Pages become boxes of gcd(page_size, 128) keys x 64 elements.  A box with no visible
 // key, or on a bad page, is loaded from past the last page, where TMA gives zeros: its
 // scores are masked, and its values add nothing.  Rows of a box past the sequence's end
 // are zeroed in shared memory before their product, since they may hold anything.
 //
-// Two chunks of 2048 tokens behind 4-6k keys (32 / 8 heads of 128, bf16): 305 us, 1310
-// TFLOP/s, 0.69 of the measured rate.  What bounds it is the softmax: some 2900 cycles for
+// Two chunks of 2048 tokens behind 4-6k keys (32 / 8 heads of 128, bf16): 305-308 us, 1300
+// TFLOP/s, 0.68 of the measured rate.  What bounds it is the softmax: some 2900 cycles for
 // two tiles of 128 x 128 (2600 with heads of 64), of which the exponential unit fills 1024
 // and the tiles' products 2080; it waits for nothing else.  The start and the units' ends
 // are a tenth.  Tried and slower: weights over the scores for these units too (337 us: the
@@ -248,8 +251,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         int first = part.tile, left = part.todo, index = 0;
         uint32_t n_scores = 0, n_out = 0;  // phases seen
         bool alive = true;
-        // !SPLIT: the warp's 32 query rows of a unit, into shared memory as the products read them.  (One warp for
-        // all 256 rows took 5000 cycles a half; here a unit's rows come while its predecessor ends.)
+        // !SPLIT: the warp's 32 query rows of a unit, into shared memory as the products read them.  (There is one
+        // place for them: one warp for all 256 rows took 5000 cycles a half between two units; here a unit's rows
+        // come while its predecessor ends.)
         bool q_there = false;
         auto load_q = [&](const Unit& w) {
             constexpr int RC = D / 8, RS = 32 / RC;  // 16-byte pieces of a row, rows a step
