@@ -185,17 +185,22 @@ def _sample_inputs(case, seed):
     return d
 
 
+def _power(e):
+    """2^e in float64, exactly (its exponent bits; pow and ldexp of the GPU may be off by a last bit)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _least_scale(amax):
     """The least power of two s with amax <= 448 s (1 for a block of zeros); amax in float64."""
     m, e = torch.frexp(amax / _TOP)  # amax / 448 = m 2^e, m in [0.5, 1)
-    s = torch.ldexp(torch.ones_like(amax), torch.where(m == 0.5, e - 1, e))
+    s = _power(torch.where(m == 0.5, e - 1, e))
     return torch.where(amax > 0, s, torch.ones_like(s))
 
 
 def _round8(x):
     """float64 values rounded to e4m3: 4 significant bits, steps of 2^-9 below 2^-6."""
     _, e = torch.frexp(x)
-    step = torch.ldexp(torch.ones_like(x), (e - 4).clamp_(min=-9))
+    step = _power((e - 4).clamp_(min=-9))
     return torch.round(x / step) * step
 
 
@@ -480,16 +485,12 @@ def _exact_append(case, seed):
             rows = x.shape[0]
             x = torch.cat((x, x.new_zeros((-rows % _BLOCK, H, D))), 0).reshape(-1, _BLOCK, H, D)
             peak = x.abs().amax((1, 3), keepdim=True)
-            scale = torch.ones_like(peak)
-            for e in range(-40, 20):  # the first power of two that holds the block
-                small = (peak <= _TOP * 2.0 ** e) & (peak > _TOP * 2.0 ** (e - 1))
-                scale = torch.where(small, torch.full_like(scale, 2.0 ** e), scale)
+            powers = torch.tensor([2.0 ** e for e in range(-60, 40)], dtype=torch.float64, device="cuda")
+            scale = powers[torch.bucketize(peak, _TOP * powers)]  # the first that holds the block
+            scale = torch.where(peak > 0, scale, torch.ones_like(scale))
             y = x / scale
-            grid = 2.0 ** (torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
-            # a logarithm next to a power of two may come out on its other side
-            grid = torch.where(y.abs() >= 16.0 * grid, 2.0 * grid, grid)
-            grid = torch.where((y.abs() < 8.0 * grid) & (grid > 2.0 ** -9), 0.5 * grid, grid)
-            y = torch.round(y / grid) * grid * scale
+            below = powers[torch.bucketize(y.abs().clamp(min=2.0 ** -6), powers, right=True) - 1]  # 2^e <= |y| < 2^(e + 1)
+            y = torch.round(y / (below / 8)) * (below / 8) * scale
             dst[b, :rows] = y.reshape(-1, H, D)[:rows]
     return q_out, back[0], back[1]
 
