@@ -6,8 +6,11 @@
  * before spec_verify reads them:
  *   spec_verify_rotate_append    rotary positions on q and k; k and v go to their pages
  *   spec_verify_attention        the new tokens' attention over the paged cache
+ *   spec_verify_read_cache       values of a cache held in 8 bits
  *   spec_verify_process_logits   penalties for repeated tokens, biases, grammar masks
  *   spec_verify_history_add      keeps the tokens that the penalties count
+ * and a drafter, or plain decoding, draws its tokens:
+ *   spec_verify_sample           temperature, top-k, top-p, min-p and a given random number
  *
  * Conventions are those of spec_verify.h: device pointers, asynchronous on
  * `stream`, nothing allocated and nothing kept, argument errors returned before
@@ -29,15 +32,21 @@ extern "C" {
 
 /* a third element type, for q, k, v and the cache (16-bit only there) */
 #define SV_F16 2
+/* the type of a cache held in 8 bits: 1 sign, 4 exponent and 3 fraction bits (bias 7), largest
+ * value 448, no infinities, 0x7f and 0xff are NaN */
+#define SV_E4M3 3
 
 #define SV_ROW_BAD_PENALTY 0x100u /* repetition not finite or <= 0; frequency or presence not finite */
 #define SV_ROW_BAD_SLOT 0x200u    /* history slot outside [0, slots) */
 #define SV_ROW_BAD_LENGTH 0x400u  /* num_new outside [0, N], cache_lens < 0, or past the page or rotary table */
 #define SV_ROW_BAD_PAGE 0x800u    /* a page id in use is outside [0, pages) */
+#define SV_ROW_BAD_MIN_P 0x1000u  /* min_p outside [0, 1] */
+#define SV_ROW_BAD_UNIFORM 0x2000u /* a random number outside [0, 1) */
 
 #define SV_MAX_POSITIONS (SV_MAX_GAMMA + 1) /* logit rows per sequence */
 #define SV_MAX_HEAD_DIM 256                 /* spec_verify_rotate_append */
 #define SV_MAX_GROUP 64                     /* query heads per cache head */
+#define SV_SCALE_BLOCK 16                   /* tokens that share a scale in an 8-bit cache */
 
 /*
  * Token history.  Per slot (a sequence's place in the server): seen [slots, words], a
@@ -141,6 +150,20 @@ typedef struct {
 } sv_paged_cache;
 
 /*
+ * A cache held in 8 bits (SV_E4M3): its pages hold codes, strides of sv_paged_cache count
+ * bytes, and every SV_SCALE_BLOCK consecutive slots of a page's head share a scale:
+ *   key = code * k[page * k_stride_page + h * k_stride_head + slot / SV_SCALE_BLOCK],
+ * and the same for values.  Scales are finite and not negative; those of a block that no
+ * token sees may be anything.
+ */
+typedef struct {
+    float* k;
+    float* v;
+    int64_t k_stride_page, k_stride_head;
+    int64_t v_stride_page, v_stride_head;
+} sv_cache_scales;
+
+/*
  * Rotates q and k by their positions and writes k and v to the cache.
  * q [B, N, q_heads, dim], k, v [B, N, kv_heads, dim] (SV_BF16 or SV_F16; dim a
  * multiple of 16, at most SV_MAX_HEAD_DIM).  The first rot_dim elements of a head
@@ -171,6 +194,46 @@ typedef struct {
 } sv_rotate_args;
 
 int spec_verify_rotate_append(const sv_rotate_args* args, void* stream);
+
+/*
+ * The same into a cache held in 8 bits, where scales.k != NULL (else as above).  For each
+ * block of SV_SCALE_BLOCK positions that new tokens go to, with x its live elements of a
+ * head (the rotated keys or the values of the new tokens; for positions before
+ * cache_lens[b], what the cache holds of them):
+ *   scale = the least power of two s >= 2^-126 with |x| <= 448 s for all finite x (1: all 0)
+ *   code  = x / scale rounded once to SV_E4M3, ties to even; infinities and NaN become NaN
+ * Rotation is exact up to that rounding (the table's entries taken as they are), so codes
+ * do not depend on how the sums are formed.  What a block held past cache_lens[b] (tokens
+ * that were rejected) has no part in it: the scale follows the live tokens down as well as
+ * up, and rescaling by a power of two loses nothing but what falls below 2^-9 scale.
+ * Codes past the new tokens stay as they are.  The blocks that two sequences of a call
+ * write to must be different ones.
+ */
+typedef struct {
+    uint64_t struct_size;
+    sv_cache_scales scales;
+} sv_rotate_options;
+
+int spec_verify_rotate_append_ex(const sv_rotate_args* args, const sv_rotate_options* options, void* stream);
+
+/*
+ * Values that a cache held in 8 bits stands for: positions first[b] .. first[b] + n - 1 of
+ * each sequence, n = count[b] (NULL: N, as is num_new; cache_lens is first), to k_out and
+ * v_out [B, N, kv_heads, dim] (dtype SV_BF16 or SV_F16, contiguous, 16-byte aligned), code *
+ * scale rounded once.  Rows past n are zeros; a sequence with bad lengths gets NaN rows, and
+ * so does a position on a bad page.  Positions that were never written give what lies there.
+ */
+typedef struct {
+    uint64_t struct_size;
+    void* k_out;
+    void* v_out;
+    int64_t dtype, B, N, kv_heads, dim;
+    sv_paged_cache cache;
+    sv_cache_scales scales;
+    uint32_t* row_status;
+} sv_read_args;
+
+int spec_verify_read_cache(const sv_read_args* args, void* stream);
 
 /*
  * Attention of the new tokens over the cache that holds them too:
@@ -214,6 +277,59 @@ typedef struct {
 
 size_t spec_verify_attention_workspace_size(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads, int64_t dim);
 int spec_verify_attention(const sv_attention_args* args, void* stream);
+
+/*
+ * The same with
+ * sinks   >= 0: with a window, positions j < sinks are visible too (up to cache_lens[b] + i).
+ *         Pages of which neither the window nor the sinks need a position are not looked up:
+ *         their entries in the page table may be anything.
+ * scales  scales.k != NULL: a cache held in 8 bits; q and out are of args->dtype.  Products
+ *         are formed of the codes, in SV_F16 with 32-bit sums: q enters divided by a power
+ *         of two of its row's (SV_BF16; elements below 2^-38 of the row's largest lose
+ *         bits), scales of keys multiply the scores in 32 bits, and those of values the
+ *         weights, relative to the largest met so far, before these are rounded.
+ * The workspace is that of spec_verify_attention.
+ */
+typedef struct {
+    uint64_t struct_size;
+    int64_t sinks;
+    sv_cache_scales scales;
+} sv_attention_options;
+
+int spec_verify_attention_ex(const sv_attention_args* args, const sv_attention_options* options, void* stream);
+
+/*
+ * Draws a token of every row of logits [B, N, V] (SV_F32 or SV_BF16), in 32-bit numbers with
+ * sums of 48 bits.  With m the row's largest logit, T, k, P, M the sequence's parameters:
+ *   w(t) = exp((z(t) - m) / T)
+ *   kept = the k largest (0, or more than V: all; of equal logits the lower id first),
+ *          of these, in that order, the shortest run with a mass >= P of theirs (1: all),
+ *          of these those with w >= M
+ *   token = the least t with sum of kept w up to t > u * sum of kept w
+ *   prob  = w(token) / sum of kept w
+ * T = 0 is greedy: the first of the largest, prob 1.  This is the q that spec_verify forms
+ * of draft logits with the same temperature, top_k and top_p.
+ * temperature, top_k, top_p, min_p  [B] or NULL (1, 0, 1, 0); uniforms [B, N] (row stride
+ * uniform_stride), each in [0, 1).  tokens, probs [B, N] contiguous; probs may be NULL.
+ * A sequence with a bad parameter, and a row with a bad random number, a NaN or +inf logit
+ * or no finite logit, gets token -1 and prob NaN, and its bit in row_status.
+ */
+typedef struct {
+    uint64_t struct_size;
+    const void* logits;
+    int64_t dtype, B, N, V, stride_b, stride_n;
+    const float* uniforms;
+    int64_t uniform_stride;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* tokens;
+    float* probs;
+    uint32_t* row_status;
+} sv_sample_args;
+
+int spec_verify_sample(const sv_sample_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -36,7 +36,8 @@ EXPORTED = ("spec_verify", "spec_verify_ex", "spec_verify_workspace_size", "spec
             "spec_verify_host_staging_size", "spec_verify_strerror", "spec_verify_static", "spec_verify_gumbel",
             "spec_verify_kseq", "spec_verify_kseq_workspace_size", "spec_verify_history_add",
             "spec_verify_process_logits", "spec_verify_rotate_append", "spec_verify_attention",
-            "spec_verify_attention_workspace_size")
+            "spec_verify_attention_workspace_size", "spec_verify_rotate_append_ex", "spec_verify_attention_ex",
+            "spec_verify_read_cache", "spec_verify_sample")
 SV_MAX_KSEQ = 13
 
 SV_ESCRATCH = -6
@@ -95,9 +96,13 @@ def load_library():
                                      ctypes.POINTER(_Options)]
     lib.spec_verify_kseq.restype = I
     # the structures of include/spec_verify_target.h are passed as packed bytes
-    for name in ("history_add", "process_logits", "rotate_append", "attention"):
+    for name in ("history_add", "process_logits", "rotate_append", "attention", "read_cache", "sample"):
         fn = getattr(lib, "spec_verify_" + name)
         fn.argtypes = [ctypes.c_char_p, P]
+        fn.restype = I
+    for name in ("rotate_append_ex", "attention_ex"):
+        fn = getattr(lib, "spec_verify_" + name)
+        fn.argtypes = [ctypes.c_char_p, ctypes.c_char_p, P]
         fn.restype = I
     lib.spec_verify_attention_workspace_size.argtypes = [ctypes.c_int64] * 5
     lib.spec_verify_attention_workspace_size.restype = SZ
@@ -403,6 +408,6 @@ def spec_verify_static(target: torch.Tensor, draft: torch.Tensor, draft_tokens: 
     return outputs
 
 
-from .target import (ROW_BAD_LENGTH, ROW_BAD_PAGE, ROW_BAD_PENALTY, ROW_BAD_SLOT, PagedCache,  # noqa: E402,F401
-                     TokenHistory, attention_workspace_size, paged_attention, process_logits, rotary_table,
-                     rotate_append)
+from .target import (ROW_BAD_LENGTH, ROW_BAD_MIN_P, ROW_BAD_PAGE, ROW_BAD_PENALTY, ROW_BAD_SLOT,  # noqa: E402,F401
+                     ROW_BAD_UNIFORM, PagedCache, PagedCache8, TokenHistory, attention_workspace_size, paged_attention,
+                     process_logits, read_cache, rotary_table, rotate_append, sample)

@@ -77,6 +77,15 @@ __device__ __forceinline__ void tma_part(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(0), "r"(row), "r"(part), "r"(head), "r"(page), "r"(smem_u32(bar))
         : "memory");
 }
+// a box of a page's rows of codes, for one head: row, head, page
+__device__ __forceinline__ void tma_codes(uint32_t dst, const CUtensorMap* map, int row, int head, int page,
+                                          uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2,%3,%4,%5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
 // all parts of the rows, one part after the other
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int row, int head, int page,
                                         uint64_t* bar) {

@@ -22,6 +22,9 @@ int row_tile(int64_t N, int64_t group) {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
 }
 
+// The same over a cache held in 8 bits (never larger than row_tile, whose workspace is used).
+int row_tile8(int64_t N, int64_t group) { return row_tile(N, group); }
+
 int check_attention(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads, int64_t dim) {
     if (B < 0 || N < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads) return SV_EINVAL;
     if (dim != 64 && dim != 128) return SV_EUNSUPPORTED;
@@ -91,7 +94,32 @@ bool encode(CUtensorMap* m, const void* base, const AttendArgs& p, int64_t sp, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// pages of codes as [pages][heads][page_size][dim]
+bool encode8(CUtensorMap* m, const void* base, const AttendArgs& p, int64_t sp, int64_t sh, int64_t ss, int box,
+             bool swizzled) {
+    EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.a.dim, (cuuint64_t)p.a.cache.page_size, (cuuint64_t)p.a.kv_heads,
+                                (cuuint64_t)p.a.cache.pages};
+    if (p.a.kv_heads == 1) sh = ss;
+    if (p.a.cache.pages == 1) sp = ss;
+    const cuuint64_t strides[3] = {(cuuint64_t)ss, (cuuint64_t)sh, (cuuint64_t)sp};
+    const cuuint32_t boxes[4] = {(cuuint32_t)p.a.dim, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, boxes, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              !swizzled         ? CU_TENSOR_MAP_SWIZZLE_NONE
+              : p.a.dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
+
+bool encode_codes(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, bool swizzled) {
+    const sv_paged_cache& c = p.a.cache;
+    return encode8(keys, c.k_pages, p, c.k_stride_page, c.k_stride_head, c.k_stride_slot, box, swizzled) &&
+           encode8(values, c.v_pages, p, c.v_stride_page, c.v_stride_head, c.v_stride_slot, box, swizzled);
+}
 
 bool encode_pages(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, int parts) {
     const sv_paged_cache& c = p.a.cache;
@@ -109,7 +137,10 @@ extern "C" size_t spec_verify_attention_workspace_size(int64_t B, int64_t N, int
     return workspace(dim, row_tile(N, q_heads / kv_heads)).total;
 }
 
-extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream) {
+namespace {
+
+// sinks: positions that a window leaves in sight; scales: of a cache held in 8 bits, or null
+int attend(const sv_attention_args* args, int64_t sinks, const sv_cache_scales* scales, void* stream) {
     if (!args || args->struct_size != sizeof(sv_attention_args)) return SV_EINVAL;
     const sv_attention_args& a = *args;
     if (a.dtype != SV_BF16 && a.dtype != SV_F16) return SV_EUNSUPPORTED;
@@ -124,10 +155,11 @@ extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream
     if ((a.q_heads > 1 && a.o_stride_h < a.dim) || (a.N > 1 && a.o_stride_n < a.dim) ||
         (a.B > 1 && a.o_stride_b < a.dim))
         return SV_EINVAL;
-    rc = check_cache(a.cache, a.B, a.kv_heads, a.dim);
+    rc = check_cache(a.cache, a.B, a.kv_heads, a.dim, scales ? 1 : 2);
+    if (rc == SV_OK && scales) rc = check_scales(*scales, a.cache, a.kv_heads);
     if (rc != SV_OK) return rc;
     const int group = (int)(a.q_heads / a.kv_heads);
-    const int rm = row_tile(a.N, group);
+    const int rm = scales ? row_tile8(a.N, group) : row_tile(a.N, group);
     const Workspace w = workspace(a.dim, rm);
     if (!a.workspace || a.workspace_bytes < (int64_t)w.total) return SV_EWORKSPACE;
     if ((uintptr_t)a.workspace & 255u) return SV_EINVAL;
@@ -148,6 +180,11 @@ extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream
     p.qscale = (float)(a.scale * kLog2e);
     p.capacity = a.cache.pages_per_seq * a.cache.page_size;
     if (p.capacity > 0x7FFFFF00) p.capacity = 0x7FFFFF00;  // positions are 32-bit
+    if (a.window > 0) {  // (positions are below 0x7FFFFF00)
+        p.sinks = (int)(sinks < 0x7FFFFF00 ? sinks : 0x7FFFFF00);
+        p.sink_tiles = (p.sinks + kKeyTile - 1) / kKeyTile;
+    }
+    if (scales) p.sc = *scales;
     char* ws = (char*)a.workspace;
     p.cut = (Cut*)(ws + w.cut);
     p.part_ml = (float*)(ws + w.ml);
@@ -160,9 +197,23 @@ extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream
     if (tiles < p.ctas) p.ctas = (int)tiles;
     cudaStream_t s = (cudaStream_t)stream;
     p.wait_ns = a.wait_limit_ns ? a.wait_limit_ns : kWaitLimitNs;
-    const cudaError_t e = rm >= 128 ? launch_attend_tiles((int)a.dtype, (int)a.dim, rm, p, s)
-                                   : launch_attend_rows((int)a.dtype, (int)a.dim, rm / 16, p, s);
+    const auto launch = rm >= 128 ? (scales ? launch_attend_tiles_8bit : p.sinks ? launch_attend_tiles_sinks : launch_attend_tiles)
+                                  : (scales ? launch_attend_rows_8bit : p.sinks ? launch_attend_rows_sinks : launch_attend_rows);
+    const cudaError_t e = launch((int)a.dtype, (int)a.dim, rm >= 128 ? rm : rm / 16, p, s);
     if (e != cudaSuccess) return SV_ECUDA;
     if (launch_attend_join((int)a.dtype, (int)a.dim, rm, p, s) != cudaSuccess) return SV_ECUDA;
     return SV_OK;
+}
+
+}  // namespace
+
+extern "C" int spec_verify_attention(const sv_attention_args* args, void* stream) {
+    return attend(args, 0, nullptr, stream);
+}
+
+extern "C" int spec_verify_attention_ex(const sv_attention_args* args, const sv_attention_options* options,
+                                        void* stream) {
+    if (!options) return attend(args, 0, nullptr, stream);
+    if (options->struct_size != sizeof(sv_attention_options) || options->sinks < 0) return SV_EINVAL;
+    return attend(args, options->sinks, options->scales.k ? &options->scales : nullptr, stream);
 }

@@ -8,6 +8,13 @@
 // result from each CTA that works on it (running maximum, sum and unnormalised output),
 // and the join kernel adds them in order.  A CTA has at most two such units, its first
 // and its last, so the partials need two places a CTA.
+//
+// With a window, the first `sinks` positions stay visible.  A unit's key tiles are then
+// those that hold them and, apart from these, those of the window; the tiles are numbered
+// through, so that the division knows nothing of the gap: key_tile() gives a number's place.
+// Kernels without sinks are compiled apart (SINKS false): the few instructions more cost a
+// prompt's chunk 13% (307 to 350 us), since its softmax has no register and no issue slot to
+// spare, and a round of 64 sequences 6%.
 #pragma once
 
 #include <cuda.h>
@@ -38,6 +45,9 @@ struct AttendArgs {
     int page_shift;      // log2 of page_size, or -1
     int max_row_tiles;   // row tiles of a sequence with all N new tokens
     float qscale;        // scale * log2(e): scores are kept as powers of two
+    int sinks;           // first positions that the window does not hide (0 without a window)
+    int sink_tiles;      // key tiles that hold them
+    sv_cache_scales sc;  // of a cache held in 8 bits (k: null for 16 bits)
     int ctas;            // CTAs that share the work (at most kMaxCtas)
     int64_t capacity;    // positions that the page table addresses
     unsigned long long wait_ns;  // limit of a wait
@@ -51,12 +61,22 @@ constexpr int64_t kMaxRows = 1 << 26;
 
 #ifdef __CUDACC__
 
-// a unit, and its key tiles [t0, t1)
+// a unit, and its key tiles [t0, t1): those below w0 are the sinks', the first of the row
 struct Unit {
     int b, h, rt;
     int past, n;
-    int t0, t1;
+    int t0, t1, w0;
 };
+// the place in the sequence of a unit's key tile
+template <bool SINKS>
+__device__ __forceinline__ int key_tile(const Unit& u, int tile) {
+    return SINKS && tile < u.w0 ? tile - u.t0 : tile;
+}
+// the first positions that a window leaves in sight
+template <bool SINKS>
+__device__ __forceinline__ int sinks_of(const AttendArgs& p) {
+    return SINKS ? p.sinks : 0;
+}
 
 __device__ __forceinline__ int by_group(const AttendArgs& p, int r) {
     return p.group_inv ? (int)__umulhi((uint32_t)r, p.group_inv) : r;
@@ -64,25 +84,31 @@ __device__ __forceinline__ int by_group(const AttendArgs& p, int r) {
 __device__ __forceinline__ int page_of(const AttendArgs& p, int key) {
     return p.page_shift >= 0 ? key >> p.page_shift : key / (int)p.a.cache.page_size;
 }
-// the visible keys [lo, hi] of a tile of rows
+// the visible keys [lo, hi] of a tile of rows, and the sinks below lo
 template <int RM>
 __device__ __forceinline__ void tile_keys(const AttendArgs& p, int past, int n, int rt, int& lo, int& hi) {
     const int r0 = rt * RM, r1 = min(r0 + RM, n * p.group) - 1;
     lo = p.a.window > 0 ? (int)max((int64_t)0, past + by_group(p, r0) + 1 - p.a.window) : 0;
     hi = past + by_group(p, r1);
 }
-template <int RM>
+template <int RM, bool SINKS>
 __device__ __forceinline__ int tile_count(const AttendArgs& p, int past, int n, int rt) {
     int lo, hi;
     tile_keys<RM>(p, past, n, rt, lo, hi);
-    return hi / kKeyTile + 1 - lo / kKeyTile;
+    return hi / kKeyTile + 1 - lo / kKeyTile + (SINKS ? min(p.sink_tiles, lo / kKeyTile) : 0);
 }
-template <int RM>
+template <int RM, bool SINKS>
 __device__ __forceinline__ void unit_tiles(const AttendArgs& p, Unit& u) {
     int lo, hi;
     tile_keys<RM>(p, u.past, u.n, u.rt, lo, hi);
-    u.t0 = lo / kKeyTile;
+    u.w0 = lo / kKeyTile;
+    u.t0 = SINKS ? u.w0 - min(p.sink_tiles, u.w0) : u.w0;
     u.t1 = hi / kKeyTile + 1;
+}
+// whether any row of the tile sees one of `len` keys from k0 on
+template <bool SINKS>
+__device__ __forceinline__ bool any_visible(const AttendArgs& p, int k0, int len, int lo, int hi) {
+    return k0 <= hi && (k0 + len > lo || (SINKS && k0 < p.sinks));
 }
 template <int RM>
 __device__ __forceinline__ int row_tiles(const AttendArgs& p, int n) {
@@ -97,7 +123,7 @@ struct Part {
     int tile;  // in u
     Unit u;
 };
-template <int RM, int NT>
+template <int RM, int NT, bool SINKS>
 __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
     __shared__ long long s_warp[NT / 32];
     __shared__ long long s_before;
@@ -107,12 +133,12 @@ __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
     // key tiles of one head of sequence b, by a thread alone or by a warp
     auto alone = [&](const SeqLens s) -> int {
         int n = 0;
-        for (int rt = row_tiles<RM>(p, s.n); rt-- > 0;) n += tile_count<RM>(p, s.past, s.n, rt);
+        for (int rt = row_tiles<RM>(p, s.n); rt-- > 0;) n += tile_count<RM, SINKS>(p, s.past, s.n, rt);
         return n;
     };
     auto by_warp = [&](const SeqLens s) -> int {
         int n = 0;
-        for (int rt = lane; rt < row_tiles<RM>(p, s.n); rt += 32) n += tile_count<RM>(p, s.past, s.n, rt);
+        for (int rt = lane; rt < row_tiles<RM>(p, s.n); rt += 32) n += tile_count<RM, SINKS>(p, s.past, s.n, rt);
         return warp_sum(n);
     };
     auto lens = [&](int b) -> SeqLens { return seq_lens(p.a.cache, b, (int)p.a.N, p.capacity); };
@@ -228,7 +254,7 @@ __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
     u.h = off >> 31 ? (int)(off / per_head) : (int)((uint32_t)off / (uint32_t)per_head);
     int at = (int)(off - (long long)u.h * per_head);
     for (int rt0 = 0;; rt0 += 32) {  // (at < per_head: a row tile holds it)
-        const int n = rt0 + lane < row_tiles<RM>(p, s.n) ? tile_count<RM>(p, s.past, s.n, rt0 + lane) : 0;
+        const int n = rt0 + lane < row_tiles<RM>(p, s.n) ? tile_count<RM, SINKS>(p, s.past, s.n, rt0 + lane) : 0;
         int x = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -245,13 +271,13 @@ __device__ void find_part(const AttendArgs& p, Part& part, int* s_tiles) {
         at -= __shfl_sync(0xFFFFFFFFu, x, 31);
         if (rt0 + 32 >= row_tiles<RM>(p, s.n)) break;
     }
-    unit_tiles<RM>(p, u);
+    unit_tiles<RM, SINKS>(p, u);
     part.tile = u.t0 + at;
     if (t == 0) p.cut[c] = Cut{begin - at, begin - at + (u.t1 - u.t0), per, more, ctas, u.b, u.h, u.rt, u.n};
 }
 
 // the unit after u (there is one: the caller counts tiles)
-template <int RM>
+template <int RM, bool SINKS>
 __device__ __forceinline__ void next_unit(const AttendArgs& p, Unit& u) {
     if (++u.rt == row_tiles<RM>(p, u.n)) {
         u.rt = 0;
@@ -265,7 +291,7 @@ __device__ __forceinline__ void next_unit(const AttendArgs& p, Unit& u) {
             } while (u.n == 0 && u.b + 1 < p.a.B);
         }
     }
-    unit_tiles<RM>(p, u);
+    unit_tiles<RM, SINKS>(p, u);
 }
 
 // Rows that no unit covers: zeros past a sequence's new tokens, NaN for a sequence whose
@@ -316,6 +342,39 @@ __device__ __forceinline__ float weight_base(float ref) {
     return ref == -INFINITY ? 0.0f : ref - kLift<T>;
 }
 
+// Cache held in 8 bits.  Four codes as two pairs in fp16 (exact):
+__device__ __forceinline__ void codes_half(uint32_t w, uint32_t& b0, uint32_t& b1) {
+    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\ncvt.rn.f16x2.e4m3x2 %0, lo;\ncvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+        : "=r"(b0), "=r"(b1)
+        : "r"(w));
+}
+// query rows of D elements, swizzled likewise
+template <int D>
+__device__ __forceinline__ uint32_t q_at(int r, int c) {
+    return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
+}
+// the scales of a block of positions:
+__device__ __forceinline__ float key_scale(const AttendArgs& p, int h, int page, int in_page) {
+    return p.sc.k[page * p.sc.k_stride_page + h * p.sc.k_stride_head + in_page / SV_SCALE_BLOCK];
+}
+__device__ __forceinline__ float value_scale(const AttendArgs& p, int h, int page, int in_page) {
+    return p.sc.v[page * p.sc.v_stride_page + h * p.sc.v_stride_head + in_page / SV_SCALE_BLOCK];
+}
+// What scores are multiplied by: not 0, which would make NaN of a masked one (-inf); a NaN stays
+__device__ __forceinline__ float score_factor(float row, float scale) {
+    const float f = row * scale;
+    return f < 1.17549435e-38f ? 1.17549435e-38f : f;
+}
+// The least that scales of values are held against, so that a block of zeros divides by something.
+constexpr float kLeastScale = 7.88860905e-31f;  // 2^-100
+// The codes are exact in fp16, so the products are formed in it.  A row of bf16 queries is brought
+// into its range by a power of two, given as the exponent bits of a float (those of its inverse
+// are (254 << 23) - them): its largest element goes to [2^14, 2^15), its sums stay below 2^31.
+__device__ __forceinline__ int row_lift(float largest) {
+    const int e = (__float_as_int(largest) >> 23) - 127;  // (0 and subnormal: as the smallest normal)
+    return min(127 + 14 - e, 253) << 23;
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {  // 2^x; 2^-inf = 0
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -333,6 +392,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // tensor maps of the pages, a head's rows in parts of 64 elements (128 bytes, swizzled):
 // boxes of `box` rows and `parts` parts
 bool encode_pages(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, int parts);
+// of a cache held in 8 bits: boxes of `box` whole rows of a head, swizzled or as they are
+bool encode_codes(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, bool swizzled);
 
 // Launch whose start may overlap with the end of the kernel before it on the stream; the
 // kernels wait for that one with grid_dependency_wait() before they read anything.
@@ -352,8 +413,13 @@ inline cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, siz
 }
 
 // the two kernels' launchers (RM rows a tile) and the join of the cut units
+// (compiled apart: plain calls, those with sinks, and those over a cache held in 8 bits)
 cudaError_t launch_attend_rows(int dtype, int dim, int mt, const AttendArgs& p, cudaStream_t s);
+cudaError_t launch_attend_rows_sinks(int dtype, int dim, int mt, const AttendArgs& p, cudaStream_t s);
+cudaError_t launch_attend_rows_8bit(int dtype, int dim, int mt, const AttendArgs& p, cudaStream_t s);
 cudaError_t launch_attend_tiles(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s);
+cudaError_t launch_attend_tiles_sinks(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s);
+cudaError_t launch_attend_tiles_8bit(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s);
 cudaError_t launch_attend_join(int dtype, int dim, int rm, const AttendArgs& p, cudaStream_t s);
 
 }  // namespace sv

@@ -26,6 +26,9 @@ namespace {
 int (*g_logits)(const sv_logits_args*, void*) = nullptr;
 int (*g_rotate)(const sv_rotate_args*, void*) = nullptr;
 int (*g_attention)(const sv_attention_args*, void*) = nullptr;
+int (*g_rotate_ex)(const sv_rotate_args*, const sv_rotate_options*, void*) = nullptr;
+int (*g_attention_ex)(const sv_attention_args*, const sv_attention_options*, void*) = nullptr;
+int (*g_sample)(const sv_sample_args*, void*) = nullptr;
 size_t (*g_attention_ws)(int64_t, int64_t, int64_t, int64_t, int64_t) = nullptr;
 PyObject* g_error = nullptr;  // raises for a status: g_error(status)
 
@@ -91,6 +94,30 @@ inline bool pages(PyObject* ko, PyObject* vo, const at::Device& d, const at::Ten
     return (s == at::kBFloat16 || s == at::kHalf) && on(x, d, s) && on(y, d, s) && x.dim() == 4 && x.sizes() == y.sizes() &&
            x.size(2) >= 16 && x.size(2) % 16 == 0 && rows(x) && rows(y);
 }
+// a PagedCache8's codes and scales
+inline bool codes(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso, const at::Device& d, const at::Tensor** k,
+                  const at::Tensor** v, sv_cache_scales* sc) {
+    const at::Tensor *ks, *vs;
+    if (!tensor(ko, k) || !tensor(vo, v) || !tensor(kso, &ks) || !tensor(vso, &vs)) return false;
+    for (const at::Tensor* t : {*k, *v})
+        if (!on(*t, d, at::kFloat8_e4m3fn) || t->dim() != 4 || t->sizes() != (*k)->sizes() || t->stride(3) != 1 ||
+            ((t->stride(0) | t->stride(1) | t->stride(2)) & 15) || ((uintptr_t)t->data_ptr() & 15))
+            return false;
+    const int64_t P = (*k)->size(2);
+    if (P < 16 || P % 16) return false;
+    for (const at::Tensor* t : {ks, vs})
+        if (!on(*t, d, at::kFloat) || t->dim() != 3 || t->size(0) != (*k)->size(0) || t->size(1) != (*k)->size(1) ||
+            t->size(2) != P / SV_SCALE_BLOCK || (t->stride(2) != 1 && t->size(2) > 1))
+            return false;
+    sc->k = ks->data_ptr<float>(), sc->v = vs->data_ptr<float>();
+    sc->k_stride_page = ks->stride(0), sc->k_stride_head = ks->stride(1);
+    sc->v_stride_page = vs->stride(0), sc->v_stride_head = vs->stride(1);
+    return true;
+}
+// q's type, as the kernels take it over this cache
+inline bool q_type(at::ScalarType q, const at::Tensor& k, bool eight) {
+    return eight ? q == at::kBFloat16 || q == at::kHalf : q == k.scalar_type();
+}
 inline void fill(sv_paged_cache* c, const at::Tensor& k, const at::Tensor& v, const at::Tensor& pt, const void* lens,
                  const void* fresh) {
     c->k_pages = k.data_ptr(), c->v_pages = v.data_ptr();
@@ -114,17 +141,21 @@ at::Tensor& scratch(const at::Device& d, void* stream, int64_t bytes) {
 }
 
 // attention(q, cache's k, v, page_table, cache_lens, num_new, scale (None: the default), window, max_context, out,
-//           row_status, wait_limit_ns)
+//           row_status, wait_limit_ns, sinks, an 8-bit cache's k_scales, v_scales (None: 16 bits))
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     const at::Tensor *q, *ck, *cv, *pt, *given = nullptr;
-    if (n != 12 || !tensor(a[0], &q) || q->dim() != 4) SV_NONE;
+    if (n != 15 || !tensor(a[0], &q) || q->dim() != 4) SV_NONE;
     const at::Device d = q->device();
     const int64_t B = q->size(0), N = q->size(1), Hq = q->size(2), D = q->size(3);
-    if (!current(d) || !pages(a[1], a[2], d, &ck, &cv)) SV_NONE;
+    const bool eight = a[13] != Py_None;
+    sv_attention_options x;
+    std::memset(&x, 0, sizeof x);
+    if (!current(d) || !(eight ? codes(a[1], a[2], a[13], a[14], d, &ck, &cv, &x.scales) : pages(a[1], a[2], d, &ck, &cv)))
+        SV_NONE;
     const int64_t Hkv = ck->size(1);
-    const at::ScalarType s = ck->scalar_type();
-    if (q->scalar_type() != s || D != ck->size(3) || !rows(*q) || Hkv < 1 || Hq % Hkv || B == 0) SV_NONE;
+    const at::ScalarType s = q->scalar_type();
+    if (!q_type(s, *ck, eight) || D != ck->size(3) || !rows(*q) || Hkv < 1 || Hq % Hkv || B == 0) SV_NONE;
     const void *lens, *fresh, *status;
     if (!page_table(a[3], d, B, &pt) || !vec(a[4], d, at::kInt, B, &lens) || !lens || !vec(a[5], d, at::kInt, B, &fresh) ||
         !vec(a[10], d, at::kInt, B, &status))
@@ -138,7 +169,9 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.window = PyLong_AsLongLong(a[7]);
     g.max_context = a[8] == Py_None ? 0 : PyLong_AsLongLong(a[8]);
     g.wait_limit_ns = PyLong_AsUnsignedLongLong(a[11]);
-    if (PyErr_Occurred() || g.window < 0) SV_NONE;
+    x.struct_size = sizeof x;
+    x.sinks = PyLong_AsLongLong(a[12]);
+    if (PyErr_Occurred() || g.window < 0 || x.sinks < 0) SV_NONE;
     void* stream = at::cuda::getCurrentCUDAStream(d.index()).stream();
     const size_t bytes = g_attention_ws(B, N, Hq, Hkv, D);
     if (bytes == 0) SV_NONE;
@@ -154,22 +187,27 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.workspace = ws.data_ptr();
     g.workspace_bytes = ws.numel();
     g.row_status = (uint32_t*)status;
-    return done(g_attention(&g, stream), out);
+    return done(eight || x.sinks ? g_attention_ex(&g, &x, stream) : g_attention(&g, stream), out);
     END_HANDLE_TH_ERRORS
 }
 
-// rotate(q, k, v, table, cache's k, v, page_table, cache_lens, num_new, interleaved, out, row_status)
+// rotate(q, k, v, table, cache's k, v, page_table, cache_lens, num_new, interleaved, out, row_status, an 8-bit cache's
+//        k_scales, v_scales (None: 16 bits))
 PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     const at::Tensor *q, *k, *v, *tab, *ck, *cv, *pt, *given = nullptr;
-    if (n != 12 || !tensor(a[0], &q) || !tensor(a[1], &k) || !tensor(a[2], &v) || !tensor(a[3], &tab) || q->dim() != 4)
+    if (n != 14 || !tensor(a[0], &q) || !tensor(a[1], &k) || !tensor(a[2], &v) || !tensor(a[3], &tab) || q->dim() != 4)
         SV_NONE;
     const at::Device d = q->device();
     const int64_t B = q->size(0), N = q->size(1), Hq = q->size(2), D = q->size(3);
-    if (!current(d) || !pages(a[4], a[5], d, &ck, &cv)) SV_NONE;
+    const bool eight = a[12] != Py_None;
+    sv_rotate_options x;
+    std::memset(&x, 0, sizeof x);
+    if (!current(d) || !(eight ? codes(a[4], a[5], a[12], a[13], d, &ck, &cv, &x.scales) : pages(a[4], a[5], d, &ck, &cv)))
+        SV_NONE;
     const int64_t Hkv = ck->size(1);
-    const at::ScalarType s = ck->scalar_type();
-    if (q->scalar_type() != s || D != ck->size(3) || !rows(*q) || B == 0 || !same_rows(*k, d, s, B, N, Hkv, D) ||
+    const at::ScalarType s = q->scalar_type();
+    if (!q_type(s, *ck, eight) || D != ck->size(3) || !rows(*q) || B == 0 || !same_rows(*k, d, s, B, N, Hkv, D) ||
         !same_rows(*v, d, s, B, N, Hkv, D))
         SV_NONE;
     if (!on(*tab, d, at::kFloat) || tab->dim() != 3 || tab->size(1) != 2 || !tab->is_contiguous() || tab->size(2) < 8 ||
@@ -202,7 +240,9 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.rot_dim = 2 * tab->size(2);
     g.interleaved = turn;
     g.row_status = (uint32_t*)status;
-    return done(g_rotate(&g, at::cuda::getCurrentCUDAStream(d.index()).stream()), out);
+    x.struct_size = sizeof x;
+    void* stream = at::cuda::getCurrentCUDAStream(d.index()).stream();
+    return done(eight ? g_rotate_ex(&g, &x, stream) : g_rotate(&g, stream), out);
     END_HANDLE_TH_ERRORS
 }
 
@@ -281,11 +321,56 @@ PyObject* logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// setup(addresses of the four C functions, the function that raises for a status)
+// sample(logits, uniforms, temperature, top_k, top_p, min_p, row_status): (tokens, probs)
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor *x, *u;
+    if (n != 7 || !tensor(a[0], &x) || !tensor(a[1], &u) || x->dim() != 3) SV_NONE;
+    const at::Device d = x->device();
+    const int64_t B = x->size(0), N = x->size(1), V = x->size(2);
+    if (!current(d) || (x->scalar_type() != at::kFloat && x->scalar_type() != at::kBFloat16) || x->stride(2) != 1 ||
+        B == 0 || !on(*u, d, at::kFloat) || u->dim() != 2 || u->size(0) != B || u->size(1) != N ||
+        (u->stride(1) != 1 && N > 1))
+        SV_NONE;
+    const void *temperature, *top_k, *top_p, *min_p, *status;
+    if (!vec(a[2], d, at::kFloat, B, &temperature) || !vec(a[3], d, at::kInt, B, &top_k) ||
+        !vec(a[4], d, at::kFloat, B, &top_p) || !vec(a[5], d, at::kFloat, B, &min_p) || !vec(a[6], d, at::kInt, B, &status))
+        SV_NONE;
+    at::Tensor tokens = at::empty({B, N}, x->options().dtype(at::kInt)), probs = at::empty({B, N}, u->options());
+    sv_sample_args g;
+    std::memset(&g, 0, sizeof g);
+    g.struct_size = sizeof g;
+    g.logits = x->data_ptr();
+    g.dtype = x->scalar_type() == at::kFloat ? SV_F32 : SV_BF16;
+    g.B = B, g.N = N, g.V = V;
+    g.stride_b = x->stride(0), g.stride_n = x->stride(1);
+    g.uniforms = u->data_ptr<float>();
+    g.uniform_stride = u->stride(0);
+    g.temperature = (const float*)temperature;
+    g.top_k = (const int32_t*)top_k;
+    g.top_p = (const float*)top_p;
+    g.min_p = (const float*)min_p;
+    g.tokens = tokens.data_ptr<int32_t>();
+    g.probs = probs.data_ptr<float>();
+    g.row_status = (uint32_t*)status;
+    PyObject* t = done(g_sample(&g, at::cuda::getCurrentCUDAStream(d.index()).stream()), tokens);
+    if (!t) return nullptr;
+    PyObject* p = THPVariable_Wrap(probs);
+    PyObject* both = p ? PyTuple_Pack(2, t, p) : nullptr;
+    Py_DECREF(t);
+    Py_XDECREF(p);
+    return both;
+    END_HANDLE_TH_ERRORS
+}
+
+// setup(addresses of the C functions, the function that raises for a status)
 PyObject* setup(PyObject*, PyObject* args) {
-    unsigned long long l, r, t, w;
+    unsigned long long l, r, t, w, rx, tx, m;
     PyObject* e;
-    if (!PyArg_ParseTuple(args, "KKKKO", &l, &r, &t, &w, &e)) return nullptr;
+    if (!PyArg_ParseTuple(args, "KKKKKKKO", &l, &r, &t, &w, &rx, &tx, &m, &e)) return nullptr;
+    g_rotate_ex = (decltype(g_rotate_ex))rx;
+    g_attention_ex = (decltype(g_attention_ex))tx;
+    g_sample = (decltype(g_sample))m;
     g_logits = (decltype(g_logits))l;
     g_rotate = (decltype(g_rotate))r;
     g_attention = (decltype(g_attention))t;
@@ -298,6 +383,7 @@ PyObject* setup(PyObject*, PyObject* args) {
 PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, nullptr},
                          {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, nullptr},
                          {"rotate", (PyCFunction)(void (*)(void))rotate, METH_FASTCALL, nullptr},
+                         {"sample", (PyCFunction)(void (*)(void))sample, METH_FASTCALL, nullptr},
                          {"logits", (PyCFunction)(void (*)(void))logits, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", "Short way to the target-step operators.", -1, methods,

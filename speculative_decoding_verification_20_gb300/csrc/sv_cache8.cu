@@ -1,0 +1,83 @@
+// sv_cache8.cu -- reading back what a cache held in 8 bits stands for (spec_verify_read_cache).
+//
+// A block has one position; a thread takes 16 codes of a head's row, keys or values, and
+// writes 16 numbers.  The call is bound by its bytes (1 read, 2 written an element), small
+// ones by the chain lengths -> page id -> codes.
+#include <cuda_runtime.h>
+
+#include "sv_internal.cuh"
+#include "sv_paged.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kReadThreads = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ sv_read_args a) {
+    const int b = (int)(blockIdx.x / (unsigned)a.N), i = (int)(blockIdx.x % (unsigned)a.N);
+    const int H = (int)a.kv_heads, per = (int)a.dim / 16;
+    const SeqLens sl = seq_lens(a.cache, b, (int)a.N, a.cache.pages_per_seq * a.cache.page_size);
+    if (sl.bad && threadIdx.x == 0 && i == 0 && a.row_status) atomicOr(a.row_status + b, SV_ROW_BAD_LENGTH);
+    const bool live = i < sl.n;
+    bool nan = sl.bad;
+    int64_t page = 0, slot = 0;
+    if (live) {
+        const int pos = sl.past + i, at = pos / (int)a.cache.page_size;
+        page = a.cache.page_table[b * a.cache.page_table_stride + at];
+        slot = pos - at * (int)a.cache.page_size;
+        if (page < 0 || page >= a.cache.pages) {
+            nan = true;
+            if (threadIdx.x == 0 && a.row_status) atomicOr(a.row_status + b, SV_ROW_BAD_PAGE);
+        }
+    }
+    for (int x = threadIdx.x; x < 2 * H * per; x += kReadThreads) {
+        const bool keys = x < H * per;
+        const int y = keys ? x : x - H * per, h = y / per, c = y % per * 16;
+        const uint32_t none = nan ? Pair<T>::pack(NAN, NAN) : 0u;
+        uint32_t w[8] = {none, none, none, none, none, none, none, none};
+        if (live && !nan) {
+            const uint8_t* src = keys ? (const uint8_t*)a.cache.k_pages + page * a.cache.k_stride_page +
+                                            h * a.cache.k_stride_head + slot * a.cache.k_stride_slot
+                                      : (const uint8_t*)a.cache.v_pages + page * a.cache.v_stride_page +
+                                            h * a.cache.v_stride_head + slot * a.cache.v_stride_slot;
+            const float s = keys ? a.scales.k[page * a.scales.k_stride_page + h * a.scales.k_stride_head + slot / SV_SCALE_BLOCK]
+                                 : a.scales.v[page * a.scales.v_stride_page + h * a.scales.v_stride_head + slot / SV_SCALE_BLOCK];
+            const uint4 q = *reinterpret_cast<const uint4*>(src + c);
+            const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 f = e4m3_pair(qs[e / 2] >> (e % 2 * 16));
+                w[e] = Pair<T>::pack(f.x * s, f.y * s);
+            }
+        }
+        T* dst = (T*)(keys ? a.k_out : a.v_out) + (((int64_t)b * a.N + i) * H + h) * a.dim + c;
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+}  // namespace
+}  // namespace sv
+
+extern "C" int spec_verify_read_cache(const sv_read_args* args, void* stream) {
+    if (!args || args->struct_size != sizeof(sv_read_args)) return SV_EINVAL;
+    const sv_read_args& a = *args;
+    if (a.dtype != SV_BF16 && a.dtype != SV_F16) return SV_EUNSUPPORTED;
+    if (a.B < 0 || a.N < 1 || a.kv_heads < 1 || a.dim < 16 || a.dim % 16) return SV_EINVAL;
+    if (a.dim > SV_MAX_HEAD_DIM || a.B > SV_MAX_BATCH || a.N > 0x7FFFFFFF || a.kv_heads > 65536 ||
+        (double)a.B * a.N > 2147483647.0)
+        return SV_ETOO_LARGE;
+    if (a.B == 0) return SV_OK;
+    if (!a.k_out || !a.v_out || (((uintptr_t)a.k_out | (uintptr_t)a.v_out) & 15u)) return SV_EINVAL;
+    int rc = sv::check_cache(a.cache, a.B, a.kv_heads, a.dim, 1);
+    if (rc == SV_OK) rc = sv::check_scales(a.scales, a.cache, a.kv_heads);
+    if (rc != SV_OK) return rc;
+    const unsigned grid = (unsigned)(a.B * a.N);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (a.dtype == SV_BF16)
+        sv::read_kernel<__nv_bfloat16><<<grid, sv::kReadThreads, 0, s>>>(a);
+    else
+        sv::read_kernel<__half><<<grid, sv::kReadThreads, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ECUDA;
+}

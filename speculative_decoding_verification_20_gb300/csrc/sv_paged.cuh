@@ -38,6 +38,26 @@ struct Pair<__half> {
     }
 };
 
+// the low two codes of w as a pair of 16-bit numbers (exact), and as 32-bit ones
+__device__ __forceinline__ uint32_t e4m3_half2(uint32_t w) {
+    uint32_t h;
+    asm("{\n.reg .b16 c;\ncvt.u16.u32 c, %1;\ncvt.rn.f16x2.e4m3x2 %0, c;\n}\n" : "=r"(h) : "r"(w));
+    return h;
+}
+__device__ __forceinline__ float2 e4m3_pair(uint32_t w) {
+    const uint32_t h = e4m3_half2(w);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// two numbers as codes, lo in the low byte; infinities become NaN (the conversion alone would
+// make them the largest value)
+__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
+    if (isinf(lo)) lo = NAN;
+    if (isinf(hi)) hi = NAN;
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(lo), "f"(hi));
+    return c;
+}
+
 // Cached and new tokens of a sequence.  bad: lengths that no result can be given
 // for (n is 0 then); capacity: positions that the page table can address.
 struct SeqLens {
@@ -54,8 +74,8 @@ __device__ __forceinline__ SeqLens seq_lens(const sv_paged_cache& c, int b, int 
 }
 #endif  // __CUDACC__
 
-// host checks of the cache's description (dim: elements of a head's row)
-inline int check_cache(const sv_paged_cache& c, int64_t B, int64_t kv_heads, int64_t dim) {
+// host checks of the cache's description (dim: elements of a head's row; of `size` bytes)
+inline int check_cache(const sv_paged_cache& c, int64_t B, int64_t kv_heads, int64_t dim, int size = 2) {
     if (!c.k_pages || !c.v_pages || !c.page_table || !c.cache_lens) return SV_EINVAL;
     if (c.pages < 1 || c.page_size < 16 || c.page_size % 16 || c.pages_per_seq < 1) return SV_EINVAL;
     if (c.pages > 0x7FFFFFFF || c.page_size > 65536 || c.pages_per_seq > 0x7FFFFFFF) return SV_ETOO_LARGE;
@@ -64,9 +84,18 @@ inline int check_cache(const sv_paged_cache& c, int64_t B, int64_t kv_heads, int
     const int64_t st[6] = {c.k_stride_page, c.k_stride_head, c.k_stride_slot,
                            c.v_stride_page, c.v_stride_head, c.v_stride_slot};
     for (int64_t x : st)
-        if (x < 0 || x % 8) return SV_EINVAL;
+        if (x < 0 || x % (16 / size)) return SV_EINVAL;
     if (c.k_stride_slot < dim || c.v_stride_slot < dim) return SV_EINVAL;
     if (kv_heads > 1 && (c.k_stride_head < dim || c.v_stride_head < dim)) return SV_EINVAL;
+    return SV_OK;
+}
+
+inline int check_scales(const sv_cache_scales& s, const sv_paged_cache& c, int64_t kv_heads) {
+    if (!s.k || !s.v || (((uintptr_t)s.k | (uintptr_t)s.v) & 3u)) return SV_EINVAL;
+    if (s.k_stride_page < 0 || s.k_stride_head < 0 || s.v_stride_page < 0 || s.v_stride_head < 0) return SV_EINVAL;
+    const int64_t n = c.page_size / SV_SCALE_BLOCK;  // two scales on one address would be one scale
+    if (kv_heads > 1 && (s.k_stride_head < n || s.v_stride_head < n)) return SV_EINVAL;
+    if (c.pages > 1 && (s.k_stride_page < n || s.v_stride_page < n)) return SV_EINVAL;
     return SV_OK;
 }
 

@@ -13,6 +13,13 @@
 // two heads in flight 29.0, six 30.8, blocks of 256 threads 37.6 us.)  The call is bound by
 // reading q, k, v and writing q', k', v' once; small ones by the chain lengths -> page id ->
 // store.
+//
+// Into a cache held in 8 bits the token's blocks do q alone, and further blocks of the same
+// launch take one head's keys or values of 16 positions each, which share a scale: live
+// elements of the block, new and held, in registers; their largest across the block; codes
+// and scale written.  A key next to the border between two codes goes to one or the other:
+// its rotation is formed without error and rounded to odd in 32 bits, so that the one rounding
+// to a code that follows is that of the exact value.
 #include <cuda_runtime.h>
 
 #include "sv_internal.cuh"
@@ -46,8 +53,160 @@ __device__ __forceinline__ void rotate16(uint4& x0, uint4& x1, const float (&cs)
     x1 = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+// 8-bit cache: blocks of 16 positions that the N new tokens of a sequence can touch
+__host__ __device__ inline int64_t touched_blocks(int64_t N) { return (N + SV_SCALE_BLOCK - 2) / SV_SCALE_BLOCK + 1; }
+
+// (hi + lo) rounded to odd: hi is the sum rounded to nearest, lo what is missing; of the two numbers
+// around the exact one the odd one, from which a second rounding to fewer bits is the right one
+__device__ __forceinline__ float to_odd(float hi, float lo) {
+    if (lo == 0.0f || !isfinite(hi)) return hi;
+    if (hi == 0.0f) return lo;
+    const int w = __float_as_int(hi);
+    return w & 1 ? hi : __int_as_float(w + ((lo > 0.0f) == (hi > 0.0f) ? 1 : -1));
+}
+// a + b and its rounding error (the error is exact whatever the sizes)
+__device__ __forceinline__ float two_sum(float a, float b, float& err) {
+    const float s = __fadd_rn(a, b), bv = __fsub_rn(s, a), av = __fsub_rn(s, bv);
+    err = __fadd_rn(__fsub_rn(b, bv), __fsub_rn(a, av));
+    return s;
+}
+// a c + b s, rounded to odd: products and their errors, then the sum and its own
+__device__ __forceinline__ float dot2_odd(float a, float c, float b, float s) {
+    const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
+    const float pe = __fmaf_rn(a, c, -p), qe = __fmaf_rn(b, s, -q);
+    float e, f;
+    const float hi = two_sum(p, q, e);
+    const float g = two_sum(pe, qe, f);
+    const float lo = __fadd_rn(e, g);
+    return to_odd(hi, lo != 0.0f ? lo : f);
+}
+
+// One head's keys or values of a block of 16 positions, by a CTA of the launch: item x of
+// [B][touched blocks][2 kv_heads].
 template <typename T>
-__global__ void __launch_bounds__(kRThreads) rotate_kernel(const __grid_constant__ sv_rotate_args a) {
+__device__ __forceinline__ void append8(const sv_rotate_args& a, const sv_cache_scales& sc, unsigned x) {
+    constexpr int kTok = SV_SCALE_BLOCK, kMaxIter = 2;  // (dim <= 256: 16 threads a token at most)
+    __shared__ float s_top[kRThreads / 32];
+    const int t = threadIdx.x, Hkv = (int)a.kv_heads;
+    const unsigned nb = (unsigned)touched_blocks(a.N);
+    const int item = (int)(x % (2u * Hkv));
+    const unsigned rest = x / (2u * Hkv);
+    const int b = (int)(rest / nb);
+    const bool keys = item < Hkv;
+    const int h = keys ? item : item - Hkv;
+    const int64_t table_cap = a.cache.pages_per_seq * a.cache.page_size;
+    const SeqLens sl = seq_lens(a.cache, b, (int)a.N, a.table_len < table_cap ? a.table_len : table_cap);
+    const int p0 = (sl.past / kTok + (int)(rest % nb)) * kTok;  // the block's first position
+    if (sl.n == 0 || p0 >= sl.past + sl.n) return;
+    const int at = p0 / (int)a.cache.page_size;
+    const int page = a.cache.page_table[b * a.cache.page_table_stride + at];
+    const int64_t slot = p0 - at * (int)a.cache.page_size;
+    if (page < 0 || page >= a.cache.pages) {
+        if (t == 0 && a.row_status) atomicOr(a.row_status + b, SV_ROW_BAD_PAGE);
+        return;
+    }
+    const int64_t cache_slot = keys ? a.cache.k_stride_slot : a.cache.v_stride_slot;
+    uint8_t* codes = keys ? (uint8_t*)a.cache.k_pages + page * a.cache.k_stride_page + h * a.cache.k_stride_head
+                          : (uint8_t*)a.cache.v_pages + page * a.cache.v_stride_page + h * a.cache.v_stride_head;
+    codes += slot * cache_slot;
+    float* scale_at = (keys ? sc.k + page * sc.k_stride_page + h * sc.k_stride_head
+                            : sc.v + page * sc.v_stride_page + h * sc.v_stride_head) + slot / kTok;
+    const float held_scale = p0 < sl.past ? *scale_at : 1.0f;
+    const int per = (int)a.dim / 16, sets = kRThreads / per, half = (int)a.rot_dim / 2;
+    const int j = t % per, set = t / per;
+    const bool turns = keys && 16 * j < a.rot_dim;
+    const int e0 = turns && !a.interleaved ? 8 * j : 16 * j;
+    const int e1 = turns && !a.interleaved ? half + 8 * j : 16 * j + 8;
+    float v[kMaxIter][16];
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMaxIter; ++i) {
+        const int tok = set + i * sets, pos = p0 + tok;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[i][e] = 0.0f;
+        if (set >= sets || tok >= kTok || pos >= sl.past + sl.n) continue;
+        if (pos < sl.past) {
+            const uint8_t* src = codes + tok * cache_slot;
+            const uint2 w0 = *reinterpret_cast<const uint2*>(src + e0), w1 = *reinterpret_cast<const uint2*>(src + e1);
+            const uint32_t w[4] = {w0.x, w0.y, w1.x, w1.y};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 f = e4m3_pair(w[e / 2] >> (e % 2 * 16));
+                v[i][2 * e] = f.x * held_scale, v[i][2 * e + 1] = f.y * held_scale;
+            }
+        } else {
+            const int64_t n = pos - sl.past;
+            const T* src = keys ? (const T*)a.k + b * a.k_stride_b + n * a.k_stride_n + h * a.k_stride_h
+                                : (const T*)a.v + b * a.v_stride_b + n * a.v_stride_n + h * a.v_stride_h;
+            const uint4 x0 = *reinterpret_cast<const uint4*>(src + e0), x1 = *reinterpret_cast<const uint4*>(src + e1);
+            const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 f = Pair<T>::unpack(w[e]);
+                v[i][2 * e] = f.x, v[i][2 * e + 1] = f.y;
+            }
+            if (turns) {
+                float cs[8], sn[8];
+                const float4* c4 = reinterpret_cast<const float4*>(a.table + (int64_t)pos * a.rot_dim + 8 * j);
+                const float4* s4 = reinterpret_cast<const float4*>(a.table + (int64_t)pos * a.rot_dim + half + 8 * j);
+                *reinterpret_cast<float4*>(cs) = __ldg(c4);
+                *reinterpret_cast<float4*>(cs + 4) = __ldg(c4 + 1);
+                *reinterpret_cast<float4*>(sn) = __ldg(s4);
+                *reinterpret_cast<float4*>(sn + 4) = __ldg(s4 + 1);
+                if (a.interleaved) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float f = v[i][2 * e], g = v[i][2 * e + 1];
+                        v[i][2 * e] = dot2_odd(f, cs[e], -g, sn[e]);
+                        v[i][2 * e + 1] = dot2_odd(g, cs[e], f, sn[e]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float f = v[i][e], g = v[i][e + 8];
+                        v[i][e] = dot2_odd(f, cs[e], -g, sn[e]);
+                        v[i][e + 8] = dot2_odd(g, cs[e], f, sn[e]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (isfinite(v[i][e])) top = fmaxf(top, fabsf(v[i][e]));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (t % 32 == 0) s_top[t / 32] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kRThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+    // the least power of two s with top <= 448 s = 1.75 2^8 s: from top's exponent and fraction bits
+    const int bits = __float_as_int(top);
+    const int k = max((bits >> 23) - 127 - ((bits & 0x7FFFFF) <= 0x600000 ? 8 : 7), -126);
+    const float scale = top > 0.0f ? __int_as_float((k + 127) << 23) : 1.0f;
+    const float inv = top > 0.0f ? __int_as_float((127 - k) << 23) : 1.0f;
+    if (t == 0) *scale_at = scale;
+#pragma unroll
+    for (int i = 0; i < kMaxIter; ++i) {
+        const int tok = set + i * sets, pos = p0 + tok;
+        if (set >= sets || tok >= kTok || pos >= sl.past + sl.n || (pos < sl.past && scale == held_scale)) continue;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = to_e4m3(v[i][4 * e] * inv, v[i][4 * e + 1] * inv) |
+                                           to_e4m3(v[i][4 * e + 2] * inv, v[i][4 * e + 3] * inv) << 16;
+        uint8_t* dst = codes + tok * cache_slot;
+        *reinterpret_cast<uint2*>(dst + e0) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(dst + e1) = make_uint2(w[2], w[3]);
+    }
+}
+
+template <typename T, bool E8>
+__global__ void __launch_bounds__(kRThreads) rotate_kernel(const __grid_constant__ sv_rotate_args a,
+                                                           const __grid_constant__ sv_cache_scales sc) {
+    if (E8 && blockIdx.x >= (unsigned)(a.B * a.N)) {
+        append8<T>(a, sc, blockIdx.x - (unsigned)(a.B * a.N));
+        return;
+    }
     const int per = (int)a.dim / 16;          // threads of a head
     const int sets = kRThreads / per;         // heads at once
     const int j = threadIdx.x % per, set = threadIdx.x / per;
@@ -64,7 +223,7 @@ __global__ void __launch_bounds__(kRThreads) rotate_kernel(const __grid_constant
     const int pos = sl.past + i;
     int page = -1;
     int64_t in_page = 0;
-    if (live) {
+    if (!E8 && live) {
         const int at = pos / (int)a.cache.page_size;
         page = a.cache.page_table[b * a.cache.page_table_stride + at];
         in_page = pos - at * (int)a.cache.page_size;
@@ -73,7 +232,7 @@ __global__ void __launch_bounds__(kRThreads) rotate_kernel(const __grid_constant
             if (threadIdx.x == 0 && a.row_status) atomicOr(a.row_status + b, SV_ROW_BAD_PAGE);
         }
     }
-    const int heads = live ? Hq + 2 * Hkv : Hq;
+    const int heads = live && !E8 ? Hq + 2 * Hkv : Hq;
     auto source = [&](int h) -> const T* {
         if (h < Hq) return (const T*)a.q + b * a.q_stride_b + i * a.q_stride_n + h * a.q_stride_h;
         if (h < Hq + Hkv) return (const T*)a.k + b * a.k_stride_b + i * a.k_stride_n + (h - Hq) * a.k_stride_h;
@@ -126,7 +285,10 @@ __global__ void __launch_bounds__(kRThreads) rotate_kernel(const __grid_constant
 }  // namespace
 }  // namespace sv
 
-extern "C" int spec_verify_rotate_append(const sv_rotate_args* args, void* stream) {
+namespace {
+
+// scales: of a cache held in 8 bits, or null
+int rotate_append(const sv_rotate_args* args, const sv_cache_scales* scales, void* stream) {
     if (!args || args->struct_size != sizeof(sv_rotate_args)) return SV_EINVAL;
     const sv_rotate_args& a = *args;
     if (a.dtype != SV_BF16 && a.dtype != SV_F16) return SV_EUNSUPPORTED;
@@ -144,14 +306,34 @@ extern "C" int spec_verify_rotate_append(const sv_rotate_args* args, void* strea
     if ((a.q_heads > 1 && a.o_stride_h < a.dim) || (a.N > 1 && a.o_stride_n < a.dim) ||
         (a.B > 1 && a.o_stride_b < a.dim))
         return SV_EINVAL;
-    const int rc = sv::check_cache(a.cache, a.B, a.kv_heads, a.dim);
+    int rc = sv::check_cache(a.cache, a.B, a.kv_heads, a.dim, scales ? 1 : 2);
+    if (rc == SV_OK && scales) rc = sv::check_scales(*scales, a.cache, a.kv_heads);
     if (rc != SV_OK) return rc;
-    if ((double)a.B * a.N > 2147483647.0) return SV_ETOO_LARGE;
-    const unsigned grid = (unsigned)(a.B * a.N);
+    const double blocks = (double)a.B * a.N + (scales ? 2.0 * a.B * sv::touched_blocks(a.N) * a.kv_heads : 0.0);
+    if (blocks > 2147483647.0) return SV_ETOO_LARGE;
+    const unsigned grid = (unsigned)blocks;
     cudaStream_t s = (cudaStream_t)stream;
-    if (a.dtype == SV_BF16)
-        sv::rotate_kernel<__nv_bfloat16><<<grid, sv::kRThreads, 0, s>>>(a);
-    else
-        sv::rotate_kernel<__half><<<grid, sv::kRThreads, 0, s>>>(a);
+    const sv_cache_scales none = {};
+    if (scales) {
+        if (a.dtype == SV_BF16)
+            sv::rotate_kernel<__nv_bfloat16, true><<<grid, sv::kRThreads, 0, s>>>(a, *scales);
+        else
+            sv::rotate_kernel<__half, true><<<grid, sv::kRThreads, 0, s>>>(a, *scales);
+    } else if (a.dtype == SV_BF16) {
+        sv::rotate_kernel<__nv_bfloat16, false><<<grid, sv::kRThreads, 0, s>>>(a, none);
+    } else {
+        sv::rotate_kernel<__half, false><<<grid, sv::kRThreads, 0, s>>>(a, none);
+    }
     return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ECUDA;
+}
+
+}  // namespace
+
+extern "C" int spec_verify_rotate_append(const sv_rotate_args* args, void* stream) {
+    return rotate_append(args, nullptr, stream);
+}
+
+extern "C" int spec_verify_rotate_append_ex(const sv_rotate_args* args, const sv_rotate_options* options, void* stream) {
+    if (options && options->struct_size != sizeof(sv_rotate_options)) return SV_EINVAL;
+    return rotate_append(args, options && options->scales.k ? &options->scales : nullptr, stream);
 }

@@ -23,7 +23,7 @@ import ctypes
 import math
 import struct
 import threading
-from typing import Optional, Tuple
+from typing import Optional, Tuple, Union
 
 import torch
 
@@ -33,6 +33,10 @@ ROW_BAD_PENALTY = 0x100
 ROW_BAD_SLOT = 0x200
 ROW_BAD_LENGTH = 0x400
 ROW_BAD_PAGE = 0x800
+ROW_BAD_MIN_P = 0x1000
+ROW_BAD_UNIFORM = 0x2000
+
+SCALE_BLOCK = 16  # tokens that share a scale in an 8-bit cache (SV_SCALE_BLOCK)
 
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: SV_F16}
 
@@ -42,6 +46,12 @@ _LOGITS = struct.Struct("<Q2Q4q4q2Q2q2Q2q3Q3QqQ2qQ")
 _CACHE = "2Q8qQ2q2Q"
 _ROTATE = struct.Struct("<Q4Q6q12qQ3q" + _CACHE + "Q")
 _ATTENTION = struct.Struct("<Q2Q6q6qd2q" + _CACHE + "QqQQ")
+_SCALES = "2Q4q"
+_ROTATE_OPTIONS = struct.Struct("<Q" + _SCALES)
+_ATTENTION_OPTIONS = struct.Struct("<Qq" + _SCALES)
+_READ = struct.Struct("<Q2Q5q" + _CACHE + _SCALES + "Q")
+_SAMPLE = struct.Struct("<QQ6qQq7Q")
+_NO_SCALES = (0, 0, 0, 0, 0, 0)
 
 
 _current_device = torch.cuda.current_device
@@ -76,7 +86,9 @@ class _Short:
                                "__graft_entry__.build()") from e
         address = lambda fn: ctypes.cast(fn, ctypes.c_void_p).value
         _bind.setup(address(lib.spec_verify_process_logits), address(lib.spec_verify_rotate_append),
-                    address(lib.spec_verify_attention), address(lib.spec_verify_attention_workspace_size), _check)
+                    address(lib.spec_verify_attention), address(lib.spec_verify_attention_workspace_size),
+                    address(lib.spec_verify_rotate_append_ex), address(lib.spec_verify_attention_ex),
+                    address(lib.spec_verify_sample), _check)
         _short = _bind
         return getattr(_bind, name)
 
@@ -139,6 +151,7 @@ def _elsewhere(device: torch.device, stream, fn, args, kwargs):
         if stream is not None:
             for t in (*args, *kwargs.values()):
                 for u in t if isinstance(t, (tuple, list)) else \
+                        (t.k, t.v, t.k_scales, t.v_scales) if isinstance(t, PagedCache8) else \
                         (t.k, t.v) if isinstance(t, PagedCache) else \
                         (t.seen, t.counts) if isinstance(t, TokenHistory) else (t,):
                     if isinstance(u, torch.Tensor) and u.is_cuda:
@@ -346,6 +359,70 @@ class PagedCache:
     device = property(lambda self: self.k.device)
 
 
+class PagedCache8:
+    """Keys and values of one layer in pages, held in 8 bits: k, v [pages, kv_heads, page_size, head_dim], float8_e4m3fn
+    codes, and a scale for each 16 tokens and head: k_scales, v_scales float32 [pages, kv_heads, page_size / 16].
+
+    A key is its code times its scale.  ``rotate_append`` keeps the scales at powers of two; ``paged_attention`` and
+    ``read_cache`` take any that are finite and not negative.  Half the memory of a ``PagedCache``, and half the time of
+    what is bound by reading it; values are off by up to 2^-4 of themselves.  The calls read the tensors as they are then.
+    """
+
+    def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
+        shape = (pages, kv_heads, page_size, head_dim)
+        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in "kv")
+        self.k_scales, self.v_scales = (torch.ones((pages, kv_heads, page_size // SCALE_BLOCK), device=device)
+                                        for _ in "kv")
+        _pages8(self)
+
+    @classmethod
+    def from_tensors(cls, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor) -> "PagedCache8":
+        """A cache over the caller's memory; any order of page, head and row in memory (views are fine), as long as
+        the head dimension is contiguous, every row starts on a 16-byte boundary and a head's scales are contiguous."""
+        self = cls.__new__(cls)
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        _pages8(self)
+        return self
+
+    # the tensors may be replaced: nothing else is kept of them
+    pages = property(lambda self: self.k.shape[0])
+    kv_heads = property(lambda self: self.k.shape[1])
+    page_size = property(lambda self: self.k.shape[2])
+    head_dim = property(lambda self: self.k.shape[3])
+    device = property(lambda self: self.k.device)
+
+
+def _pages8(cache: PagedCache8) -> Tuple[tuple, tuple]:
+    """The head of the C description of a cache's pages, and that of its scales, of what it holds now."""
+    k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+        raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim] of one shape, type and device")
+    if k.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"the cache must be float8_e4m3fn, got {k.dtype}")
+    if k.shape[2] < 16 or k.shape[2] % 16:
+        raise ValueError(f"page_size must be a multiple of 16, got {k.shape[2]}")
+    for t in (k, v):
+        if t.stride(3) != 1 or t.data_ptr() % 16 or any(s % 16 for s in t.stride()[:3]):
+            raise ValueError("rows of the cache must be contiguous and start on 16-byte boundaries")
+    want = (k.shape[0], k.shape[1], k.shape[2] // SCALE_BLOCK)
+    for t in (ks, vs):
+        if t.dtype != torch.float32 or t.device != k.device or tuple(t.shape) != want or \
+                (t.stride(2) != 1 and want[2] > 1):
+            raise ValueError(f"scales must be float32 {list(want)} on the cache's device, a head's contiguous")
+    return ((k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], *k.stride()[:3], *v.stride()[:3]),
+            (ks.data_ptr(), vs.data_ptr(), *ks.stride()[:2], *vs.stride()[:2]))
+
+
+def _of_cache(cache, q: torch.Tensor) -> Tuple[tuple, Optional[tuple], torch.dtype]:
+    """A cache's C description, its scales' (None: 16 bits) and the type of the queries."""
+    if isinstance(cache, PagedCache8):
+        pages, scales = _pages8(cache)
+        if q.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+        return pages, scales, q.dtype
+    return _pages(cache), None, cache.dtype
+
+
 def _pages(cache: PagedCache) -> tuple:
     """The head of the C description of a cache: addresses, pages, page size and strides, of what it holds now."""
     k, v = cache.k, cache.v
@@ -431,8 +508,8 @@ def _out_rows(out, shape, dtype, device):
     return out
 
 
-def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, cache: PagedCache,
-                  page_table: torch.Tensor, cache_lens: torch.Tensor, num_new: Optional[torch.Tensor] = None, *,
+def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+                  cache: Union[PagedCache, PagedCache8], page_table: torch.Tensor, cache_lens: torch.Tensor, num_new: Optional[torch.Tensor] = None, *,
                   interleaved: bool = False, out: Optional[torch.Tensor] = None,
                   row_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rotates q [B, N, q_heads, dim] and k [B, N, kv_heads, dim] by their positions, writes k and v to the cache.
@@ -441,10 +518,14 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
     (default: all).  table: from rotary_table, at least as long as the last position; its rotary_dim
     (a multiple of 16) may be less than dim.  Pairs are (j, j + rotary_dim / 2), or (2j, 2j + 1) with
     interleaved.  Returns the rotated q (``out``, which may be q; rows past num_new are zeros).
+    Into a ``PagedCache8`` (q, k, v bfloat16 or float16) each block of 16 positions that gets new tokens gets a new
+    scale, the least power of two that holds what is live in it after the call, and what it held is rescaled; blocks
+    that two sequences write to must be different ones.
     """
     if stream is None:
+        scales = (cache.k_scales, cache.v_scales) if isinstance(cache, PagedCache8) else (None, None)
         res = _short.rotate(q, k, v, table, cache.k, cache.v, page_table, cache_lens, num_new, interleaved, out,
-                            row_status)
+                            row_status, *scales)
         if res is not None:
             return res
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
@@ -454,7 +535,7 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
         return _elsewhere(dev, stream, rotate_append, (q, k, v, table, cache, page_table, cache_lens, num_new), dict(
             interleaved=interleaved, out=out, row_status=row_status))
     B, N, Hq, D = shape
-    pages, dtype = _pages(cache), cache.dtype
+    pages, scales, dtype = _of_cache(cache, q)
     if D != cache.head_dim or dev != cache.device:
         raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
     if table.dim() != 3 or table.shape[1] != 2 or table.dtype != torch.float32 or table.device != dev or \
@@ -473,12 +554,47 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
     new = _vec(num_new, B, torch.int32, dev, "num_new")
     _status(row_status, B, dev)
     xs, os, ks, vs = x.stride(), o.stride(), k.stride(), v.stride()
-    _check(_library().spec_verify_rotate_append(_ROTATE.pack(
+    args = _ROTATE.pack(
         _ROTATE.size, x.data_ptr(), o.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPE[dtype], B, N, Hq, cache.kv_heads, D,
         xs[0], xs[1], xs[2], os[0], os[1], os[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], table.data_ptr(), tlen,
         2 * half, 1 if interleaved else 0, *pages, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(),
-        _p(new), _p(row_status)), _raw_stream(dev.index)))
+        _p(new), _p(row_status))
+    if scales is None:
+        _check(_library().spec_verify_rotate_append(args, _raw_stream(dev.index)))
+    else:
+        _check(_library().spec_verify_rotate_append_ex(args, _ROTATE_OPTIONS.pack(_ROTATE_OPTIONS.size, *scales),
+                                                       _raw_stream(dev.index)))
     return o
+
+
+def read_cache(cache: PagedCache8, page_table: torch.Tensor, first, N: int, count: Optional[torch.Tensor] = None, *,
+               dtype: torch.dtype = torch.bfloat16, row_status: Optional[torch.Tensor] = None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Keys and values that an 8-bit cache holds: k, v [B, N, kv_heads, dim] of positions first[b] .. first[b] + N - 1
+    (int32 [B]; count [B] of the N are wanted, default all; the others are zeros), code times scale rounded to dtype."""
+    if not isinstance(cache, PagedCache8):
+        raise TypeError("read_cache takes a PagedCache8")
+    if not cache.k.is_cuda:
+        raise ValueError("the cache must be on a CUDA device")
+    dev = cache.device
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(dev, stream, read_cache, (cache, page_table, first, N, count), dict(dtype=dtype,
+                                                                                              row_status=row_status))
+    pages, scales = _pages8(cache)
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, pages a sequence]")
+    B, H, D = page_table.shape[0], cache.kv_heads, cache.head_dim
+    pt = _page_table(page_table, B, dev)
+    lens = _vec(first, B, torch.int32, dev, "first")
+    new = _vec(count, B, torch.int32, dev, "count")
+    _status(row_status, B, dev)
+    k, v = (torch.empty((B, N, H, D), dtype=dtype, device=dev) for _ in "kv")
+    _check(_library().spec_verify_read_cache(_READ.pack(
+        _READ.size, k.data_ptr(), v.data_ptr(), _DTYPE[dtype], B, N, H, D, *pages, pt.data_ptr(), pt.stride(0), pt.shape[1],
+        lens.data_ptr(), _p(new), *scales, _p(row_status)), _raw_stream(dev.index)))
+    return k, v
 
 
 def attention_workspace_size(B: int, N: int, q_heads: int, kv_heads: int, dim: int) -> int:
@@ -486,22 +602,26 @@ def attention_workspace_size(B: int, N: int, q_heads: int, kv_heads: int, dim: i
     return int(_library().spec_verify_attention_workspace_size(B, N, q_heads, kv_heads, dim))
 
 
-def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, cache_lens: torch.Tensor,
-                    num_new: Optional[torch.Tensor] = None, *, scale: Optional[float] = None, window: int = 0,
+def paged_attention(q: torch.Tensor, cache: Union[PagedCache, PagedCache8], page_table: torch.Tensor,
+                    cache_lens: torch.Tensor, num_new: Optional[torch.Tensor] = None, *,
+                    scale: Optional[float] = None, window: int = 0, sinks: int = 0,
                     max_context: Optional[int] = None, out: Optional[torch.Tensor] = None,
                     row_status: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                     wait_limit_ns: int = 0, stream=None) -> torch.Tensor:
     """Attention of the new tokens q [B, N, q_heads, dim] (dim 64 or 128) over the cache that holds their keys.
 
     Token i of sequence b sees the positions up to cache_lens[b] + i, with window > 0 only the last ``window``
-    of them.  scale: default 1 / sqrt(dim).  max_context: the host's upper bound of cache_lens + num_new
+    of them and the first ``sinks`` positions (pages between the two are not touched: their table entries may be
+    anything).  Over a ``PagedCache8`` q is bfloat16 or float16 and the products are formed in float16 with 32-bit sums.
+    scale: default 1 / sqrt(dim).  max_context: the host's upper bound of cache_lens + num_new
     (default: the page table's width); it only sizes the launch.  Rows past num_new are zeros.
     workspace: uint8 of attention_workspace_size() bytes; calls on one must not overlap on the GPU (default: one kept
     for each stream, or the graph's own memory while a graph is captured).  Threads may share a stream.
     """
     if stream is None and workspace is None:
+        scales = (cache.k_scales, cache.v_scales) if isinstance(cache, PagedCache8) else (None, None)
         res = _short.attention(q, cache.k, cache.v, page_table, cache_lens, num_new, scale, window, max_context, out,
-                               row_status, wait_limit_ns)
+                               row_status, wait_limit_ns, sinks, *scales)
         if res is not None:
             return res
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 4:
@@ -509,16 +629,18 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     dev, shape = q.device, q.shape
     if stream is not None or _current_device() != dev.index:
         return _elsewhere(dev, stream, paged_attention, (q, cache, page_table, cache_lens, num_new), dict(
-            scale=scale, window=window, max_context=max_context, out=out, row_status=row_status, workspace=workspace,
-            wait_limit_ns=wait_limit_ns))
+            scale=scale, window=window, sinks=sinks, max_context=max_context, out=out, row_status=row_status,
+            workspace=workspace, wait_limit_ns=wait_limit_ns))
     B, N, Hq, D = shape
-    pages, dtype, Hkv = _pages(cache), cache.dtype, cache.kv_heads
+    (pages, scales, dtype), Hkv = _of_cache(cache, q), cache.kv_heads
     if D != cache.head_dim or dev != cache.device:
         raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
     if Hq % Hkv:
         raise ValueError(f"{Hq} query heads cannot share {Hkv} cache heads evenly")
     if window < 0:
         raise ValueError("window must be 0 (none) or positive")
+    if sinks < 0:
+        raise ValueError("sinks must be 0 (none) or positive")
     x = _rows(q, "q", shape, dtype, dev)
     o = torch.empty(shape, dtype=dtype, device=dev) if out is None else _out_rows(out, shape, dtype, dev)
     pt = _page_table(page_table, B, dev)
@@ -530,10 +652,63 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     with _attend_lock:
         if workspace is None:
             workspace = _workspace(lib.spec_verify_attention_workspace_size(B, N, Hq, Hkv, D), dev, raw)
-        status = lib.spec_verify_attention(_ATTENTION.pack(
+        args = _ATTENTION.pack(
             _ATTENTION.size, x.data_ptr(), o.data_ptr(), _DTYPE[dtype], B, N, Hq, Hkv, D, xs[0], xs[1], xs[2],
             os[0], os[1], os[2], 1.0 / math.sqrt(D) if scale is None else float(scale), window, max_context or 0,
             *pages, pt.data_ptr(), pt.stride(0), pt.shape[1], lens.data_ptr(), _p(new), workspace.data_ptr(),
-            workspace.numel(), _p(row_status), wait_limit_ns), raw)
+            workspace.numel(), _p(row_status), wait_limit_ns)
+        if scales is None and not sinks:
+            status = lib.spec_verify_attention(args, raw)
+        else:
+            status = lib.spec_verify_attention_ex(args, _ATTENTION_OPTIONS.pack(
+                _ATTENTION_OPTIONS.size, sinks, *(scales or _NO_SCALES)), raw)
     _check(status)
     return o
+
+
+# ---------------------------------------------------------------------------
+# drawing tokens
+# ---------------------------------------------------------------------------
+def sample(logits: torch.Tensor, uniforms: torch.Tensor, temperature=None, top_k=None, top_p=None, min_p=None, *,
+           row_status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """A token of every row of logits [B, N, V] (float32 or bfloat16, CUDA), from given random numbers.
+
+    uniforms: float32 [B, N], each in [0, 1).  temperature (0: greedy), top_k (0: none), top_p, min_p: per-sequence
+    tensors, sequences or scalars.  Kept are the top_k largest (of equal logits the lower id first), of these the
+    shortest run of the likeliest with a mass of at least top_p of theirs, of these those at least min_p times as likely
+    as the likeliest; the token is the first in the order of ids up to which the kept mass exceeds uniform times all of
+    it.  This is the q that spec_verify forms of the logits with the same temperature, top_k and top_p.
+    Returns tokens int32 [B, N] and the probability that each had, float32 [B, N].  Rows with a bad parameter or random
+    number, a NaN or +inf logit or no finite logit get -1 and NaN (and their bits in row_status).
+    """
+    if stream is None:
+        res = _short.sample(logits, uniforms, temperature, top_k, top_p, min_p, row_status)
+        if res is not None:
+            return res
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 3:
+        raise ValueError("logits must be a CUDA tensor [B, N, V]")
+    dev = logits.device
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(dev, stream, sample, (logits, uniforms, temperature, top_k, top_p, min_p),
+                          dict(row_status=row_status))
+    code = _DTYPE.get(logits.dtype)
+    if code not in (0, 1):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    B, N, V = logits.shape
+    x = logits if logits.stride(2) == 1 or V == 1 else logits.contiguous()
+    if not isinstance(uniforms, torch.Tensor) or uniforms.dtype != torch.float32 or uniforms.device != dev or \
+            tuple(uniforms.shape) != (B, N):
+        raise ValueError(f"uniforms must be a float32 CUDA tensor [{B}, {N}]")
+    if uniforms.stride(1) != 1 and N > 1:
+        uniforms = uniforms.contiguous()
+    t = _vec(temperature, B, torch.float32, dev, "temperature")
+    k = _vec(top_k, B, torch.int32, dev, "top_k")
+    p = _vec(top_p, B, torch.float32, dev, "top_p")
+    m = _vec(min_p, B, torch.float32, dev, "min_p")
+    _status(row_status, B, dev)
+    tokens = torch.empty((B, N), dtype=torch.int32, device=dev)
+    probs = torch.empty((B, N), dtype=torch.float32, device=dev)
+    _check(_library().spec_verify_sample(_SAMPLE.pack(
+        _SAMPLE.size, x.data_ptr(), code, B, N, V, x.stride(0), x.stride(1), uniforms.data_ptr(), uniforms.stride(0), _p(t),
+        _p(k), _p(p), _p(m), tokens.data_ptr(), probs.data_ptr(), _p(row_status)), _raw_stream(dev.index)))
+    return tokens, probs
