@@ -4,21 +4,28 @@
 // A token is where a sum of weights passes u times their total, so with V tokens there are V
 // borders, some 1e-5 apart or less, and which side of one a draw falls on must not depend on
 // how the sum was formed.  Weights exp((z - m) / T) are therefore formed as pairs of 32-bit
-// numbers (to about 2^-40 of themselves; the 64-bit units of this GPU are too few), turned
+// numbers (to 2^-34 of themselves; the 64-bit units of this GPU are too few), turned
 // into whole numbers of 2^-44, and added as such: sums are exact and have no order.
 //
 // A cluster of CTAs has a row, each a slice of it in shared memory.  What is kept is always a
 // run of the order (logit falling, id rising), so it is given by its last member: a cut
 // (value, id).
-//   top-k up to 128 a CTA, or few tokens  every warp's j-th largest lane maximum is a floor
-//       that at least k tokens reach; those that do (a few times k) are listed, and one CTA
-//       sorts them, cuts them by k, mass and min-p and draws.
-//   otherwise  the cut is found by narrowing: a pass counts or weighs the tokens at and above
-//       seven pivots of the interval that holds it, in 3 bits a pass, until the interval has few
-//       tokens (listed and sorted as above) or one value (whose tokens are counted by id).
-//       Then a pass adds up what is kept, warp by warp in the order of ids, and the warp in
-//       whose part the sum passes u times the total goes through it again.
-// A pass is bound by the instructions of the weights, some 45 an element.
+//   small top-k, few tokens, or min-p alone  the k-th largest of the warps' few largest lane
+//       maxima is a floor that at least k tokens reach; those that do (some 1.2 k) are listed by
+//       one CTA, which cuts them by k, mass and min-p and draws.  In a list of up to 512 each
+//       token adds up those before it, which needs no order; a longer one is sorted.
+//   larger top-k  the cut is found by narrowing: a pass counts the tokens at and above seven
+//       pivots of the interval that holds it, until the interval has few tokens (listed as
+//       above) or one value (whose tokens are counted by id).
+//   top-p  a histogram of rough masses over the distance from the largest, and one inside the
+//       interval that it leaves, then one pass of exact masses, above the interval, in it and in
+//       all, and a list of what is in it.  (If the interval was wrong, or has too many: narrowing
+//       by exact masses.)
+//   then a pass adds up what is kept, warp by warp in the order of ids, and the warp in whose
+//       part the sum passes u times the total goes through it again.
+// A pass is bound by the instructions of the weights, some 35 an element.  Nothing is done in
+// 64-bit floating point: a warp's instruction of it takes 16 cycles, and a logarithm by all
+// threads took 12 us.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -38,7 +45,8 @@ constexpr int kPer = kList / kSThreads;
 constexpr int kPivots = 7;
 constexpr int kFix = 44;          // weights are whole numbers of 2^-44: sums of 2^18 of them stay below 2^62
 constexpr int kHalfFix = kFix / 2;
-constexpr int kFloorRank = 8;     // lanes of a warp that the floor may rank
+constexpr int kTops = 8;          // lanes of a warp that the floor may rank
+constexpr int kShort = kSThreads;  // tokens of a list that needs no order
 
 struct Cut {  // kept: x > v, and x == v up to id
     float v;
@@ -47,19 +55,52 @@ struct Cut {  // kept: x > v, and x == v up to id
 struct Slot {  // what a CTA tells the others
     long long mass[kPivots + 1];
     int count[kPivots + 1];
+    uint32_t bins[kSThreads];
     long long warp[kSWarps];
-    float top, floor;
-    int bad, n, id;
+    alignas(16) int tops[kSWarps][kTops];  // of each warp its largest lane maxima (ord), falling
+    int n, id;
     Cut cut;
 };
+constexpr int kTable = 1024;  // entries of 2^(i / 1024), in two parts
+struct alignas(16) SampleTable {
+    float v[2 * kTable];
+};
+constexpr SampleTable make_table() {
+    SampleTable t{};
+    for (int i = 0; i < kTable; ++i) {
+        const double x = 0.69314718055994530942 * i / kTable;
+        double y = 1.0, term = 1.0;
+        for (int k = 1; k < 20; ++k) y += term = term * x / k;
+        t.v[2 * i] = (float)y;
+        t.v[2 * i + 1] = (float)(y - (double)t.v[2 * i]);
+    }
+    return t;
+}
+__device__ const SampleTable g_table = make_table();
+constexpr int kBins = kSThreads, kCopies = 4;  // of a histogram, and copies of it
+struct Pair16 {
+    uint64_t key;
+    unsigned long long mass;
+};
 struct SampleSmem {
-    uint64_t list[kList];
-    float2 tab[64];  // 2^(i / 64) in two parts
+    union {
+        uint64_t list[kList];
+        struct {
+            uint64_t list_start[kShort];
+            Pair16 pairs[kShort];
+        };
+        uint32_t bins[kBins][kCopies];
+    };
+    SampleTable tab;
     Slot slot[2];
+    long long sum_mass[kPivots + 1];  // of the cluster
+    int sum_count[kPivots + 1];
     long long wmass[kSWarps][kPivots + 1];
     int wcount[kSWarps][kPivots + 1];
+    long long keep[kSWarps];  // of each warp the mass above the interval of top-p
+    float wbin[kSWarps], edge;
     long long total, before;
-    int n_list, place, r;
+    int n_list, place, edges[2];
 };
 
 // values in their order as whole numbers (both zeros are 0)
@@ -98,31 +139,19 @@ __device__ __forceinline__ void weigh(const Weight& w, float x, int& hi, int& lo
         hi = lo = kMagicBits;
         return;
     }
-    // 2^p = 2^(j / 64) 2^f: f in [-1/128, 1/128]
-    const float js = __fadd_rn(p, 196608.0f);  // 1.5 * 2^17: steps of 1/64
-    const int j = __float_as_int(js) - 0x48400000;
-    const float f = __fsub_rn(p, __fsub_rn(js, 196608.0f));
-    // (f + q) ln 2 = t + s
-    constexpr float kLn2 = (float)0.69314718055994530942, kLn2Lo = (float)(0.69314718055994530942 - (double)kLn2);
-    const float t = __fmul_rn(f, kLn2);
-    float s = __fmaf_rn(f, kLn2, -t);
-    s = __fmaf_rn(f, kLn2Lo, s);
-    s = __fmaf_rn(q, kLn2, s);
-    // exp(t + s) - 1 - t: the series to t^5 (t is below 2^-7.5)
-    float g = __fmaf_rn(t, 1.0f / 120.0f, 1.0f / 24.0f);
-    g = __fmaf_rn(t, g, 1.0f / 6.0f);
-    g = __fmaf_rn(t, g, 0.5f);
-    g = __fmul_rn(__fmul_rn(t, t), g);
-    g = __fadd_rn(g, __fmaf_rn(t, s, s));
-    const float2 b = w.tab[j & 63];
-    // b (1 + t + g): the parts below 1 first, then their sum and what it leaves
-    const float a = __fmul_rn(b.x, t), ae = __fmaf_rn(b.x, t, -a), bg = __fmul_rn(b.x, g);
-    const float k = __fadd_rn(a, bg), ke = __fsub_rn(bg, __fsub_rn(k, a));
-    const float h = __fadd_rn(b.x, k);
-    float l = __fsub_rn(k, __fsub_rn(h, b.x));
-    l = __fadd_rn(l, __fadd_rn(ae, ke));
-    l = __fmaf_rn(b.y, __fadd_rn(1.0f, t), l);
-    const float scale = __int_as_float(((j >> 6) + kHalfFix + 127) << 23);
+    // 2^p = 2^(j / 1024) 2^f: f in [-2^-11, 2^-11]
+    const float js = __fadd_rn(p, 12288.0f);  // 1.5 * 2^13: steps of 1/1024
+    const int j = __float_as_int(js) - 0x46400000;
+    const float f = __fsub_rn(p, __fsub_rn(js, 12288.0f));
+    // 2^(f + q) - 1 by its series to f^3: below 2^-11, so off by 2^-35
+    constexpr float kLn2 = 0.69314718f, kLn2Sq = 0.24022651f, kLn2Cb = 0.05550411f;  // ln 2, its square / 2, cube / 6
+    float g = __fmaf_rn(f, kLn2Cb, kLn2Sq);
+    g = __fmaf_rn(f, g, kLn2);
+    g = __fmaf_rn(q, kLn2, __fmul_rn(f, g));
+    const float2 b = w.tab[j & (kTable - 1)];
+    const float k = __fmaf_rn(b.x, g, b.y);
+    const float h = __fadd_rn(b.x, k), l = __fsub_rn(k, __fsub_rn(h, b.x));
+    const float scale = __int_as_float(((j >> 10) + kHalfFix + 127) << 23);
     // the whole number nearest to the upper part, then what is missing, 2^22 times as large
     const float u = __fmul_rn(h, scale), r = __fadd_rn(u, kMagic);
     hi = __float_as_int(r);
@@ -136,6 +165,22 @@ __device__ __forceinline__ long long weight(const Weight& w, float x) {
     int hi, lo;
     weigh(w, x, hi, lo);
     return fixed(hi, lo);
+}
+
+// floor(x * 2^bits) of a number in [0, 1], and the same rounded up
+__device__ __forceinline__ unsigned long long scaled(float x, int bits, bool up = false) {
+    const int b = __float_as_int(x), e = max(b >> 23, 1) - 150 + bits;
+    const unsigned long long f = (b & 0x7FFFFF) | (b >> 23 ? 0x800000 : 0);
+    if (e >= 0) return f << e;
+    return e <= -25 ? (up && f ? 1 : 0) : (f + (up ? (1ull << -e) - 1 : 0)) >> -e;
+}
+// a / b rounded to nearest (to within 2^-40 of a step's half)
+__device__ __forceinline__ float ratio(long long a, long long b) {
+    const float ah = __ll2float_rn(a), bh = __ll2float_rn(b);
+    const float al = __ll2float_rn(a - (long long)ah), bl = __ll2float_rn(b - (long long)bh);
+    const float q = __fdiv_rn(ah, bh);
+    const float r = __fmaf_rn(-q, bl, __fadd_rn(__fmaf_rn(-q, bh, ah), al));
+    return __fadd_rn(q, __fdiv_rn(r, bh));
 }
 
 template <typename T>
@@ -270,29 +315,111 @@ struct SampleRow {
         __syncthreads();
         if (t == 0) mine().n = s.n_list;
         exchange();
-        int n = 0, counts[kSCluster];
-        for (int r = 0; r < C; ++r) n += counts[r] = of(r)->n;
+        int n = 0, at = 0;
+#pragma unroll
+        for (int r = 0; r < kSCluster; ++r) {  // (unrolled, so that the others' memory is waited for once)
+            const int c = r < C ? of(r)->n : 0;
+            if (r < rank) at += c;
+            n += c;
+        }
         if (C > 1) {
-            if (n <= kList && rank == 0) {
-                int at = counts[0];
-                for (int r = 1; r < C; ++r) {
-                    const uint64_t* src = cl.map_shared_rank(s.list, r);
-                    for (int i = t; i < counts[r]; i += kSThreads) s.list[at + i] = src[i];
-                    at += counts[r];
-                }
+            if (n <= kList && rank > 0) {
+                uint64_t* dst = cl.map_shared_rank(s.list, 0) + at;
+                for (int i = t; i < s.n_list; i += kSThreads) dst[i] = s.list[i];
             }
-            cl.sync();  // the others' lists may be written again
+            cl.sync();
         } else {
             __syncthreads();
         }
         return n;
     }
 
-    // ceil(P S) for the comparison of whole numbers with it
-    static __device__ long long mass_target(float P, long long S) { return (long long)ceil((double)P * (double)S); }
+    // ceil(P S) for the comparison of whole numbers with it, floor(u S)
+    static __device__ long long mass_target(float P, long long S) {
+        const unsigned long long p = scaled(P, 64);
+        return (long long)(__umul64hi(p, (unsigned long long)S) + (p * (unsigned long long)S != 0));
+    }
+    static __device__ long long share_of(float u, long long S) {
+        return (long long)__umul64hi(scaled(u, 64), (unsigned long long)S);
+    }
+    __device__ long long sum_of(long long own) {  // over the CTA
+        own = warp_sum(own);
+        __syncthreads();
+        if (lane == 0) s.wmass[warp][0] = own;
+        __syncthreads();
+        long long n = 0;
+#pragma unroll
+        for (int i = 0; i < kSWarps; ++i) n += s.wmass[i][0];
+        return n;
+    }
 
-    // Draws from the list's n entries, sorted: top-k, top-p and min-p (x >= least), then by id.  By one CTA.
-    __device__ void draw_from_list(int n, int K, float P, float least, float u, int32_t* token, float* prob) {
+    // A short list (n <= kShort), token by token: G neighbouring threads have entry e.  Of the
+    // entries with a greater key their number (low 10 bits) and mass (above).
+    struct Entry {
+        int e, G;
+        bool first;  // of the G threads
+        uint64_t key;
+        long long w;
+    };
+    __device__ Entry entry(int n) {
+        int size = 16;
+        while (size < n) size <<= 1;
+        Entry x;
+        x.G = kSThreads / size;
+        x.e = t / x.G;
+        x.first = t % x.G == 0;
+        x.key = 0;
+        x.w = 0;
+        return x;
+    }
+    __device__ Entry listed(int n) {
+        Entry x = entry(n);
+        if (x.e < n) {
+            x.key = s.list[x.e];
+            x.w = weight(w, key_value(x.key));
+            if (x.first) s.pairs[x.e] = Pair16{x.key, (unsigned long long)x.w << 10 | 1};
+        }
+        __syncthreads();
+        return x;
+    }
+    __device__ unsigned long long above(const Entry& x, int n) {
+        unsigned long long sum = 0;
+        if (x.e < n)
+#pragma unroll 4
+            for (int f = t % x.G; f < n; f += x.G) {
+                const Pair16 p = s.pairs[f];
+                if (p.key > x.key) sum += p.mass;
+            }
+        for (int o = 1; o < x.G; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        return sum;
+    }
+
+    // Draws from the list's n entries: top-k, top-p and min-p (a weight of `least`), then by id.  By one CTA.
+    __device__ void draw_from_list(int n, int K, float P, long long least, float u, int32_t* token, float* prob) {
+        if (n <= kShort) {
+            const Entry x = listed(n);
+            const unsigned long long a = above(x, n);
+            const int place = (int)(a & 1023);
+            const bool in = x.e < n && place < K;
+            const long long S = sum_of(in && x.first ? x.w : 0);
+            const long long target = P < 1.0f ? mass_target(P, S) : 0x7FFFFFFFFFFFFFFFll;
+            const bool keep = in && (long long)(a >> 10) < target && x.w >= least;
+            // what is kept comes first in the order: again by ids (the low half of a key falls with them)
+            if (keep && x.first) s.pairs[place] = Pair16{x.key & 0xFFFFFFFFu, (unsigned long long)x.w};
+            const int kept_n = count_of(keep && x.first);
+            Entry y = entry(kept_n);
+            if (y.e < kept_n) {
+                y.key = s.pairs[y.e].key;
+                y.w = (long long)s.pairs[y.e].mass;
+            }
+            const long long kept_mass = sum_of(y.first ? y.w : 0);
+            const long long before = (long long)above(y, kept_n), v = share_of(u, kept_mass);
+            if (y.e < kept_n && y.first && before <= v && before + y.w > v) {
+                *token = key_id(y.key);
+                if (prob) *prob = ratio(y.w, kept_mass);
+            }
+            return;
+        }
         sort(n);
         if (K < n) n = K;
         long long val[kPer], before[kPer];
@@ -307,7 +434,7 @@ struct SampleRow {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = t * kPer + i;
-            keep += e < n && before[i] < target && key_value(s.list[e]) >= least;
+            keep += e < n && before[i] < target && val[i] >= least;
         }
         n = count_of(keep);
         // in the order of ids
@@ -327,18 +454,53 @@ struct SampleRow {
             val[i] = e < n ? weight(w, key_value(~s.list[e] << 32)) : 0;
         }
         const long long kept_mass = scan(val, before);
-        const long long v = (long long)floor((double)u * (double)kept_mass);
+        const long long v = share_of(u, kept_mass);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             if (before[i] <= v && before[i] + val[i] > v) {
                 *token = (int)(~s.list[t * kPer + i] >> 32);
-                if (prob) *prob = (float)((double)val[i] / (double)kept_mass);
+                if (prob) *prob = ratio(val[i], kept_mass);
             }
+    }
+
+    // The cut behind the first `number` of the list's n entries in their order, or (number 0) behind those that
+    // have less than `target` mass before them, `done` of it not in the list; to all.
+    __device__ Cut cut_in_list(int n, int number, long long done, long long target) {
+        if (rank == 0) {
+            if (n <= kShort) {
+                const Entry x = listed(n);
+                const unsigned long long a = above(x, n);
+                if (number == 0)
+                    number = count_of(x.e < n && x.first && done + (long long)(a >> 10) < target);
+                if (x.e < n && x.first && (int)(a & 1023) == max(number, 1) - 1)
+                    mine().cut = Cut{key_value(x.key), key_id(x.key)};
+            } else {
+                sort(n);
+                if (number == 0) {
+                    long long val[kPer], before[kPer];
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const int e = t * kPer + i;
+                        val[i] = e < n ? weight(w, key_value(s.list[e])) : 0;
+                    }
+                    scan(val, before);
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) number += t * kPer + i < n && done + before[i] < target;
+                    number = count_of(number);
+                }
+                if (t == 0) {
+                    const uint64_t k = s.list[max(number, 1) - 1];
+                    mine().cut = Cut{key_value(k), key_id(k)};
+                }
+            }
+        }
+        exchange();
+        return of(0)->cut;
     }
 
     // One pass of narrowing: of the members of `cut` in [lo, hi), mass and number at and above each
     // pivot; entry kPivots: of all of them.  Summed over the cluster.
-    template <bool MASS>
+    template <bool MASS, int USED = kPivots>
     __device__ void pass(Cut cut, float lo, float hi, const float (&p)[kPivots], long long (&mass)[kPivots + 1],
                          int (&count)[kPivots + 1]) {
         int h[kPivots + 1], l[kPivots + 1], n[kPivots + 1];
@@ -351,7 +513,7 @@ struct SampleRow {
                 wh -= kMagicBits, wl -= kMagicBits;
 #pragma unroll
                 for (int j = 0; j <= kPivots; ++j)
-                    if (j == kPivots || x >= p[j]) {
+                    if (j == kPivots || (j < USED && x >= p[j])) {
                         if (MASS) h[j] += wh, l[j] += wl;
                         ++n[j];
                     }
@@ -359,6 +521,7 @@ struct SampleRow {
         });
 #pragma unroll
         for (int j = 0; j <= kPivots; ++j) {
+            if (j >= USED && j < kPivots) continue;
             const int c = __reduce_add_sync(0xFFFFFFFFu, n[j]);
             if (lane == 0) s.wcount[warp][j] = c;
             if (MASS) {
@@ -378,25 +541,31 @@ struct SampleRow {
             mine().mass[t] = m;
         }
         exchange();
+        if (t <= kPivots) {
+            int c[kSCluster];
+            long long m[kSCluster];
 #pragma unroll
-        for (int j = 0; j <= kPivots; ++j) mass[j] = 0, count[j] = 0;
-        for (int r = 0; r < C; ++r) {
-            const Slot* q = of(r);
-#pragma unroll
-            for (int j = 0; j <= kPivots; ++j) {
-                count[j] += q->count[j];
-                if (MASS) mass[j] += q->mass[j];
+            for (int r = 0; r < kSCluster; ++r) {
+                c[r] = r < C ? of(r)->count[t] : 0;
+                m[r] = MASS && r < C ? of(r)->mass[t] : 0;
             }
+#pragma unroll
+            for (int r = 1; r < kSCluster; ++r) c[0] += c[r], m[0] += m[r];
+            s.sum_count[t] = c[0], s.sum_mass[t] = m[0];
         }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j <= kPivots; ++j) mass[j] = s.sum_mass[j], count[j] = s.sum_count[j];
     }
 
     // The warp in whose part the running sum of f over ids first passes `over` (or share * the total of
     // all, where over < 0): its place in the cluster, the sum before it and the total, in s; nobody: -1.
+    // ready: of each warp's sum a part that is known.
     template <typename F>
-    __device__ void locate(F f, long long over, double share) {
+    __device__ void locate(F f, long long over, float share, long long ready = 0) {
         long long own = 0;
         each([&](float x, int id) { own += f(x, id); });
-        own = warp_sum(own);
+        own = warp_sum(own) + ready;
         if (lane == 0) mine().warp[warp] = own;
         exchange();
         if (warp == 0) {
@@ -415,7 +584,7 @@ struct SampleRow {
                 if (lane >= o) x += y;
             }
             const long long total = __shfl_sync(0xFFFFFFFFu, x, 31);
-            const long long v = over >= 0 ? over : (long long)floor(share * (double)total);
+            const long long v = over >= 0 ? over : share_of(share, total);
             if (lane == 0) s.place = -1, s.total = total;
             __syncwarp();
             long long before = x - sum;
@@ -465,6 +634,10 @@ struct SampleRow {
         }
     }
 
+    __device__ float first_pivot(int j, float temp) {  // by distance from the largest
+        constexpr float kFirst[kPivots] = {16.0f, 12.0f, 9.0f, 7.0f, 5.0f, 3.0f, 1.5f};
+        return w.m - kFirst[j] * temp;
+    }
     // The cut of the K largest members (MASS false), or of the shortest run with P of the members' mass.
     template <bool MASS>
     __device__ Cut narrow(Cut cut, int K, float P, float temp) {
@@ -475,11 +648,10 @@ struct SampleRow {
             float p[kPivots];
 #pragma unroll
             for (int j = 0; j < kPivots; ++j) {
-                constexpr float kFirst[kPivots] = {16.0f, 12.0f, 9.0f, 7.0f, 5.0f, 3.0f, 1.5f};
                 const float x = (float)(j + 1) / (kPivots + 1);
                 // by distance from the largest; then by value and by the order of floats in turn: one converges
                 // quickly on smooth rows, the other in 11 passes on any
-                p[j] = round == 0 ? w.m - kFirst[j] * temp
+                p[j] = round == 0 ? first_pivot(j, temp)
                        : round & 1 ? lo * (1.0f - x) + hi * x
                                    : of_ord((int)(ord(lo) + ((long long)ord(hi) - ord(lo)) * (j + 1) / (kPivots + 1)));
                 p[j] = fminf(fmaxf(p[j], lo), hi);
@@ -514,36 +686,13 @@ struct SampleRow {
                 Cut res;
                 if (in <= kList) {
                     const int n = gather([&](float x, int id) { return x >= lo && x < hi && kept(cut, x, id); });
-                    if (rank == 0) {
-                        sort(n);
-                        int keep = 0;
-                        if (MASS) {
-                            long long val[kPer], before[kPer];
-#pragma unroll
-                            for (int i = 0; i < kPer; ++i) {
-                                const int e = t * kPer + i;
-                                val[i] = e < n ? weight(w, key_value(s.list[e])) : 0;
-                            }
-                            scan(val, before);
-#pragma unroll
-                            for (int i = 0; i < kPer; ++i) keep += t * kPer + i < n && above + before[i] < target;
-                            keep = count_of(keep);
-                        } else {
-                            keep = (int)(target - above);
-                        }
-                        if (t == 0) {
-                            const uint64_t k = s.list[max(keep, 1) - 1];
-                            mine().cut = Cut{key_value(k), key_id(k)};
-                        }
-                    }
-                    exchange();
-                    res = of(0)->cut;
+                    res = cut_in_list(n, MASS ? 0 : (int)(target - above), above, target);
                 } else {
                     // one value: its first `keep` by id
                     const long long each_one = MASS ? weight(w, lo) : 1;
                     const long long keep = (target - above + each_one - 1) / max(each_one, 1ll);
                     auto one = [&](float x, int id) -> long long { return x == lo && kept(cut, x, id); };
-                    locate(one, keep - 1, 0.0);
+                    locate(one, keep - 1, 0.0f);
                     const int at = s.place;
                     search(one, [&](float, int id) { mine().id = id; });
                     exchange();
@@ -552,6 +701,99 @@ struct SampleRow {
                 return res;
             }
         }
+    }
+
+    // A histogram of rough masses of the members, over p = log2 of their weights: bin i has those with
+    // from - (i + 1) * width < p <= from - i * width, the last all below as well (`open`); those above
+    // `from` are in none.  Masses count in 2^-13 of the bin's upper end (rounded to 2^-14 of it: 2^18 of them fit).
+    // Bin t's mass comes back to thread t, the same in all CTAs.
+    __device__ float histogram(Cut cut, float from, float width, bool open) {
+        for (int i = t; i < kBins * kCopies; i += kSThreads) (&s.bins[0][0])[i] = 0;
+        __syncthreads();
+        const float per = 1.0f / width;
+        each([&](float x, int id) {
+            const float p = (x - w.m) * w.c_hi;
+            float i = (from - p) * per;
+            if (i >= 0.0f && (open || i < (float)kBins) && kept(cut, x, id)) {
+                i = floorf(fminf(i, kBins - 1.0f));
+                float y;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(p - (from - i * width)));
+                atomicAdd(&s.bins[(int)i][lane & (kCopies - 1)], (uint32_t)__float2int_rn(y * 8192.0f));
+            }
+        });
+        __syncthreads();
+        const uint4 four = *reinterpret_cast<const uint4*>(s.bins[t]);
+        mine().bins[t] = four.x + four.y + four.z + four.w;
+        exchange();
+        float sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kSCluster; ++r) sum += r < C ? (float)of(r)->bins[t] : 0.0f;
+        float y;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(from - t * width));
+        return sum * y * (1.0f / 8192.0f);
+    }
+    // The first bin (of thread t: `mass`) up to which P of all is reached perhaps, and that up to which it is for
+    // certain (kBins: none); the mass before the former, and of all bins.  `before`: what lies before them;
+    // all: the whole mass (0: that of the bins).
+    __device__ void crossing(float mass, float before, float P, float all, int& first, int& last, float& lead, float& total) {
+        float x = mass;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) s.wbin[warp] = x;
+        if (t < 2) s.edges[t] = kBins;
+        if (t == 0) s.edge = 0.0f;
+        __syncthreads();
+        float base = before;
+        total = 0.0f;
+        for (int i = 0; i < kSWarps; ++i) {
+            if (i < warp) base += s.wbin[i];
+            total += s.wbin[i];
+        }
+        const float S = all > 0.0f ? all : total, need = P * S, room = S * (1.0f / 8192);
+        const float upto = base + x;
+        if (upto >= need - room) atomicMin(&s.edges[0], t);
+        if (upto > need + room) atomicMin(&s.edges[1], t);
+        __syncthreads();
+        first = s.edges[0], last = s.edges[1];
+        if (t == first) s.edge = upto - mass;
+        __syncthreads();
+        lead = s.edge;
+    }
+
+    // The cut of the shortest run with P of the members' mass.  inner: where the interval ends, above which all
+    // is kept (its mass by warps is in s.keep); infinite: they are not known.
+    __device__ Cut nucleus(Cut cut, float P, float temp, float& inner) {
+        // the interval as p = log2 of weights, from `top` down to `bottom`
+        int first, last;
+        float lead, all, rest;
+        constexpr float kWidth = 1.0f / 16;
+        crossing(histogram(cut, 0.0f, kWidth, true), 0.0f, P, 0.0f, first, last, lead, all);
+        float top = -kWidth * first, bottom = last >= kBins - 1 ? -INFINITY : -kWidth * (last + 1);
+        if (first < kBins && last < kBins - 1) {
+            const float width = (top - bottom) / kBins;
+            crossing(histogram(cut, top, width, false), lead, P, all, first, last, lead, rest);
+            if (last < kBins) bottom = top - width * (last + 1);
+            if (first < kBins) top = top - width * first;
+        }
+        // as values, a little wider
+        const float slack = 1e-6f * fabsf(w.m);
+        const float hi = top == 0.0f ? of_ord(ord(w.m) + 1) : w.m + top / w.c_hi * (1.0f - 1e-6f) + slack;
+        const float lo = bottom == -INFINITY ? -3.402823466e38f : w.m + bottom / w.c_hi * (1.0f + 1e-6f) - slack;
+        const float p[kPivots] = {lo, hi, hi, hi, hi, hi, hi};
+        long long mass[kPivots + 1];
+        int count[kPivots + 1];
+        pass<true, 2>(cut, -3.402823466e38f, INFINITY, p, mass, count);
+        const long long target = mass_target(P, mass[kPivots]);
+        inner = INFINITY;
+        if (mass[1] >= target || mass[0] < target || count[0] - count[1] > kList) return narrow<true>(cut, 0, P, temp);
+        if (lane == 0) s.keep[warp] = s.wmass[warp][1];
+        inner = hi;
+        const int n = gather([&](float x, int id) { return x >= lo && x < hi && kept(cut, x, id); });
+        return cut_in_list(n, 0, mass[1], target);
     }
 };
 
@@ -637,54 +879,50 @@ __global__ void __launch_bounds__(kSThreads, 2)
             for (int y = 0; y < VEC; ++y) top = max_nan(top, x[y]);
         }
     }
-    if (t < 64) {
-        const double d = exp2(t / 64.0);
-        s.tab[t] = make_float2((float)d, (float)(d - (double)(float)d));
-    }
+    for (int k = t; k < kTable / 2; k += kSThreads)
+        reinterpret_cast<float4*>(s.tab.v)[k] = __ldg(reinterpret_cast<const float4*>(g_table.v) + k);
     SampleRow<T> r{a, s, slice, cg::this_cluster(), C, rank, t, lane, warp, v0, v1, first - pad, 0, {}};
 
-    // ---- the largest, and a floor that at least K tokens reach
-    const int j = (K + C * kSWarps - 1) / (C * kSWarps);  // of each warp
-    const bool ranked = K < V && j <= kFloorRank;
+    // ---- the largest of the row and, of each warp, its largest lane maxima: one more than would do
+    const int warps = C * kSWarps, j = min((K + warps - 1) / warps + 1, kTops);
+    const bool ranked = K < V && warps * j >= K;
     const bool poison = __any_sync(0xFFFFFFFFu, !(top < INFINITY));
     int o = ord(top);
-    const float wtop = of_ord(__reduce_max_sync(0xFFFFFFFFu, o));
-    float wfloor = -INFINITY;
-    if (ranked) {
-        int least = 0;
-        for (int k = 0; k < j; ++k) {
-            least = __reduce_max_sync(0xFFFFFFFFu, o);
-            const unsigned who = __ballot_sync(0xFFFFFFFFu, o == least);
-            if (lane == __ffs(who) - 1) o = (int)0x80000000;
-        }
-        wfloor = of_ord(max(least, ord(-INFINITY)));
+    for (int k = 0; k < (ranked ? j : 1); ++k) {
+        const int most = __reduce_max_sync(0xFFFFFFFFu, o);
+        const unsigned who = __ballot_sync(0xFFFFFFFFu, o == most);
+        if (lane == __ffs(who) - 1) o = ord(-INFINITY);
+        if (lane == 0) r.mine().tops[warp][k] = most;
     }
-    if (lane == 0) {
-        s.wcount[warp][0] = poison;
-        s.wcount[warp][1] = __float_as_int(wtop);
-        s.wcount[warp][2] = __float_as_int(wfloor);
-    }
-    __syncthreads();
-    if (t == 0) {
-        int any = 0;
-        float hi = -INFINITY, lo = INFINITY;
-        for (int k = 0; k < kSWarps; ++k) {
-            any |= s.wcount[k][0];
-            hi = fmaxf(hi, __int_as_float(s.wcount[k][1]));
-            lo = fminf(lo, __int_as_float(s.wcount[k][2]));
-        }
-        Slot& q = r.mine();
-        q.bad = any, q.top = hi, q.floor = lo;
-    }
+    if (poison && lane == 0) r.mine().tops[warp][0] = 0x7FFFFFFF;  // (no float's)
     r.exchange();
-    int any = 0;
-    float m = -INFINITY, floor_at = INFINITY;
-    for (int k = 0; k < C; ++k) {
-        const Slot* q = r.of(k);
-        any |= q->bad;
-        m = fmaxf(m, q->top);
-        floor_at = fminf(floor_at, q->floor);
+    constexpr int PER = kSCluster * kSWarps * kTops / kSThreads;
+    int v[PER], most = ord(-INFINITY);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        // the largest of every warp, then their second largest, ... (C is a power of two)
+        const int at = t + k * kSThreads, y = at & (warps - 1), of = at / kSWarps >> (__ffs(C) - 1);
+        v[k] = of < (ranked ? j : 1) ? r.of(y / kSWarps)->tops[y % kSWarps][of] : (int)0x80000000;
     }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) most = max(most, v[k]);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if (lane == 0) s.wcount[warp][0] = most;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSWarps; ++k) most = max(most, s.wcount[k][0]);
+    const bool any = most == 0x7FFFFFFF;
+    const float m = of_ord(most);
+    uint32_t floor_bits = 0;  // the K-th largest of the warps' maxima, to 16 bits
+    if (ranked)
+        for (int bit = 31; bit >= 16; --bit) {
+            const uint32_t x = floor_bits | 1u << bit;
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+                if (k * kSThreads < warps * j) n += __syncthreads_count(((uint32_t)v[k] ^ 0x80000000u) >= x);
+            if (n >= K) floor_bits = x;
+        }
     if (any || m == -INFINITY) {
         refuse(SV_ROW_NONFINITE);
     } else if (Tm == 0.0f) {
@@ -707,34 +945,46 @@ __global__ void __launch_bounds__(kSThreads, 2)
             if (prob) *prob = 1.0f;
         }
     } else {
-        const double c = 1.4426950408889634 / (double)fmaxf(Tm, 1e-30f);
-        r.w = Weight{m, (float)c, (float)(c - (double)(float)c), s.tab};
-        // min-p: the least value that is likely enough
-        float least = -INFINITY;
+        constexpr float kLog2e = (float)1.4426950408889634074, kLog2eLo = (float)(1.4426950408889634074 - (double)kLog2e);
+        const float temp = fmaxf(Tm, 1e-30f), c = __fdiv_rn(kLog2e, temp);
+        r.w = Weight{m, c, __fdiv_rn(__fadd_rn(__fmaf_rn(-c, temp, kLog2e), kLog2eLo), temp), reinterpret_cast<const float2*>(s.tab.v)};
+        // min-p: the least weight, and a value below which no weight is as large
+        const long long least = (long long)scaled(M, kFix, true);
+        float from = -INFINITY;
         if (M > 0.0f) {
-            const double x = (double)m + (double)Tm * log((double)M);
-            least = fminf(__double2float_ru(x), m);
+            const float x = temp * logf(M);
+            from = m + x - 1e-5f * (fabsf(x) + fabsf(m));
         }
         const bool alone = K == V && P >= 1.0f;  // nothing but min-p
         int listed = kList + 1;
         if (ranked || V <= kList || (alone && M > 0.0f)) {
-            const float from = ranked ? floor_at : alone ? least : -INFINITY;
-            listed = r.gather([&](float x, int) { return x >= from && x > -INFINITY; });
-            if (listed <= kList && rank == 0) r.draw_from_list(listed, K, P, least, u, token, prob);
+            const float low = ranked ? of_ord(max((int)(floor_bits ^ 0x80000000u), ord(-INFINITY))) : alone ? from : -INFINITY;
+            listed = r.gather([&](float x, int) { return x >= low && x > -INFINITY; });
+            if (listed <= kList) {
+                // (nobody reads another's shared memory any more)
+                if (rank == 0) r.draw_from_list(listed, K, P, least, u, token, prob);
+                return;
+            }
         }
-        if (listed > kList) {
-            Cut cut{-INFINITY, -1};
-            if (K < V) cut = r.template narrow<false>(cut, K, P, Tm);
-            if (P < 1.0f) cut = r.template narrow<true>(cut, K, P, Tm);
-            if (least > cut.v) cut = Cut{least, 0x7FFFFFFF};
-            auto mass = [&](float x, int id) -> long long { return kept(cut, x, id) ? weight(r.w, x) : 0; };
-            r.locate(mass, -1, (double)u);
-            const long long total = s.total;
-            r.search(mass, [&](float x, int id) {
-                *token = id;
-                if (prob) *prob = (float)((double)weight(r.w, x) / (double)total);
-            });
-        }
+        Cut cut{-INFINITY, -1};
+        if (K < V) cut = r.template narrow<false>(cut, K, P, temp);
+        float inner = INFINITY;
+        if (P < 1.0f) cut = r.nucleus(cut, P, temp, inner);
+        auto mass = [&](float x, int id) -> long long {
+            if (!(x >= from) || !kept(cut, x, id)) return 0;
+            const long long y = weight(r.w, x);
+            return y >= least ? y : 0;
+        };
+        if (inner < INFINITY && weight(r.w, cut.v) >= least)  // min-p takes nothing more: what lies above is known
+            r.locate([&](float x, int id) -> long long { return x < inner && kept(cut, x, id) ? weight(r.w, x) : 0; }, -1, u,
+                     s.keep[warp]);
+        else
+            r.locate(mass, -1, u);
+        const long long total = s.total;
+        r.search(mass, [&](float x, int id) {
+            *token = id;
+            if (prob) *prob = ratio(weight(r.w, x), total);
+        });
     }
     if (C > 1) r.cl.sync();  // nobody leaves while its shared memory may be read
 }
