@@ -95,8 +95,7 @@ bool encode(CUtensorMap* m, const void* base, const AttendArgs& p, int64_t sp, i
 }
 
 // pages of codes as [pages][heads][page_size][dim]
-bool encode8(CUtensorMap* m, const void* base, const AttendArgs& p, int64_t sp, int64_t sh, int64_t ss, int box,
-             bool swizzled) {
+bool encode8(CUtensorMap* m, const void* base, const AttendArgs& p, int64_t sp, int64_t sh, int64_t ss, int box) {
     EncodeFn fn = encoder();
     if (!fn) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)p.a.dim, (cuuint64_t)p.a.cache.page_size, (cuuint64_t)p.a.kv_heads,
@@ -106,19 +105,16 @@ bool encode8(CUtensorMap* m, const void* base, const AttendArgs& p, int64_t sp, 
     const cuuint64_t strides[3] = {(cuuint64_t)ss, (cuuint64_t)sh, (cuuint64_t)sp};
     const cuuint32_t boxes[4] = {(cuuint32_t)p.a.dim, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, boxes, ones,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              !swizzled         ? CU_TENSOR_MAP_SWIZZLE_NONE
-              : p.a.dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, p.a.dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
-bool encode_codes(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, bool swizzled) {
+bool encode_codes(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box) {
     const sv_paged_cache& c = p.a.cache;
-    return encode8(keys, c.k_pages, p, c.k_stride_page, c.k_stride_head, c.k_stride_slot, box, swizzled) &&
-           encode8(values, c.v_pages, p, c.v_stride_page, c.v_stride_head, c.v_stride_slot, box, swizzled);
+    return encode8(keys, c.k_pages, p, c.k_stride_page, c.k_stride_head, c.k_stride_slot, box) &&
+           encode8(values, c.v_pages, p, c.v_stride_page, c.v_stride_head, c.v_stride_slot, box);
 }
 
 bool encode_pages(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, int parts) {

@@ -392,8 +392,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // tensor maps of the pages, a head's rows in parts of 64 elements (128 bytes, swizzled):
 // boxes of `box` rows and `parts` parts
 bool encode_pages(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, int parts);
-// of a cache held in 8 bits: boxes of `box` whole rows of a head, swizzled or as they are
-bool encode_codes(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box, bool swizzled);
+// of a cache held in 8 bits: boxes of `box` whole rows of a head, swizzled
+bool encode_codes(CUtensorMap* keys, CUtensorMap* values, const AttendArgs& p, int box);
 
 // Launch whose start may overlap with the end of the kernel before it on the stream; the
 // kernels wait for that one with grid_dependency_wait() before they read anything.

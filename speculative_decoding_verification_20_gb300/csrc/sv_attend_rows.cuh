@@ -579,7 +579,7 @@ template <typename T, int D, int MT, bool SINKS, bool E8>
 cudaError_t launch_rows(const AttendArgs& p, cudaStream_t s) {
     constexpr int bytes = RowsCfg<D, MT, E8>::kSmem;
     CUtensorMap km, vm;
-    if (!(E8 ? encode_codes(&km, &vm, p, kLook, true) : encode_pages(&km, &vm, p, kLook, D / 64))) return cudaErrorInvalidValue;
+    if (!(E8 ? encode_codes(&km, &vm, p, kLook) : encode_pages(&km, &vm, p, kLook, D / 64))) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> ready{0};  // devices whose kernel has its shared memory
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

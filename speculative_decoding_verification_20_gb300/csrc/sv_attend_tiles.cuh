@@ -62,7 +62,9 @@ struct TilesCfg {
     static constexpr int kTileBytes = kKeyTile * D * 2;
     static constexpr int kQBytes = 256 * D * 2;
     static constexpr int kWBytes = SPLIT ? 0 : 2 * 128 * kKeyTile * 2;  // weights of the two tiles
-    static constexpr int kStages = E8 ? (D == 64 ? (SPLIT ? 8 : 4) : SPLIT ? 3 : 2) : D == 64 ? 8 : SPLIT ? 5 : 3;
+    // E8: stages of keys, then those of values
+    static constexpr int kKeys = D == 64 ? (SPLIT ? 4 : 2) : SPLIT ? 2 : 1, kValues = D == 64 ? kKeys : 1;
+    static constexpr int kStages = E8 ? kKeys + kValues : D == 64 ? 8 : SPLIT ? 5 : 3;
     static constexpr int kRawBytes = kKeyTile * D;        // E8: codes of a tile's keys, or its values
     static constexpr int kRaw = E8 ? (D == 64 ? 6 : SPLIT ? 3 : 2) : 0;
     static constexpr int kHalves = D / 64;                // 128-byte columns of a tile
@@ -682,105 +684,225 @@ __global__ void __launch_bounds__(TilesCfg<D, SPLIT, E8>::kThreads, 1)
                 __syncwarp();
                 next_place();
             };
-            while (alive && left > 0) {
-                const int end = min(u.t1, first + left);
-                const uint32_t last = at + 2 * (end - first);  // the place after the unit's
-                const int q_place = SPLIT ? index & 1 : x;
-                if (SPLIT || u.rt * RM + x * 128 < u.n * p.group) {
-                    const int start = first + (SPLIT ? x : 0);
-                    int lo, hi;
-                    tile_keys<RM>(p, u.past, u.n, u.rt, lo, hi);
-                    const int vend = u.past + u.n;
-                    const uint32_t q_desc = uniform(desc_keys(q_s + q_place * 128 * D * 2));
-                    uint32_t i = at + 2 * (start - first);
-                    // SPLIT: a half waits for the queries of every unit, also of one whose single
-                    // tile is the other's, and frees their place only then.  So nobody frees a place
-                    // twice while the other half has yet to read it, and nobody is a phase of s_q
-                    // ahead: a parity only tells a barrier's last two phases apart.  The place is
-                    // written again when both have freed it, so the unit's count gives the phase.
-                    alive = bar_wait(&s_q[q_place], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
-                    if (start < end) {
-                        alive = alive && reach(i);
-                        if (alive) scores(q_desc, start + STEP >= end, q_place);
-                    } else if (SPLIT && alive && lane == 0) {
-                        bar_arrive(&s_q_free[q_place]);
+            if constexpr (E8) {
+                // Keys and values have a ring each, a place a tile: the next keys of a half come while its
+                // values' place is still taken.  As above, every half waits for every place in order and
+                // gives it back; those of a unit that is not its own go by in the order in which they come.
+                struct Ring {
+                    uint32_t at, stage, turn;
+                } kr = {0, 0, 0}, vr = {0, 0, 0};
+                auto advance = [&](Ring& r, uint32_t n) {
+                    ++r.at;
+                    if (++r.stage == n) {
+                        r.stage = 0;
+                        r.turn ^= 1;
                     }
-                    for (int tile = start; alive && tile < end; tile += STEP, i += 2 * STEP) {
-                        const bool more = tile + STEP < end;
-                        if (!SPLIT) {
-                            // the next scores, as soon as these are read: they are there when the
-                            // softmax ends
-                            if (more) alive = bar_wait(&s_full[stage], turn, limit, dead);
-                            alive = alive && bar_wait(&s_weights[x][0], n_w & 1, limit, dead);
-                            if (alive && more) scores(q_desc, tile + 2 >= end, q_place);
-                            alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
-                        } else {
-                            alive = reach(i + 1);
-                        }
-                        if (!alive) break;
-                        const uint32_t vstage = stage, vs = ring_s + stage * C::kTileBytes;
-                        next_place();
-                        // rows of a box outside the visible keys: what they hold times 0 must be
-                        // 0 (both tiles' warps write these zeros, each before its product)
-                        // (sinks and window may share a tile: what lies between them is zeroed too)
-                        // (E8: whoever converts them does so)
-                        const int k0 = key_tile<SINKS>(u, tile) * kKeyTile;
-                        if (!E8 && (k0 < lo || k0 + kKeyTile > vend)) {
-                            const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, vend - k0));
-                            const int from = SINKS && k0 < p.sinks ? min(z0, p.sinks - k0) : z0 & ~(ta.box - 1);
-                            const int to = (z1 + ta.box - 1) & ~(ta.box - 1);
-                            constexpr int RC = D / 8;  // 16-byte pieces of a row
-                            for (int j = lane; j < (z0 - from + to - z1) * RC; j += 32) {
-                                const int zr = j / RC, c = j % RC;
-                                const int rr = zr < z0 - from ? from + zr : z1 + zr - (z0 - from);
-                                *reinterpret_cast<uint4*>(smem_p + (vs - smem) + (c / 8) * C::kHalfBytes + rr * 128 +
-                                                          ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_async_smem();
-                            __syncwarp();
-                        }
-                        const uint32_t v_desc = uniform(desc_values(vs, C::kHalfBytes));
-                        const uint32_t w_desc = uniform(desc_keys(w_s + x * (C::kWBytes / 2)));
+                };
+                auto full = [&](Ring& r, uint32_t base, uint32_t n, uint32_t i) -> bool {
+                    while (r.at != i) {
+                        if (!bar_wait(&s_full[base + r.stage], r.turn, limit, dead)) return false;
+                        if (lane == 0) bar_arrive(&s_empty[base + r.stage]);
+                        advance(r, n);
+                    }
+                    return bar_wait(&s_full[base + r.stage], r.turn, limit, dead);
+                };
+                auto keys = [&](uint32_t i) { return full(kr, 0, C::kKeys, i); };
+                auto values = [&](uint32_t i) { return full(vr, C::kKeys, C::kValues, i); };
+                auto scores8 = [&](uint32_t q_desc, bool last, int place) {
+                    const uint32_t b = uniform(desc_keys(ring_s + kr.stage * C::kTileBytes));
+                    fence_after();
+                    if (elect()) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            if (SPLIT || half) alive = alive && bar_wait(&s_weights[x][half], n_w & 1, limit, dead);
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = ((k / 4) * C::kHalfBytes + (k % 4) * 32) >> 4;
+                            mma_ss(tS, q_desc + off, b + off, i_s, k > 0);
+                        }
+                        mma_commit(&s_scores[x]);
+                        mma_commit(&s_empty[kr.stage]);
+                        if (SPLIT && last) mma_commit(&s_q_free[place]);
+                    }
+                    __syncwarp();
+                    advance(kr, C::kKeys);
+                };
+                uint32_t done = 0;  // tiles of the units before
+                while (alive && left > 0) {
+                    const int end = min(u.t1, first + left);
+                    const uint32_t all = done + (uint32_t)(end - first);
+                    const int q_place = SPLIT ? index & 1 : x;
+                    if (SPLIT || u.rt * RM + x * 128 < u.n * p.group) {
+                        const int start = first + (SPLIT ? x : 0);
+                        const uint32_t q_desc = uniform(desc_keys(q_s + q_place * 128 * D * 2));
+                        uint32_t i = done + (uint32_t)(start - first);
+                        alive = bar_wait(&s_q[q_place], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
+                        if (start < end) {
+                            alive = alive && keys(i);
+                            if (alive) scores8(q_desc, start + STEP >= end, q_place);
+                        } else if (SPLIT && alive && lane == 0) {
+                            bar_arrive(&s_q_free[q_place]);
+                        }
+                        for (int tile = start; alive && tile < end; tile += STEP, i += STEP) {
+                            const bool more = tile + STEP < end;
+                            if (!SPLIT) {
+                                // the next scores, as soon as these are read
+                                if (more) alive = keys(i + 1);
+                                alive = alive && bar_wait(&s_weights[x][0], n_w & 1, limit, dead);
+                                if (alive && more) scores8(q_desc, tile + 2 >= end, q_place);
+                            }
+                            alive = alive && values(i);
                             if (!alive) break;
-                            fence_after();
-                            if (elect()) {
+                            const uint32_t vstage = C::kKeys + vr.stage;
+                            advance(vr, C::kValues);
+                            const uint32_t v_desc = uniform(desc_values(ring_s + vstage * C::kTileBytes, C::kHalfBytes));
+                            const uint32_t w_desc = uniform(desc_keys(w_s + x * (C::kWBytes / 2)));
 #pragma unroll
-                                for (int k = half * 4; k < half * 4 + 4; ++k) {
-                                    const uint32_t b = v_desc + k * (16 * 128 >> 4);
-                                    const bool add = tile > start || k > 0;
-                                    if constexpr (SPLIT)
-                                        mma_ts(tO, tS + k * 8, b, i_o, add);
-                                    else
-                                        mma_ss(tO, w_desc + (((k / 4) * (128 * 128) + (k % 4) * 32) >> 4), b, i_o, add);
+                            for (int half = 0; half < 2; ++half) {
+                                if (SPLIT || half) alive = alive && bar_wait(&s_weights[x][half], n_w & 1, limit, dead);
+                                if (!alive) break;
+                                fence_after();
+                                if (elect()) {
+#pragma unroll
+                                    for (int k = half * 4; k < half * 4 + 4; ++k) {
+                                        const uint32_t b = v_desc + k * (16 * 128 >> 4);
+                                        const bool add = tile > start || k > 0;
+                                        if constexpr (SPLIT)
+                                            mma_ts(tO, tS + k * 8, b, i_o, add);
+                                        else
+                                            mma_ss(tO, w_desc + (((k / 4) * (128 * 128) + (k % 4) * 32) >> 4), b, i_o, add);
+                                    }
+                                    if (half) {
+                                        if (!SPLIT || !more) mma_commit(&s_out[x]);
+                                        mma_commit(&s_empty[vstage]);
+                                    }
                                 }
-                                if (half) {
-                                    if (!SPLIT || !more) mma_commit(&s_out[x]);
-                                    mma_commit(&s_empty[vstage]);
-                                }
+                                __syncwarp();
                             }
-                            __syncwarp();
-                        }
-                        if (!alive) break;
-                        ++n_w;
-                        if (SPLIT && more) {
-                            alive = reach(i + 2 * STEP);
-                            if (alive) scores(q_desc, tile + 2 * STEP >= end, q_place);
+                            if (!alive) break;
+                            ++n_w;
+                            if (SPLIT && more) {
+                                alive = keys(i + STEP);
+                                if (alive) scores8(q_desc, tile + 2 * STEP >= end, q_place);
+                            }
                         }
                     }
+                    while (alive && (kr.at != all || vr.at != all)) {  // what is left of the unit is the other half's
+                        if (kr.at != all && kr.at == vr.at) {
+                            alive = keys(kr.at);
+                            if (alive && lane == 0) bar_arrive(&s_empty[kr.stage]);
+                            if (alive) advance(kr, C::kKeys);
+                        } else {
+                            alive = values(vr.at);
+                            if (alive && lane == 0) bar_arrive(&s_empty[C::kKeys + vr.stage]);
+                            if (alive) advance(vr, C::kValues);
+                        }
+                    }
+                    done = all;
+                    left -= end - first;
+                    ++index;
+                    if (alive && left > 0) {
+                        next_unit<RM, SINKS>(p, u);
+                        first = u.t0;
+                    }
                 }
-                while (alive && at != last) {  // what is left of the unit is the other half's
-                    alive = bar_wait(&s_full[stage], turn, limit, dead);
-                    if (alive && lane == 0) bar_arrive(&s_empty[stage]);
-                    if (alive) next_place();
-                }
-                left -= end - first;
-                ++index;
-                if (alive && left > 0) {
-                    next_unit<RM, SINKS>(p, u);
-                    first = u.t0;
+            } else {
+                while (alive && left > 0) {
+                    const int end = min(u.t1, first + left);
+                    const uint32_t last = at + 2 * (end - first);  // the place after the unit's
+                    const int q_place = SPLIT ? index & 1 : x;
+                    if (SPLIT || u.rt * RM + x * 128 < u.n * p.group) {
+                        const int start = first + (SPLIT ? x : 0);
+                        int lo, hi;
+                        tile_keys<RM>(p, u.past, u.n, u.rt, lo, hi);
+                        const int vend = u.past + u.n;
+                        const uint32_t q_desc = uniform(desc_keys(q_s + q_place * 128 * D * 2));
+                        uint32_t i = at + 2 * (start - first);
+                        // SPLIT: a half waits for the queries of every unit, also of one whose single
+                        // tile is the other's, and frees their place only then.  So nobody frees a place
+                        // twice while the other half has yet to read it, and nobody is a phase of s_q
+                        // ahead: a parity only tells a barrier's last two phases apart.  The place is
+                        // written again when both have freed it, so the unit's count gives the phase.
+                        alive = bar_wait(&s_q[q_place], (SPLIT ? index >> 1 : (int)n_q++) & 1, limit, dead);
+                        if (start < end) {
+                            alive = alive && reach(i);
+                            if (alive) scores(q_desc, start + STEP >= end, q_place);
+                        } else if (SPLIT && alive && lane == 0) {
+                            bar_arrive(&s_q_free[q_place]);
+                        }
+                        for (int tile = start; alive && tile < end; tile += STEP, i += 2 * STEP) {
+                            const bool more = tile + STEP < end;
+                            if (!SPLIT) {
+                                // the next scores, as soon as these are read: they are there when the
+                                // softmax ends
+                                if (more) alive = bar_wait(&s_full[stage], turn, limit, dead);
+                                alive = alive && bar_wait(&s_weights[x][0], n_w & 1, limit, dead);
+                                if (alive && more) scores(q_desc, tile + 2 >= end, q_place);
+                                alive = alive && bar_wait(&s_full[stage], turn, limit, dead);
+                            } else {
+                                alive = reach(i + 1);
+                            }
+                            if (!alive) break;
+                            const uint32_t vstage = stage, vs = ring_s + stage * C::kTileBytes;
+                            next_place();
+                            // rows of a box outside the visible keys: what they hold times 0 must be
+                            // 0 (both tiles' warps write these zeros, each before its product)
+                            // (sinks and window may share a tile: what lies between them is zeroed too)
+                            const int k0 = key_tile<SINKS>(u, tile) * kKeyTile;
+                            if (k0 < lo || k0 + kKeyTile > vend) {
+                                const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, vend - k0));
+                                const int from = SINKS && k0 < p.sinks ? min(z0, p.sinks - k0) : z0 & ~(ta.box - 1);
+                                const int to = (z1 + ta.box - 1) & ~(ta.box - 1);
+                                constexpr int RC = D / 8;  // 16-byte pieces of a row
+                                for (int j = lane; j < (z0 - from + to - z1) * RC; j += 32) {
+                                    const int zr = j / RC, c = j % RC;
+                                    const int rr = zr < z0 - from ? from + zr : z1 + zr - (z0 - from);
+                                    *reinterpret_cast<uint4*>(smem_p + (vs - smem) + (c / 8) * C::kHalfBytes + rr * 128 +
+                                                              ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                                }
+                                fence_async_smem();
+                                __syncwarp();
+                            }
+                            const uint32_t v_desc = uniform(desc_values(vs, C::kHalfBytes));
+                            const uint32_t w_desc = uniform(desc_keys(w_s + x * (C::kWBytes / 2)));
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                if (SPLIT || half) alive = alive && bar_wait(&s_weights[x][half], n_w & 1, limit, dead);
+                                if (!alive) break;
+                                fence_after();
+                                if (elect()) {
+#pragma unroll
+                                    for (int k = half * 4; k < half * 4 + 4; ++k) {
+                                        const uint32_t b = v_desc + k * (16 * 128 >> 4);
+                                        const bool add = tile > start || k > 0;
+                                        if constexpr (SPLIT)
+                                            mma_ts(tO, tS + k * 8, b, i_o, add);
+                                        else
+                                            mma_ss(tO, w_desc + (((k / 4) * (128 * 128) + (k % 4) * 32) >> 4), b, i_o, add);
+                                    }
+                                    if (half) {
+                                        if (!SPLIT || !more) mma_commit(&s_out[x]);
+                                        mma_commit(&s_empty[vstage]);
+                                    }
+                                }
+                                __syncwarp();
+                            }
+                            if (!alive) break;
+                            ++n_w;
+                            if (SPLIT && more) {
+                                alive = reach(i + 2 * STEP);
+                                if (alive) scores(q_desc, tile + 2 * STEP >= end, q_place);
+                            }
+                        }
+                    }
+                    while (alive && at != last) {  // what is left of the unit is the other half's
+                        alive = bar_wait(&s_full[stage], turn, limit, dead);
+                        if (alive && lane == 0) bar_arrive(&s_empty[stage]);
+                        if (alive) next_place();
+                    }
+                    left -= end - first;
+                    ++index;
+                    if (alive && left > 0) {
+                        next_unit<RM, SINKS>(p, u);
+                        first = u.t0;
+                    }
                 }
             }
             // products still in flight end before tensor memory is given back
@@ -791,29 +913,76 @@ __global__ void __launch_bounds__(TilesCfg<D, SPLIT, E8>::kThreads, 1)
         } else if (warp == 9) {
             // ------------------------------------------------------------ loads
             if constexpr (E8) {
-                // Codes, in the order in which the products take keys and values.  A lane looks up
-                // 16 keys: their page, and the scales.
-                Unit u = part.u;
-                int tile = part.tile, left = part.todo;
-                uint32_t stage = 0, turn = 0, count = 0;  // tiles looked up so far
-                const int per = ta.box / SV_SCALE_BLOCK, no_page = (int)p.a.cache.pages;
+                // Codes, in the order in which the products take keys and values.  Pages and scales of
+                // four tiles are looked up at once, 16 keys a lane, while the four before are loaded:
+                // page ids first, scales behind the first of these tiles.  (Looked up a tile at a
+                // time, the two dependent loads took longer than a tile's copies.)
+                constexpr int kAhead = 32 / kSubs;
+                const int per = ta.box / SV_SCALE_BLOCK, no_page = (int)p.a.cache.pages, sub = lane % kSubs;
+                struct Batch {
+                    Unit u;
+                    int tile, n, left;  // n tiles of the unit from `tile` on; of the CTA's part left behind them
+                    int page, in_page;  // the lane's box (bad and invisible ones: no_page)
+                    float ks, vs;       // its 16 keys' scales
+                    bool bad, seen;
+                } now, next;
+                auto keys_of = [&](const Batch& x, int i) { return key_tile<SINKS>(x.u, x.tile + i) * kKeyTile; };
+                // the page id of the lane's box
+                auto look_up = [&](Batch& x) {
+                    int lo, hi;
+                    tile_keys<RM>(p, x.u.past, x.u.n, x.u.rt, lo, hi);
+                    x.n = min(min(kAhead, x.u.t1 - x.tile), x.left);
+                    x.left -= x.n;
+                    x.page = no_page;
+                    x.in_page = 0;
+                    x.bad = x.seen = false;
+                    if (lane / kSubs < x.n) {
+                        const int k0 = keys_of(x, lane / kSubs), kb = k0 + sub / per * ta.box;
+                        x.seen = any_visible<SINKS>(p, k0 + sub * SV_SCALE_BLOCK, SV_SCALE_BLOCK, lo, hi);
+                        if (any_visible<SINKS>(p, kb, ta.box, lo, hi)) {
+                            const int i = page_of(p, kb);
+                            x.page = p.a.cache.page_table[x.u.b * p.a.cache.page_table_stride + i];
+                            x.in_page = kb - i * (int)p.a.cache.page_size;
+                            x.bad = true;  // (to be seen)
+                        }
+                    }
+                };
+                auto fetch_scales = [&](Batch& x) {
+                    x.bad = x.bad && (x.page < 0 || x.page >= no_page);
+                    if (x.bad) x.page = no_page;
+                    x.ks = 1.0f, x.vs = 0.0f;
+                    if (x.seen && x.page != no_page) {
+                        const int at = x.in_page + sub % per * SV_SCALE_BLOCK;
+                        x.ks = key_scale(p, x.u.h, x.page, at);
+                        x.vs = value_scale(p, x.u.h, x.page, at);
+                    }
+                };
+                // the batch behind x
+                auto follow = [&](const Batch& x, Batch& y) {
+                    y.u = x.u;
+                    y.tile = x.tile + x.n;
+                    y.left = x.left;
+                    if (y.tile == x.u.t1) {
+                        next_unit<RM, SINKS>(p, y.u);
+                        y.tile = y.u.t0;
+                    }
+                    look_up(y);
+                };
+                uint32_t stage = 0, turn = 0, count = 0;  // tiles so far
                 bool alive = true;
                 int issued = 0, index = 0;
                 float vref = kLeastScale;
-                struct Found {
-                    int page, in_page, slot;  // (bad and invisible boxes: no_page)
-                    int z;                    // rows that nobody sees: [z & 255, z >> 8 & 255), and z >> 16 on
-                } now, ahead;
-                auto put = [&](const CUtensorMap* map, int h, const Found& f, bool values) {
+                // a tile's keys or values, from lanes 8 i and on of the batch
+                auto put = [&](const CUtensorMap* map, int h, int page, int in_page, int slot, int z, bool values) {
                     alive = alive && bar_wait(&s_raw_empty[stage], turn ^ 1, limit, dead);
                     if (!alive) return;
                     if (lane == 0) {
-                        s_desc[stage] = make_int4(values, f.slot, f.z, 0);
+                        s_desc[stage] = make_int4(values, slot, z, 0);
                         bar_expect(&s_raw[stage], C::kRawBytes);
                     }
                     __syncwarp();
                     if (lane < kSubs && lane % per == 0)
-                        tma_codes(raw_s + stage * C::kRawBytes + lane * SV_SCALE_BLOCK * D, map, f.in_page, h, f.page,
+                        tma_codes(raw_s + stage * C::kRawBytes + lane * SV_SCALE_BLOCK * D, map, in_page, h, page,
                                   &s_raw[stage]);
                     ++issued;
                     if (++stage == C::kRaw) {
@@ -821,72 +990,59 @@ __global__ void __launch_bounds__(TilesCfg<D, SPLIT, E8>::kThreads, 1)
                         turn ^= 1;
                     }
                 };
-                // looks a unit's tile up and leaves its scales in the next slot; the unit's first tile
-                // starts vref anew
-                auto find = [&](const Unit& w, int tl, bool first) -> Found {
+                // the tile whose values are still to be loaded: keys are one tile ahead of them
+                int v_page = 0, v_in_page = 0, v_slot = 0, v_z = 0, v_h = -1;
+                now.u = part.u;
+                now.tile = part.tile;
+                now.left = part.todo;
+                look_up(now);
+                fetch_scales(now);
+                bool first = true;  // the CTA's first tile of a unit
+                while (alive) {
+                    const bool more = now.left > 0;
+                    if (more) follow(now, next);
                     int lo, hi;
-                    tile_keys<RM>(p, w.past, w.n, w.rt, lo, hi);
-                    const int k0 = key_tile<SINKS>(w, tl) * kKeyTile, k = k0 + lane * SV_SCALE_BLOCK;
-                    const int kb = k0 + lane / per * ta.box;  // the lane's box
-                    Found f;
-                    f.page = no_page;
-                    f.in_page = 0;
-                    f.slot = (int)(count++ % kSlots);
-                    const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, hi + 1 - k0));
-                    f.z = min(z0, max(0, sinks_of<SINKS>(p) - k0)) | z0 << 8 | z1 << 16;
-                    float ks = 1.0f, vs = 0.0f;
-                    bool bad = false;
-                    if (lane < kSubs && any_visible<SINKS>(p, kb, ta.box, lo, hi)) {
-                        const int i = page_of(p, kb);
-                        f.page = p.a.cache.page_table[w.b * p.a.cache.page_table_stride + i];
-                        f.in_page = kb - i * (int)p.a.cache.page_size;
-                        bad = f.page < 0 || f.page >= no_page;
-                        if (bad) {
-                            f.page = no_page;
-                        } else if (any_visible<SINKS>(p, k, SV_SCALE_BLOCK, lo, hi)) {
-                            ks = key_scale(p, w.h, f.page, f.in_page + (k - kb));
-                            vs = value_scale(p, w.h, f.page, f.in_page + (k - kb));
+                    tile_keys<RM>(p, now.u.past, now.u.n, now.u.rt, lo, hi);
+                    for (int i = 0; alive && i < now.n; ++i) {
+                        const int from = i * kSubs + sub;
+                        const int page = __shfl_sync(0xFFFFFFFFu, now.page, from);
+                        const int in_page = __shfl_sync(0xFFFFFFFFu, now.in_page, from);
+                        const float ks = __shfl_sync(0xFFFFFFFFu, now.ks, from), vs = __shfl_sync(0xFFFFFFFFu, now.vs, from);
+                        const bool bad = __any_sync(0xFFFFFFFFu, now.bad && lane / kSubs == i);
+                        if (first && lane == 0) s_bad[index % kBadSlots] = 0;
+                        __syncwarp();
+                        if (bad && lane == 0) {
+                            *(volatile int*)&s_bad[index % kBadSlots] = 1;
+                            if (p.a.row_status) atomicOr(p.a.row_status + now.u.b, SV_ROW_BAD_PAGE);
+                            __threadfence_block();
                         }
-                    }
-                    if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) {
-                        *(volatile int*)&s_bad[index % kBadSlots] = 1;
-                        if (p.a.row_status) atomicOr(p.a.row_status + w.b, SV_ROW_BAD_PAGE);
-                        __threadfence_block();
-                    }
-                    float top = vs;
+                        const int slot = (int)(count++ % kSlots), k0 = keys_of(now, i);
+                        float top = vs;
 #pragma unroll
-                    for (int o = 1; o < kSubs; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                    vref = fmaxf(first ? kLeastScale : vref, __shfl_sync(0xFFFFFFFFu, top, 0));
-                    if (lane < kSubs) {
-                        s_ks[f.slot][lane] = ks;
-                        s_vs[f.slot][lane] = vs / vref;
-                        if (lane == 0) s_vref[f.slot] = vref;
-                    }
-                    __syncwarp();
-                    return f;
-                };
-                while (alive && left > 0) {
-                    const int end = min(u.t1, tile + left);
-                    left -= end - tile;
-                    if (lane == 0) s_bad[index % kBadSlots] = 0;
-                    __syncwarp();
-                    now = find(u, tile, true);
-                    if (!SPLIT) put(&kmap, u.h, now, false);  // keys are one tile ahead of the values
-                    for (; alive && tile < end; ++tile) {
-                        if (SPLIT) put(&kmap, u.h, now, false);
-                        if (tile + 1 < end) {
-                            ahead = find(u, tile + 1, false);
-                            if (!SPLIT) put(&kmap, u.h, ahead, false);
+                        for (int o = 1; o < kSubs; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                        vref = fmaxf(first ? kLeastScale : vref, top);
+                        first = false;
+                        if (lane < kSubs) {
+                            s_ks[slot][lane] = ks;
+                            s_vs[slot][lane] = vs / vref;
+                            if (lane == 0) s_vref[slot] = vref;
                         }
-                        put(&vmap, u.h, now, true);
-                        now = ahead;
+                        __syncwarp();
+                        const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, hi + 1 - k0));
+                        const int z = min(z0, max(0, sinks_of<SINKS>(p) - k0)) | z0 << 8 | z1 << 16;
+                        put(&kmap, now.u.h, page, in_page, slot, z, false);
+                        if (v_h >= 0) put(&vmap, v_h, v_page, v_in_page, v_slot, v_z, true);
+                        v_page = page, v_in_page = in_page, v_slot = slot, v_z = z, v_h = now.u.h;
+                        if (now.tile + i + 1 == now.u.t1) {
+                            ++index;
+                            first = true;
+                        }
+                        if (i == 0 && more) fetch_scales(next);
                     }
-                    ++index;
-                    if (left > 0) {
-                        next_unit<RM, SINKS>(p, u);
-                        tile = u.t0;
-                    }
+                    if (!more) break;
+                    now = next;
                 }
+                put(&vmap, v_h, v_page, v_in_page, v_slot, v_z, true);
                 // copies still in flight end before the CTA does (whoever gave up)
                 const unsigned long long t0 = now_ns();
                 const int n = min(issued, C::kRaw);
@@ -999,53 +1155,58 @@ __global__ void __launch_bounds__(TilesCfg<D, SPLIT, E8>::kThreads, 1)
             }
         } else if (E8 && warp >= 12) {
             // ------------------------------------------------------ codes to fp16
-            // A thread takes every 128th 16 bytes of a tile.  They become two pieces of 16 bytes of the
-            // row, of which lanes of the row's first and second half write one first each, so that eight
-            // lanes' writes fall on different banks.
-            constexpr int RC = D / 16, PER = 128 * RC / 128;
-            const int ct = t - 384, c = ct % RC, r0 = ct / RC;
-            uint32_t rs = 0, rturn = 0, os = 0, oturn = 0;
+            // A thread has a row.  Codes lie swizzled as their fp16 will, so that eight lanes' reads, and
+            // their writes, fall on different banks, and a row's pieces differ by an exclusive or.
+            constexpr int PC = D / 16;  // 16-byte pieces of a row of codes: each becomes two
+            const int r = t - 384;
+            const uint32_t raw_at = raw_s - smem + r * D + ((D == 64 ? r >> 1 & 3 : r & 7) << 4);
+            const uint32_t at = ring_s - smem + r * 128 + ((r & 7) << 4);
+            uint32_t rs = 0, rturn = 0, ks = 0, kturn = 0, vs = 0, vturn = 0;
             bool alive = true;
             for (int i = 0; alive && i < 2 * part.todo; ++i) {
-                alive = bar_wait(&s_raw[rs], rturn, limit, dead) && bar_wait(&s_empty[os], oturn ^ 1, limit, dead);
+                alive = bar_wait(&s_raw[rs], rturn, limit, dead);
                 if (!alive) break;
                 const int4 d = s_desc[rs];
-                const int z0 = d.z & 255, z1 = d.z >> 8 & 255, z2 = d.z >> 16;
-                const unsigned char* src = smem_p + (raw_s - smem) + rs * C::kRawBytes + ct * 16;
-                unsigned char* dst = smem_p + (ring_s - smem) + os * C::kTileBytes + (c >> 2) * C::kHalfBytes;
-#pragma unroll 4
-                for (int k = 0; k < PER; ++k) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(src + k * 2048);
-                    const int r = r0 + k * (128 / RC);
+                const uint32_t os = d.x ? C::kKeys + vs : ks;
+                const uint32_t src = raw_at + rs * C::kRawBytes, dst = at + os * C::kTileBytes;
+                // (all codes first: a load behind a store to shared memory would wait for it)
+                uint4 q[PC];
+#pragma unroll
+                for (int c = 0; c < PC; ++c) q[c] = *reinterpret_cast<const uint4*>(smem_p + (src ^ c << 4));
+                // what rows that nobody sees hold times 0 must be 0
+                const bool none = d.x && ((r >= (d.z & 255) && r < (d.z >> 8 & 255)) || r >= d.z >> 16);
+                const __half2 f = __float2half2_rn(d.x ? s_vs[d.y][r / SV_SCALE_BLOCK] : 1.0f);
+                __syncwarp();
+                if (lane == 0) bar_arrive(&s_raw_empty[rs]);
+                alive = bar_wait(&s_empty[os], (d.x ? vturn : kturn) ^ 1, limit, dead);
+                if (!alive) break;
+#pragma unroll
+                for (int c = 0; c < PC; ++c) {
                     uint32_t w[8];
-                    codes_half(q.x, w[0], w[1]);
-                    codes_half(q.y, w[2], w[3]);
-                    codes_half(q.z, w[4], w[5]);
-                    codes_half(q.w, w[6], w[7]);
+                    codes_half(q[c].x, w[0], w[1]);
+                    codes_half(q[c].y, w[2], w[3]);
+                    codes_half(q[c].z, w[4], w[5]);
+                    codes_half(q[c].w, w[6], w[7]);
                     if (d.x) {
-                        const __half2 f = __float2half2_rn(s_vs[d.y][r / SV_SCALE_BLOCK]);
-                        const bool none = (r >= z0 && r < z1) || r >= z2;  // what they hold times 0 must be 0
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), f);
                             w[e] = none ? 0u : *reinterpret_cast<const uint32_t*>(&y);
                         }
                     }
-                    const uint4 a = make_uint4(w[0], w[1], w[2], w[3]), b = make_uint4(w[4], w[5], w[6], w[7]);
-                    const bool late = RC == 8 && c >= 4;
-                    unsigned char* row = dst + r * 128;
-                    const int p0 = (2 * c & 7) + (late ? 1 : 0), p1 = p0 ^ 1;
-                    *reinterpret_cast<uint4*>(row + ((p0 ^ (r & 7)) << 4)) = late ? b : a;
-                    *reinterpret_cast<uint4*>(row + ((p1 ^ (r & 7)) << 4)) = late ? a : b;
+                    const uint32_t to = (dst ^ (2 * c & 7) << 4) + (c >> 2) * C::kHalfBytes;
+                    *reinterpret_cast<uint4*>(smem_p + to) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(smem_p + (to ^ 16)) = make_uint4(w[4], w[5], w[6], w[7]);
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(&s_full[os]);
-                    bar_arrive(&s_raw_empty[rs]);
-                }
+                if (lane == 0) bar_arrive(&s_full[os]);
                 if (++rs == C::kRaw) rs = 0, rturn ^= 1;
-                if (++os == C::kStages) os = 0, oturn ^= 1;
+                if (d.x) {
+                    if (++vs == C::kValues) vs = 0, vturn ^= 1;
+                } else {
+                    if (++ks == C::kKeys) ks = 0, kturn ^= 1;
+                }
             }
         } else if (SPLIT) {
             // ---------------------------------------------------------- queries
@@ -1102,7 +1263,7 @@ cudaError_t launch_tiles(const AttendArgs& p, cudaStream_t s) {
     ta.box = 16;
     while (ta.box < kKeyTile && p.a.cache.page_size % (2 * ta.box) == 0) ta.box *= 2;
     CUtensorMap km, vm;
-    if (!(E8 ? encode_codes(&km, &vm, p, ta.box, false) : encode_pages(&km, &vm, p, ta.box, 1))) return cudaErrorInvalidValue;
+    if (!(E8 ? encode_codes(&km, &vm, p, ta.box) : encode_pages(&km, &vm, p, ta.box, 1))) return cudaErrorInvalidValue;
     // once a device: room in shared memory
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
