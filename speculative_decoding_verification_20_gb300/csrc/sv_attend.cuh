@@ -348,11 +348,6 @@ __device__ __forceinline__ void codes_half(uint32_t w, uint32_t& b0, uint32_t& b
         : "=r"(b0), "=r"(b1)
         : "r"(w));
 }
-// query rows of D elements, swizzled likewise
-template <int D>
-__device__ __forceinline__ uint32_t q_at(int r, int c) {
-    return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
-}
 // the scales of a block of positions:
 __device__ __forceinline__ float key_scale(const AttendArgs& p, int h, int page, int in_page) {
     return p.sc.k[page * p.sc.k_stride_page + h * p.sc.k_stride_head + in_page / SV_SCALE_BLOCK];

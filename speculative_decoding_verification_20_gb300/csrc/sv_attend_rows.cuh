@@ -82,6 +82,11 @@ template <int D>
 __device__ __forceinline__ uint32_t code_at(int r, int c) {
     return (uint32_t)(r * D + ((c ^ (D == 64 ? r >> 1 & 3 : r & 7)) << 4));
 }
+// query rows of D elements, swizzled likewise
+template <int D>
+__device__ __forceinline__ uint32_t q_at(int r, int c) {
+    return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
+}
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kACompute) : "memory"); }
 
 template <int D, int MT, bool E8>
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             const int pos_first = u.past + by_group(p, r00);
             float o[D / 8][4];
             float ref[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
-            float vref = E8 ? kLeastScale : 1.0f;
+            float vref = E8 ? kLeastScale : 1.0f, vinv = 1.0f / vref;
             const float qf[2] = {E8 ? s_qf[r0] : p.qscale, E8 ? s_qf[r0 + 8] : p.qscale};
 #pragma unroll
             for (int d = 0; d < D / 8; ++d)
@@ -424,11 +429,14 @@ __global__ void __launch_bounds__(kAThreads, 1)
                                 o[d][2 * e + 1] *= f;
                             }
                         }
-                        vref = vtop;
+                        if (E8 && vtop > vref) {
+                            vref = vtop;
+                            vinv = 1.0f / vtop;
+                        }
                     }
                     if constexpr (E8) {
-                        vw[0] /= vref;
-                        vw[1] /= vref;
+                        vw[0] *= vinv;
+                        vw[1] *= vinv;
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {

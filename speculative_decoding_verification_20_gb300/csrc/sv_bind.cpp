@@ -29,6 +29,7 @@ int (*g_attention)(const sv_attention_args*, void*) = nullptr;
 int (*g_rotate_ex)(const sv_rotate_args*, const sv_rotate_options*, void*) = nullptr;
 int (*g_attention_ex)(const sv_attention_args*, const sv_attention_options*, void*) = nullptr;
 int (*g_sample)(const sv_sample_args*, void*) = nullptr;
+int (*g_read)(const sv_read_args*, void*) = nullptr;
 size_t (*g_attention_ws)(int64_t, int64_t, int64_t, int64_t, int64_t) = nullptr;
 PyObject* g_error = nullptr;  // raises for a status: g_error(status)
 
@@ -321,6 +322,16 @@ PyObject* logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// a pair of results
+PyObject* both(PyObject* first, const at::Tensor& second) {
+    if (!first) return nullptr;
+    PyObject* p = THPVariable_Wrap(second);
+    PyObject* t = p ? PyTuple_Pack(2, first, p) : nullptr;
+    Py_DECREF(first);
+    Py_XDECREF(p);
+    return t;
+}
+
 // sample(logits, uniforms, temperature, top_k, top_p, min_p, row_status): (tokens, probs)
 PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -353,24 +364,47 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g.tokens = tokens.data_ptr<int32_t>();
     g.probs = probs.data_ptr<float>();
     g.row_status = (uint32_t*)status;
-    PyObject* t = done(g_sample(&g, at::cuda::getCurrentCUDAStream(d.index()).stream()), tokens);
-    if (!t) return nullptr;
-    PyObject* p = THPVariable_Wrap(probs);
-    PyObject* both = p ? PyTuple_Pack(2, t, p) : nullptr;
-    Py_DECREF(t);
-    Py_XDECREF(p);
-    return both;
+    return both(done(g_sample(&g, at::cuda::getCurrentCUDAStream(d.index()).stream()), tokens), probs);
+    END_HANDLE_TH_ERRORS
+}
+
+// read(k, v, k_scales, v_scales, page_table, first, N, count, half (else bfloat16), row_status): (k, v)
+PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor *k, *ck, *cv, *pt;
+    if (n != 10 || !tensor(a[0], &k)) SV_NONE;
+    const at::Device d = k->device();
+    sv_read_args g;
+    std::memset(&g, 0, sizeof g);
+    if (!current(d) || !codes(a[0], a[1], a[2], a[3], d, &ck, &cv, &g.scales) || !tensor(a[4], &pt) || pt->dim() != 2) SV_NONE;
+    const int64_t B = pt->size(0), N = PyLong_AsLongLong(a[6]);
+    const int half = PyObject_IsTrue(a[8]);
+    const void *first, *count, *status;
+    if (PyErr_Occurred() || half < 0 || B == 0 || N < 1 || !page_table(a[4], d, B, &pt) || !vec(a[5], d, at::kInt, B, &first) ||
+        !first || !vec(a[7], d, at::kInt, B, &count) || !vec(a[9], d, at::kInt, B, &status))
+        SV_NONE;
+    const auto options = k->options().dtype(half ? at::kHalf : at::kBFloat16);
+    at::Tensor ko = at::empty({B, N, ck->size(1), ck->size(3)}, options), vo = at::empty_like(ko);
+    fill(&g.cache, *ck, *cv, *pt, first, count);
+    g.struct_size = sizeof g;
+    g.k_out = ko.data_ptr();
+    g.v_out = vo.data_ptr();
+    g.dtype = half ? SV_F16 : SV_BF16;
+    g.B = B, g.N = N, g.kv_heads = ck->size(1), g.dim = ck->size(3);
+    g.row_status = (uint32_t*)status;
+    return both(done(g_read(&g, at::cuda::getCurrentCUDAStream(d.index()).stream()), ko), vo);
     END_HANDLE_TH_ERRORS
 }
 
 // setup(addresses of the C functions, the function that raises for a status)
 PyObject* setup(PyObject*, PyObject* args) {
-    unsigned long long l, r, t, w, rx, tx, m;
+    unsigned long long l, r, t, w, rx, tx, m, c;
     PyObject* e;
-    if (!PyArg_ParseTuple(args, "KKKKKKKO", &l, &r, &t, &w, &rx, &tx, &m, &e)) return nullptr;
+    if (!PyArg_ParseTuple(args, "KKKKKKKKO", &l, &r, &t, &w, &rx, &tx, &m, &c, &e)) return nullptr;
     g_rotate_ex = (decltype(g_rotate_ex))rx;
     g_attention_ex = (decltype(g_attention_ex))tx;
     g_sample = (decltype(g_sample))m;
+    g_read = (decltype(g_read))c;
     g_logits = (decltype(g_logits))l;
     g_rotate = (decltype(g_rotate))r;
     g_attention = (decltype(g_attention))t;
@@ -383,6 +417,7 @@ PyObject* setup(PyObject*, PyObject* args) {
 PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, nullptr},
                          {"attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, nullptr},
                          {"rotate", (PyCFunction)(void (*)(void))rotate, METH_FASTCALL, nullptr},
+                         {"read", (PyCFunction)(void (*)(void))read, METH_FASTCALL, nullptr},
                          {"sample", (PyCFunction)(void (*)(void))sample, METH_FASTCALL, nullptr},
                          {"logits", (PyCFunction)(void (*)(void))logits, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -1,8 +1,8 @@
 // sv_cache8.cu -- reading back what a cache held in 8 bits stands for (spec_verify_read_cache).
 //
-// A block has one position; a thread takes 16 codes of a head's row, keys or values, and
+// A block has four positions; a thread takes 16 codes of a head's row, keys or values, of each and
 // writes 16 numbers.  The call is bound by its bytes (1 read, 2 written an element), small
-// ones by the chain lengths -> page id -> codes.
+// ones by the chain lengths -> page id -> codes, which the four go through together.
 #include <cuda_runtime.h>
 
 #include "sv_internal.cuh"
@@ -11,49 +11,66 @@
 namespace sv {
 namespace {
 
-constexpr int kReadThreads = 128;
+constexpr int kReadThreads = 128, kReadRows = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ sv_read_args a) {
-    const int b = (int)(blockIdx.x / (unsigned)a.N), i = (int)(blockIdx.x % (unsigned)a.N);
+    const unsigned groups = (unsigned)((a.N + kReadRows - 1) / kReadRows);
+    const int b = (int)(blockIdx.x / groups), i0 = (int)(blockIdx.x % groups) * kReadRows;
     const int H = (int)a.kv_heads, per = (int)a.dim / 16;
     const SeqLens sl = seq_lens(a.cache, b, (int)a.N, a.cache.pages_per_seq * a.cache.page_size);
-    if (sl.bad && threadIdx.x == 0 && i == 0 && a.row_status) atomicOr(a.row_status + b, SV_ROW_BAD_LENGTH);
-    const bool live = i < sl.n;
-    bool nan = sl.bad;
-    int64_t page = 0, slot = 0;
-    if (live) {
-        const int pos = sl.past + i, at = pos / (int)a.cache.page_size;
-        page = a.cache.page_table[b * a.cache.page_table_stride + at];
-        slot = pos - at * (int)a.cache.page_size;
-        if (page < 0 || page >= a.cache.pages) {
-            nan = true;
+    if (sl.bad && threadIdx.x == 0 && i0 == 0 && a.row_status) atomicOr(a.row_status + b, SV_ROW_BAD_LENGTH);
+    int64_t page[kReadRows], slot[kReadRows];
+    bool nan[kReadRows];
+#pragma unroll
+    for (int i = 0; i < kReadRows; ++i) {
+        page[i] = -1;  // (nothing to read)
+        slot[i] = 0;
+        nan[i] = sl.bad;
+        if (i0 + i >= sl.n) continue;
+        const int pos = sl.past + i0 + i, at = pos / (int)a.cache.page_size;
+        page[i] = a.cache.page_table[b * a.cache.page_table_stride + at];
+        slot[i] = pos - at * (int)a.cache.page_size;
+        nan[i] = page[i] < 0 || page[i] >= a.cache.pages;
+        if (nan[i]) {
+            page[i] = -1;
             if (threadIdx.x == 0 && a.row_status) atomicOr(a.row_status + b, SV_ROW_BAD_PAGE);
         }
     }
     for (int x = threadIdx.x; x < 2 * H * per; x += kReadThreads) {
         const bool keys = x < H * per;
         const int y = keys ? x : x - H * per, h = y / per, c = y % per * 16;
-        const uint32_t none = nan ? Pair<T>::pack(NAN, NAN) : 0u;
-        uint32_t w[8] = {none, none, none, none, none, none, none, none};
-        if (live && !nan) {
-            const uint8_t* src = keys ? (const uint8_t*)a.cache.k_pages + page * a.cache.k_stride_page +
-                                            h * a.cache.k_stride_head + slot * a.cache.k_stride_slot
-                                      : (const uint8_t*)a.cache.v_pages + page * a.cache.v_stride_page +
-                                            h * a.cache.v_stride_head + slot * a.cache.v_stride_slot;
-            const float s = keys ? a.scales.k[page * a.scales.k_stride_page + h * a.scales.k_stride_head + slot / SV_SCALE_BLOCK]
-                                 : a.scales.v[page * a.scales.v_stride_page + h * a.scales.v_stride_head + slot / SV_SCALE_BLOCK];
-            const uint4 q = *reinterpret_cast<const uint4*>(src + c);
-            const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
+        const uint8_t* base = keys ? (const uint8_t*)a.cache.k_pages + h * a.cache.k_stride_head
+                                   : (const uint8_t*)a.cache.v_pages + h * a.cache.v_stride_head;
+        const float* scales = keys ? a.scales.k + h * a.scales.k_stride_head : a.scales.v + h * a.scales.v_stride_head;
+        const int64_t sp = keys ? a.cache.k_stride_page : a.cache.v_stride_page;
+        const int64_t ss = keys ? a.cache.k_stride_slot : a.cache.v_stride_slot;
+        const int64_t scp = keys ? a.scales.k_stride_page : a.scales.v_stride_page;
+        uint4 q[kReadRows];
+        float s[kReadRows];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 f = e4m3_pair(qs[e / 2] >> (e % 2 * 16));
-                w[e] = Pair<T>::pack(f.x * s, f.y * s);
-            }
+        for (int i = 0; i < kReadRows; ++i) {
+            if (page[i] < 0) continue;
+            q[i] = *reinterpret_cast<const uint4*>(base + page[i] * sp + slot[i] * ss + c);
+            s[i] = scales[page[i] * scp + slot[i] / SV_SCALE_BLOCK];
         }
-        T* dst = (T*)(keys ? a.k_out : a.v_out) + (((int64_t)b * a.N + i) * H + h) * a.dim + c;
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int i = 0; i < kReadRows; ++i) {
+            if (i0 + i >= a.N) break;
+            const uint32_t none = nan[i] ? Pair<T>::pack(NAN, NAN) : 0u;
+            uint32_t w[8] = {none, none, none, none, none, none, none, none};
+            if (page[i] >= 0) {
+                const uint32_t qs[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = e4m3_pair(qs[e / 2] >> (e % 2 * 16));
+                    w[e] = Pair<T>::pack(f.x * s[i], f.y * s[i]);
+                }
+            }
+            T* dst = (T*)(keys ? a.k_out : a.v_out) + (((int64_t)b * a.N + i0 + i) * H + h) * a.dim + c;
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
     }
 }
 
@@ -73,7 +90,7 @@ extern "C" int spec_verify_read_cache(const sv_read_args* args, void* stream) {
     int rc = sv::check_cache(a.cache, a.B, a.kv_heads, a.dim, 1);
     if (rc == SV_OK) rc = sv::check_scales(a.scales, a.cache, a.kv_heads);
     if (rc != SV_OK) return rc;
-    const unsigned grid = (unsigned)(a.B * a.N);
+    const unsigned grid = (unsigned)(a.B * ((a.N + sv::kReadRows - 1) / sv::kReadRows));
     cudaStream_t s = (cudaStream_t)stream;
     if (a.dtype == SV_BF16)
         sv::read_kernel<__nv_bfloat16><<<grid, sv::kReadThreads, 0, s>>>(a);

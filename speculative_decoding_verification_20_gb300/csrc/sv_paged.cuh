@@ -48,11 +48,8 @@ __device__ __forceinline__ float2 e4m3_pair(uint32_t w) {
     const uint32_t h = e4m3_half2(w);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// two numbers as codes, lo in the low byte; infinities become NaN (the conversion alone would
-// make them the largest value)
+// two numbers (not infinite) as codes, lo in the low byte
 __device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
-    if (isinf(lo)) lo = NAN;
-    if (isinf(hi)) hi = NAN;
     uint16_t c;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(lo), "f"(hi));
     return c;

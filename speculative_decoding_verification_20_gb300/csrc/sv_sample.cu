@@ -334,10 +334,10 @@ struct SampleRow {
         return n;
     }
 
-    // ceil(P S) for the comparison of whole numbers with it, floor(u S)
+    // ceil(P S) for the comparison of whole numbers with it (at least 1: the likeliest is kept), floor(u S)
     static __device__ long long mass_target(float P, long long S) {
         const unsigned long long p = scaled(P, 64);
-        return (long long)(__umul64hi(p, (unsigned long long)S) + (p * (unsigned long long)S != 0));
+        return max((long long)(__umul64hi(p, (unsigned long long)S) + (p * (unsigned long long)S != 0)), 1ll);
     }
     static __device__ long long share_of(float u, long long S) {
         return (long long)__umul64hi(scaled(u, 64), (unsigned long long)S);

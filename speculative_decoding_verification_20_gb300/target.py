@@ -88,7 +88,7 @@ class _Short:
         _bind.setup(address(lib.spec_verify_process_logits), address(lib.spec_verify_rotate_append),
                     address(lib.spec_verify_attention), address(lib.spec_verify_attention_workspace_size),
                     address(lib.spec_verify_rotate_append_ex), address(lib.spec_verify_attention_ex),
-                    address(lib.spec_verify_sample), _check)
+                    address(lib.spec_verify_sample), address(lib.spec_verify_read_cache), _check)
         _short = _bind
         return getattr(_bind, name)
 
@@ -574,6 +574,11 @@ def read_cache(cache: PagedCache8, page_table: torch.Tensor, first, N: int, coun
     (int32 [B]; count [B] of the N are wanted, default all; the others are zeros), code times scale rounded to dtype."""
     if not isinstance(cache, PagedCache8):
         raise TypeError("read_cache takes a PagedCache8")
+    if stream is None and dtype in (torch.bfloat16, torch.float16):
+        res = _short.read(cache.k, cache.v, cache.k_scales, cache.v_scales, page_table, first, N, count,
+                          dtype == torch.float16, row_status)
+        if res is not None:
+            return res
     if not cache.k.is_cuda:
         raise ValueError("the cache must be on a CUDA device")
     dev = cache.device

@@ -179,3 +179,50 @@ def test_draws_feed_verification():
     assert res["row_status"].tolist() == [0] * B
     assert res["accepted_len"].tolist() == [G] * B
     assert torch.equal(res["out_tokens"][:, :G], x) and bool((prob > 0).all())
+
+
+def test_threads_and_rows_that_share_memory():
+    """Calls of two threads on streams of their own; rows of logits that lie on one another."""
+    import threading
+
+    z, u = rows(20, 2, 9001, F32, seed=12)
+    x, uu = z.cuda(), u.cuda()
+    want = sv.sample(x, uu, 0.8, 30, 0.9)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got = sv.sample(x, uu, 0.8, 30, 0.9, stream=s)
+            s.synchronize()
+            if not (torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])):
+                bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    one = x[:1, :1].expand(20, 2, 9001)
+    tok, prob = sv.sample(one, uu, 0.8, None, 0.9)
+    for b in range(20):
+        for i in range(2):
+            t, p, near = ref.sample(z[0, 0].double(), float(u[b, i]), float(torch.tensor(0.8, dtype=F32)), 0,
+                                    float(torch.tensor(0.9, dtype=F32)), 0.0)
+            assert near > NEAR and int(tok[b, i]) == t and abs(float(prob[b, i]) - p) <= p * U32 * 1.01
+
+
+@pytest.mark.parametrize("V", [300, 70000])
+def test_settings_at_the_ends_of_their_ranges(V):
+    z, u = rows(6, 1, V, F32, seed=21)
+    check(z, u, [1.0, 0.01, 1.0, 1.0, 1.0, 1000.0], [0, 0, V, V - 1, 1, 0], [1e-30, 1e-38, 1e-7, 1.0, 1e-40, 1 - 2.0 ** -24],
+          [0.0, 0.0, 1e-30, 1e-40, 1.0, 1.0])
+    u[:] = torch.tensor([[0.0], [1e-40], [2.0 ** -24], [1 - 2.0 ** -24], [1e-30], [2.0 ** -60]])
+    tok, prob = sv.sample(z.cuda(), u.cuda(), 1.0, None, 0.999999, None)
+    for b in range(6):  # (the first and the last kept token: the sums' ends, not between borders)
+        w = torch.exp(z[b, 0].double() - z[b, 0].max().double())
+        assert w[int(tok[b, 0])] > 0 and 0 < float(prob[b, 0]) <= 1
+        if b != 3:
+            assert int(tok[b, 0]) <= int((torch.cumsum(w, 0) > w.sum() * 2.0 ** -22).nonzero()[0, 0])
