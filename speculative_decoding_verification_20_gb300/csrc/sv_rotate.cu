@@ -74,15 +74,17 @@ __device__ __forceinline__ float two_sum(float a, float b, float& err) {
     err = __fadd_rn(__fsub_rn(b, bv), __fsub_rn(a, av));
     return s;
 }
-// a c + b s, rounded to odd: products and their errors, then the sum and its own
+// a c + b s, rounded to odd: products and their errors, then the sum and its own.  (The products'
+// errors may be steps of a smaller sum: they go into it before what is missing is looked at.)
 __device__ __forceinline__ float dot2_odd(float a, float c, float b, float s) {
     const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
     const float pe = __fmaf_rn(a, c, -p), qe = __fmaf_rn(b, s, -q);
-    float e, f;
-    const float hi = two_sum(p, q, e);
-    const float g = two_sum(pe, qe, f);
-    const float lo = __fadd_rn(e, g);
-    return to_odd(hi, lo != 0.0f ? lo : f);
+    float e, f, g, h;
+    const float sum = two_sum(p, q, e);
+    const float errors = two_sum(pe, qe, f);
+    const float low = two_sum(e, errors, g);
+    const float hi = two_sum(sum, low, h);
+    return to_odd(hi, h != 0.0f ? h : __fadd_rn(g, f));
 }
 
 // The same to 1.5 steps (an exact product's error added behind the other product).

@@ -56,14 +56,15 @@ def visible(past, n, window, sinks, device):
     return ok
 
 
-def attention(q, k, v, past, scale, window, sinks, eight=False):
+def attention(q, k, v, past, scale, window, sinks, eight=False, ratios=False):
     """q [n, Hq, D]; k, v [Hkv, past + n, D] float64 values.  Returns float64 [n, Hq, D] and its tolerance.
 
     As in target_ref.attention, with h half a step of what the weights are rounded to (8-bit cache: fp16), and of the
     scores' error two roundings more for the scales.  fp16 weights are kept 2^7 times as large and at most 2^8 above the
     row's reference, so that the largest is at least 2^7 and one below 2^-14 is off by up to 2^-25: 2^-32 of the
     largest's; with an 8-bit cache the weights are relative to the largest scale of a value, so this is of the largest
-    value that can be."""
+    value that can be.  ratios: values' scales are not powers of two, so that above 32 rows a cache head their quotients by
+    the largest, and the values times these, are rounded to fp16: two half steps more."""
     n, Hq, D = q.shape
     Hkv, L = k.shape[0], k.shape[1]
     grp = Hq // Hkv
@@ -80,7 +81,7 @@ def attention(q, k, v, past, scale, window, sinks, eight=False):
     size = p @ v.abs()
     delta = s_abs.masked_fill(~ok, 0.0).amax(-1, keepdim=True) * (2 * D + (8 if eight else 4)) * U32
     h = half_step(torch.float16 if eight else dtype)
-    tol = size * (h * (1 + eight * 2.0 ** -8) + 2 * delta + 4 * (L + 64) * U32) + half_step(dtype) * o.abs() + 1e-30
+    tol = size * (h * (1 + eight * 2.0 ** -8 + 2 * ratios) + 2 * delta + 4 * (L + 64) * U32) + half_step(dtype) * o.abs() + 1e-30
     if dtype == torch.float16:  # the result's own absolute step
         tol = tol + 2.0 ** -25
     if eight or dtype == torch.float16:
