@@ -403,10 +403,12 @@ struct SampleRow {
             const bool in = x.e < n && place < K;
             const long long S = sum_of(in && x.first ? x.w : 0);
             const long long target = P < 1.0f ? mass_target(P, S) : 0x7FFFFFFFFFFFFFFFll;
-            const bool keep = in && (long long)(a >> 10) < target && x.w >= least;
-            // what is kept comes first in the order: again by ids (the low half of a key falls with them)
-            if (keep && x.first) s.pairs[place] = Pair16{x.key & 0xFFFFFFFFu, (unsigned long long)x.w};
-            const int kept_n = count_of(keep && x.first);
+            // what is kept comes first in the order (by number: weights of neighbouring logits may be off by more than
+            // their distance)
+            const int kept_n = count_of(in && x.first && (long long)(a >> 10) < target && x.w >= least);
+            // again, by ids (the low half of a key falls with them)
+            if (x.e < n && x.first && place < kept_n) s.pairs[place] = Pair16{x.key & 0xFFFFFFFFu, (unsigned long long)x.w};
+            __syncthreads();
             Entry y = entry(kept_n);
             if (y.e < kept_n) {
                 y.key = s.pairs[y.e].key;

@@ -364,8 +364,9 @@ class PagedCache8:
     codes, and a scale for each 16 tokens and head: k_scales, v_scales float32 [pages, kv_heads, page_size / 16].
 
     A key is its code times its scale.  ``rotate_append`` keeps the scales at powers of two; ``paged_attention`` and
-    ``read_cache`` take any that are finite and not negative.  Half the memory of a ``PagedCache``, and half the time of
-    what is bound by reading it; values are off by up to 2^-4 of themselves.  The calls read the tensors as they are then.
+    ``read_cache`` take any that are finite and not negative.  Half the memory of a ``PagedCache``; attention over it takes
+    about as long up to 32 rows a cache head (new tokens x query heads that share it), longer above.  Values are off by
+    up to 2^-4 of themselves.  The calls read the tensors as they are then.
     """
 
     def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
