@@ -17,13 +17,13 @@ constexpr double kLog2e = 1.4426950408889634;
 //    20 rows   331 /  186 / 199 / 204       128 rows  1278 / 697 / 224 / 228
 //    32 rows   333 /  190 / 201 / 204       132 rows  1437 / 859 / 398 / 239
 // (Of calls of some 20 us, 36 rows take 14.7 us in tiles of 32 and 18.0 in one of 128.)
+// Over a cache held in 8 bits the borders are the same: 64 sequences x 8 tokens behind 1.5-8k (32 rows)
+// take 231 us in a tile of 32 and 440 in one of 128; 2 x 6 tokens behind 90-131k (48 rows) 133 in two of
+// 32 and 122 in one of 128; two chunks of 2048 (8192 rows) 1774 in tiles of 32 and 464 in tiles of 256.
 int row_tile(int64_t N, int64_t group) {
     const int64_t rows = N * group;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
 }
-
-// The same over a cache held in 8 bits (never larger than row_tile, whose workspace is used).
-int row_tile8(int64_t N, int64_t group) { return row_tile(N, group); }
 
 int check_attention(int64_t B, int64_t N, int64_t q_heads, int64_t kv_heads, int64_t dim) {
     if (B < 0 || N < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads) return SV_EINVAL;
@@ -155,7 +155,7 @@ int attend(const sv_attention_args* args, int64_t sinks, const sv_cache_scales* 
     if (rc == SV_OK && scales) rc = check_scales(*scales, a.cache, a.kv_heads);
     if (rc != SV_OK) return rc;
     const int group = (int)(a.q_heads / a.kv_heads);
-    const int rm = scales ? row_tile8(a.N, group) : row_tile(a.N, group);
+    const int rm = row_tile(a.N, group);
     const Workspace w = workspace(a.dim, rm);
     if (!a.workspace || a.workspace_bytes < (int64_t)w.total) return SV_EWORKSPACE;
     if ((uintptr_t)a.workspace & 255u) return SV_EINVAL;

@@ -22,7 +22,8 @@
 // in shared memory with their elements in that order.  Of values a lane gets two neighbouring
 // codes of two keys: even and odd columns of 16 become a product each.  The keys' scales
 // multiply the scores; the values' scales multiply the weights, relative to the largest met so
-// far (vref), which is raised as the maximum is.
+// far (vref), which is raised as the maximum is.  The call above then takes 226 us, 2.9 TB/s: a
+// block takes a warp some 700 instructions, and both warps of a group convert the same codes.
 //
 // Scores and outputs use the warp-wide 16x8x16 matrix instructions: 16 rows of them are
 // what a decode step fills.

@@ -39,6 +39,16 @@
 // 64 keys (365 us of then 331) and registers moved from the other warps to the softmax (340: the warps
 // that issue products then spill).
 //
+// Over a cache held in 8 bits (E8) warp 9 loads codes, and four more warps turn them into the
+// operand tiles in fp16, a thread a row: keys as they are, values times their scale over the
+// largest that the unit has met (vref); the keys' scales multiply the scores, in sixteens.  Keys
+// and values have a ring of operand tiles each.  Such calls read half the bytes but
+// are slower than 16-bit pages (2 x 6 tokens behind 90-131k: 122 us, 87; the chunks above 464): the
+// conversion takes some 2800 cycles a tile beside the softmax, for each row tile anew, and the
+// kernel's code is larger than the instruction cache.  Tried and slower: a team of four warps each
+// for keys and values (134 us / 490), with two loading warps besides (124 / 472), softmax and
+// conversion as loops (133 / 485), pieces of rows dealt out by lanes (144 / 580).
+//
 // Every wait has a limit.  When one runs out, the CTA writes NaN for what is left of its
 // part, sets SV_ROW_INTERNAL, lets its copies and products finish (with a limit) and ends.
 #pragma once
