@@ -301,8 +301,9 @@ typedef struct {
 int spec_verify_attention_ex(const sv_attention_args* args, const sv_attention_options* options, void* stream);
 
 /*
- * Draws a token of every row of logits [B, N, V] (SV_F32 or SV_BF16), in 32-bit numbers with
- * sums of 48 bits.  With m the row's largest logit, T, k, P, M the sequence's parameters:
+ * Draws a token of every row of logits [B, N, V] (SV_F32 or SV_BF16).  Weights are formed to
+ * 2^-33.6 of themselves, rounded to whole numbers of 2^-44 (to 0.54 of one) and added as such,
+ * without a further rounding.  With m the row's largest logit, T, k, P, M the sequence's parameters:
  *   w(t) = exp((z(t) - m) / T)
  *   kept = the k largest (0, or more than V: all; of equal logits the lower id first),
  *          of these, in that order, the shortest run with a mass >= P of theirs (1: all),

@@ -4,8 +4,9 @@
 // A token is where a sum of weights passes u times their total, so with V tokens there are V
 // borders, some 1e-5 apart or less, and which side of one a draw falls on must not depend on
 // how the sum was formed.  Weights exp((z - m) / T) are therefore formed as pairs of 32-bit
-// numbers (to 2^-34 of themselves; the 64-bit units of this GPU are too few), turned
-// into whole numbers of 2^-44, and added as such: sums are exact and have no order.
+// numbers (to 2^-33.6 of themselves; the 64-bit units of this GPU are too few), turned
+// into whole numbers of 2^-44 (to 0.54 of one), and added as such: sums are exact and have no
+// order.
 //
 // A cluster of CTAs has a row, each a slice of it in shared memory.  What is kept is always a
 // run of the order (logit falling, id rising), so it is given by its last member: a cut
@@ -143,11 +144,13 @@ __device__ __forceinline__ void weigh(const Weight& w, float x, int& hi, int& lo
     const float js = __fadd_rn(p, 12288.0f);  // 1.5 * 2^13: steps of 1/1024
     const int j = __float_as_int(js) - 0x46400000;
     const float f = __fsub_rn(p, __fsub_rn(js, 12288.0f));
-    // 2^(f + q) - 1 by its series to f^3: below 2^-11, so off by 2^-35
+    // 2^(f + q) - 1 by its series to f^3 and f q: |f| <= 2^-11 and |q| < 2^-17, so what is left out is below 2^-40
+    // where a weight is above 2^-16.  (Without f q weights were off by up to 2^-31: q is half a step of p at most.)
+    // Five roundings of 2^-36 remain: f's factor twice, f's product, g and, of a table's entry, k.
     constexpr float kLn2 = 0.69314718f, kLn2Sq = 0.24022651f, kLn2Cb = 0.05550411f;  // ln 2, its square / 2, cube / 6
     float g = __fmaf_rn(f, kLn2Cb, kLn2Sq);
     g = __fmaf_rn(f, g, kLn2);
-    g = __fmaf_rn(q, kLn2, __fmul_rn(f, g));
+    g = __fmaf_rn(q, __fmaf_rn(f, 2.0f * kLn2Sq, kLn2), __fmul_rn(f, g));
     const float2 b = w.tab[j & (kTable - 1)];
     const float k = __fmaf_rn(b.x, g, b.y);
     const float h = __fadd_rn(b.x, k), l = __fsub_rn(k, __fsub_rn(h, b.x));
