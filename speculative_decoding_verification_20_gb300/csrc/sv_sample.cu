@@ -975,12 +975,18 @@ __global__ void __launch_bounds__(kSThreads, 2)
         if (K < V) cut = r.template narrow<false>(cut, K, P, temp);
         float inner = INFINITY;
         if (P < 1.0f) cut = r.nucleus(cut, P, temp, inner);
+        // Of what is kept, what min-p takes is known by weight, unless the cut's own is enough: then it takes nothing.
+        // (Looked at one by one, a token above the cut may be below `least` all the same, since weights of neighbouring
+        // logits may be out of order by their rounding; both passes have to count it then.)
+        const bool known = inner < INFINITY && weight(r.w, cut.v) >= least;
+        const long long bar = known ? 0 : least;
+        if (known) from = -INFINITY;
         auto mass = [&](float x, int id) -> long long {
             if (!(x >= from) || !kept(cut, x, id)) return 0;
             const long long y = weight(r.w, x);
-            return y >= least ? y : 0;
+            return y >= bar ? y : 0;
         };
-        if (inner < INFINITY && weight(r.w, cut.v) >= least)  // min-p takes nothing more: what lies above is known
+        if (known)  // what lies above the interval has been added up
             r.locate([&](float x, int id) -> long long { return x < inner && kept(cut, x, id) ? weight(r.w, x) : 0; }, -1, u,
                      s.keep[warp]);
         else
