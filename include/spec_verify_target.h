@@ -201,7 +201,8 @@ int spec_verify_rotate_append(const sv_rotate_args* args, void* stream);
  * head (the rotated keys or the values of the new tokens; for positions before
  * cache_lens[b], what the cache holds of them):
  *   scale = the least power of two s >= 2^-126 with |x| <= 448 s for all finite x (1: all 0)
- *   code  = x / scale rounded once to SV_E4M3, ties to even; infinities and NaN become NaN
+ *   code  = x / scale rounded once to SV_E4M3, ties to even; infinities and NaN become NaN,
+ *           and so does what the cache holds, if code times scale is beyond 32-bit numbers
  * Rotation is exact up to that rounding (the table's entries taken as they are), so codes
  * do not depend on how the sums are formed.  What a block held past cache_lens[b] (tokens
  * that were rejected) has no part in it: the scale follows the live tokens down as well as

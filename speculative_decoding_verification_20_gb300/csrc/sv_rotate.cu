@@ -86,8 +86,14 @@ __device__ __forceinline__ float dot2_odd(float a, float c, float b, float s) {
     const float hi = two_sum(sum, low, h);
     return to_odd(hi, h != 0.0f ? h : __fadd_rn(g, f));
 }
+// A held code times its scale, rounded to odd: 28 bits where the scale is no power of two.  (The error of a
+// small product is formed 2^64 times as large, so that it does not fall below 32-bit numbers.)
+__device__ __forceinline__ float product_odd(float code, float scale) {
+    const float p = __fmul_rn(code, scale), up = scale < 1.0f ? 0x1p64f : 1.0f;
+    return p == 0.0f ? p : to_odd(p, __fmaf_rn(code, scale * up, -(p * up)));
+}
 
-// The same to 1.5 steps (an exact product's error added behind the other product).
+// dot2_odd's sum to 1.5 steps (an exact product's error added behind the other product).
 __device__ __forceinline__ float dot2(float a, float c, float b, float s) {
     const float w = __fmul_rn(b, s), e = __fmaf_rn(b, s, -w);
     return __fadd_rn(__fmaf_rn(a, c, w), e);
@@ -149,6 +155,13 @@ __device__ __forceinline__ void append8(const sv_rotate_args& a, const sv_cache_
             for (int e = 0; e < 8; ++e) {
                 const float2 f = e4m3_pair(w[e / 2] >> (e % 2 * 16));
                 v[i][2 * e] = f.x * held_scale, v[i][2 * e + 1] = f.y * held_scale;
+            }
+            if (__float_as_int(held_scale) & 0x7FFFFF) {  // a scale that the caller set, no power of two
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = e4m3_pair(w[e / 2] >> (e % 2 * 16));
+                    v[i][2 * e] = product_odd(f.x, held_scale), v[i][2 * e + 1] = product_odd(f.y, held_scale);
+                }
             }
         } else {
             const int64_t n = pos - sl.past;
