@@ -5,6 +5,8 @@
 // ones by the chain lengths -> page id -> codes, which the four go through together.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "sv_internal.cuh"
 #include "sv_paged.cuh"
 
@@ -12,6 +14,20 @@ namespace sv {
 namespace {
 
 constexpr int kReadThreads = 128, kReadRows = 4;
+
+// A code times a scale of 24 bits has 28, and is rounded once: the product is cut to 24 bits, and its last bit set where
+// something may be missing.  That is the exact product's rounding if that is not itself in the middle between two
+// results (9 bits; fp16: 12): a scale of more significant bits than these gives none that is, since a product's odd part
+// is a multiple of the scale's; with one of fewer the product has 16 at most, and nothing is cut off (of a bf16 result
+// below 2^-134 something may be, and does not matter).
+template <typename T>
+__device__ __forceinline__ uint32_t last_bit(float scale) {
+    constexpr uint32_t kBelow = std::is_same<T, __half>::value ? 0xFFFu : 0x7FFFu;
+    return (__float_as_uint(scale < 1.0f ? scale * 0x1p64f : scale) & kBelow) != 0;  // (subnormal ones have fewer)
+}
+__device__ __forceinline__ float product_cut(float code, float scale, uint32_t last) {
+    return __uint_as_float(__float_as_uint(__fmul_rz(code, scale)) | last);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ sv_read_args a) {
@@ -60,11 +76,12 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
             const uint32_t none = nan[i] ? Pair<T>::pack(NAN, NAN) : 0u;
             uint32_t w[8] = {none, none, none, none, none, none, none, none};
             if (page[i] >= 0) {
+                const uint32_t last = last_bit<T>(s[i]);
                 const uint32_t qs[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float2 f = e4m3_pair(qs[e / 2] >> (e % 2 * 16));
-                    w[e] = Pair<T>::pack(f.x * s[i], f.y * s[i]);
+                    w[e] = Pair<T>::pack(product_cut(f.x, s[i], last), product_cut(f.y, s[i], last));
                 }
             }
             T* dst = (T*)(keys ? a.k_out : a.v_out) + (((int64_t)b * a.N + i0 + i) * H + h) * a.dim + c;

@@ -1,8 +1,11 @@
 """The 8-bit cache with scales that the caller set: any finite numbers, not powers of two."""
+import math
+
 import pytest
 import torch
 
 import speculative_decoding_verification_20_gb300 as sv
+from tests import drafter_ref as ref
 from tests.test_cache8_gpu import bits, built, empty_cache, expected_append, i32  # noqa: F401  (built: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -37,3 +40,48 @@ def test_append_rounds_held_codes_once(D, inter):
     for t, w, name in zip((cache.k, cache.v, cache.k_scales, cache.v_scales), want, ("k", "v", "k_scales", "v_scales")):
         assert torch.equal(bits(t), bits(w)), (name, int((bits(t) != bits(w)).sum()))
     assert not torch.equal(bits(cache.v), old)
+
+
+def rounded(x, dtype):
+    """float64 to the nearest bfloat16 or float16 number, ties to even, as float64."""
+    p, least = (8, -133) if dtype == BF else (11, -24)
+    _, e = torch.frexp(x)
+    step = ref.power((e - p).clamp(min=least))
+    y = torch.round(x / step) * step
+    return torch.where(y.abs() > torch.finfo(dtype).max, torch.sign(y) * math.inf, y)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind", ["ties", "any", "small", "large", "powers"])
+def test_reading_back_rounds_once(dtype, kind):
+    """Scales of 24 bits: such that a code times one is within 32 bits' step of the middle between two numbers of the
+    result's type, and any, from products below the type's range to those above."""
+    B, H, D, L = 40, 3, 64, 48
+    g = torch.Generator().manual_seed(len(kind))
+    cache = empty_cache(B * 3, 16, H, D)
+    table = torch.randperm(3 * B, generator=g).to(torch.int32).reshape(B, 3).cuda()
+    for codes, scales in ((cache.k, cache.k_scales), (cache.v, cache.v_scales)):
+        shape = (3 * B, H, 1)
+        if kind == "ties":
+            n = 8 if dtype == BF else 11
+            c = torch.tensor([9.0, 10.0, 11.0, 13.0, 14.0, 15.0])[torch.randint(0, 6, shape, generator=g)]
+            tie = 2.0 * torch.randint(1 << (n - 1), 1 << n, shape, generator=g) + 1
+            s = (tie.double() / c.double()).float() * torch.exp2(torch.randint(-6, 3, shape, generator=g).float())
+        else:
+            lo, hi = dict(any=(-8, 5), small=(-149, -118) if dtype == BF else (-30, -14), powers=(-30, 7),
+                          large=(110, 121) if dtype == BF else (6, 9))[kind]
+            s = torch.exp2(torch.randint(lo, hi, shape, generator=g).float())
+            if kind != "powers":
+                s = s * (1 + torch.rand(shape, generator=g))
+        scales.copy_(s)
+        x = torch.randint(0, 256, codes.shape, generator=g).to(torch.uint8)
+        codes.view(torch.uint8).copy_(torch.where(x & 0x7F == 0x7F, x - 1, x))
+        if kind == "ties":
+            codes[:, :, ::2] = c[..., None].cuda().to(torch.float8_e4m3fn)
+    k, v = sv.read_cache(cache, table, i32([0] * B), L, dtype=dtype)
+    assert k.dtype == v.dtype == dtype
+    at = table.long()
+    for got, codes, scales in ((k, cache.k, cache.k_scales), (v, cache.v, cache.v_scales)):
+        x = codes[at].double() * scales[at][..., None].double()  # [B, 3, H, 16, D]
+        want = rounded(x, dtype).transpose(2, 3).reshape(B, L, H, D)
+        assert torch.equal(got.double(), want), int((got.double() != want).sum())
