@@ -154,7 +154,8 @@ typedef struct {
  * bytes, and every SV_SCALE_BLOCK consecutive slots of a page's head share a scale:
  *   key = code * k[page * k_stride_page + h * k_stride_head + slot / SV_SCALE_BLOCK],
  * and the same for values.  Scales are finite and not negative; those of a block that no
- * token sees may be anything.
+ * token sees may be anything.  Each has a place of its own: strides of pages and heads (where
+ * there is more than one) are at least page_size / SV_SCALE_BLOCK.
  */
 typedef struct {
     float* k;

@@ -95,7 +95,7 @@ inline bool pages(PyObject* ko, PyObject* vo, const at::Device& d, const at::Ten
     return (s == at::kBFloat16 || s == at::kHalf) && on(x, d, s) && on(y, d, s) && x.dim() == 4 && x.sizes() == y.sizes() &&
            x.size(2) >= 16 && x.size(2) % 16 == 0 && rows(x) && rows(y);
 }
-// a PagedCache8's codes and scales
+// a PagedCache8's codes and scales (scales that share memory are copied, or refused, by the Python side)
 inline bool codes(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso, const at::Device& d, const at::Tensor** k,
                   const at::Tensor** v, sv_cache_scales* sc) {
     const at::Tensor *ks, *vs;
@@ -108,7 +108,8 @@ inline bool codes(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso, cons
     if (P < 16 || P % 16) return false;
     for (const at::Tensor* t : {ks, vs})
         if (!on(*t, d, at::kFloat) || t->dim() != 3 || t->size(0) != (*k)->size(0) || t->size(1) != (*k)->size(1) ||
-            t->size(2) != P / SV_SCALE_BLOCK || (t->stride(2) != 1 && t->size(2) > 1))
+            t->size(2) != P / SV_SCALE_BLOCK || (t->stride(2) != 1 && t->size(2) > 1) ||
+            (t->size(0) > 1 && t->stride(0) < t->size(2)) || (t->size(1) > 1 && t->stride(1) < t->size(2)))
             return false;
     sc->k = ks->data_ptr<float>(), sc->v = vs->data_ptr<float>();
     sc->k_stride_page = ks->stride(0), sc->k_stride_head = ks->stride(1);

@@ -374,15 +374,17 @@ class PagedCache8:
         self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in "kv")
         self.k_scales, self.v_scales = (torch.ones((pages, kv_heads, page_size // SCALE_BLOCK), device=device)
                                         for _ in "kv")
-        _pages8(self)
+        _check8(self)
 
     @classmethod
     def from_tensors(cls, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor) -> "PagedCache8":
         """A cache over the caller's memory; any order of page, head and row in memory (views are fine), as long as
-        the head dimension is contiguous, every row starts on a 16-byte boundary and a head's scales are contiguous."""
+        the head dimension is contiguous, every row starts on a 16-byte boundary and a head's scales are contiguous.
+        Scales may share memory (one for each head, or one for all, expanded) in a cache that is only read: each call
+        reads a copy of them, written out; ``rotate_append`` needs a scale for each block."""
         self = cls.__new__(cls)
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        _pages8(self)
+        _check8(self)
         return self
 
     # the tensors may be replaced: nothing else is kept of them
@@ -393,8 +395,7 @@ class PagedCache8:
     device = property(lambda self: self.k.device)
 
 
-def _pages8(cache: PagedCache8) -> Tuple[tuple, tuple]:
-    """The head of the C description of a cache's pages, and that of its scales, of what it holds now."""
+def _check8(cache: PagedCache8) -> None:
     k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
     if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
         raise ValueError("k and v must be [pages, kv_heads, page_size, head_dim] of one shape, type and device")
@@ -408,20 +409,37 @@ def _pages8(cache: PagedCache8) -> Tuple[tuple, tuple]:
     want = (k.shape[0], k.shape[1], k.shape[2] // SCALE_BLOCK)
     for t in (ks, vs):
         if t.dtype != torch.float32 or t.device != k.device or tuple(t.shape) != want or \
-                (t.stride(2) != 1 and want[2] > 1):
+                (t.stride(2) > 1 and want[2] > 1):
             raise ValueError(f"scales must be float32 {list(want)} on the cache's device, a head's contiguous")
+
+
+def _pages8(cache: PagedCache8, written: bool = False) -> Tuple[tuple, tuple, tuple]:
+    """The head of the C description of a cache's pages, and that of its scales, of what it holds now; and the scales'
+    tensors, to be kept until the call is enqueued."""
+    _check8(cache)
+    k, v = cache.k, cache.v
+    scales = []
+    for t in (cache.k_scales, cache.v_scales):
+        n = t.shape[2]
+        if (n > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) < n) or (t.shape[0] > 1 and t.stride(0) < n):
+            if written:
+                raise ValueError("blocks that share a scale cannot be appended to: each needs one of its own")
+            t = t.contiguous()
+        scales.append(t)
+    ks, vs = scales
     return ((k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[2], *k.stride()[:3], *v.stride()[:3]),
-            (ks.data_ptr(), vs.data_ptr(), *ks.stride()[:2], *vs.stride()[:2]))
+            (ks.data_ptr(), vs.data_ptr(), *ks.stride()[:2], *vs.stride()[:2]), (ks, vs))
 
 
-def _of_cache(cache, q: torch.Tensor) -> Tuple[tuple, Optional[tuple], torch.dtype]:
-    """A cache's C description, its scales' (None: 16 bits) and the type of the queries."""
+def _of_cache(cache, q: torch.Tensor, written: bool = False) -> Tuple[tuple, Optional[tuple], torch.dtype, Optional[tuple]]:
+    """A cache's C description, its scales' (None: 16 bits), the type of the queries, and what is to be kept until the
+    call is enqueued."""
     if isinstance(cache, PagedCache8):
-        pages, scales = _pages8(cache)
+        pages, scales, held = _pages8(cache, written)
         if q.dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-        return pages, scales, q.dtype
-    return _pages(cache), None, cache.dtype
+        return pages, scales, q.dtype, held
+    return _pages(cache), None, cache.dtype, None
 
 
 def _pages(cache: PagedCache) -> tuple:
@@ -536,7 +554,7 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
         return _elsewhere(dev, stream, rotate_append, (q, k, v, table, cache, page_table, cache_lens, num_new), dict(
             interleaved=interleaved, out=out, row_status=row_status))
     B, N, Hq, D = shape
-    pages, scales, dtype = _of_cache(cache, q)
+    pages, scales, dtype, _ = _of_cache(cache, q, written=True)
     if D != cache.head_dim or dev != cache.device:
         raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
     if table.dim() != 3 or table.shape[1] != 2 or table.dtype != torch.float32 or table.device != dev or \
@@ -586,7 +604,7 @@ def read_cache(cache: PagedCache8, page_table: torch.Tensor, first, N: int, coun
     if stream is not None or _current_device() != dev.index:
         return _elsewhere(dev, stream, read_cache, (cache, page_table, first, N, count), dict(dtype=dtype,
                                                                                               row_status=row_status))
-    pages, scales = _pages8(cache)
+    pages, scales, held = _pages8(cache)  # (held: until the call is enqueued)
     if dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
@@ -638,7 +656,7 @@ def paged_attention(q: torch.Tensor, cache: Union[PagedCache, PagedCache8], page
             scale=scale, window=window, sinks=sinks, max_context=max_context, out=out, row_status=row_status,
             workspace=workspace, wait_limit_ns=wait_limit_ns))
     B, N, Hq, D = shape
-    (pages, scales, dtype), Hkv = _of_cache(cache, q), cache.kv_heads
+    (pages, scales, dtype, held), Hkv = _of_cache(cache, q), cache.kv_heads  # (held: until the call is enqueued)
     if D != cache.head_dim or dev != cache.device:
         raise ValueError(f"the cache has heads of {cache.head_dim} on {cache.device}")
     if Hq % Hkv:

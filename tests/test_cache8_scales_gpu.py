@@ -85,3 +85,42 @@ def test_reading_back_rounds_once(dtype, kind):
         x = codes[at].double() * scales[at][..., None].double()  # [B, 3, H, 16, D]
         want = rounded(x, dtype).transpose(2, 3).reshape(B, L, H, D)
         assert torch.equal(got.double(), want), int((got.double() != want).sum())
+
+
+@pytest.mark.parametrize("heads,pages", [(False, False), (False, True), (True, False)])
+@pytest.mark.parametrize("blocks", [False, True])
+def test_scales_may_share_memory_where_they_are_read(heads, pages, blocks):
+    """One scale for all, for each page or for each head, expanded: as if it were written out.  blocks: one buffer for the
+    blocks of a page, expanded over the others."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    P, H, S, D, B = 12, 2, 48, 64, 2
+    make = lambda *s: 0.5 + torch.rand(*s, generator=g, device="cuda")
+    shape = (P if pages else 1, H if heads else 1, S // 16 if blocks else 1)
+    ks, vs = make(*shape).expand(P, H, S // 16), make(*shape).expand(P, H, S // 16)
+    k, v = (torch.randn(P, H, S, D, generator=g, device="cuda").to(torch.float8_e4m3fn) for _ in "kv")
+    shared = sv.PagedCache8.from_tensors(k, v, ks, vs)
+    own = sv.PagedCache8.from_tensors(k, v, ks.clone(memory_format=torch.contiguous_format),
+                                      vs.clone(memory_format=torch.contiguous_format))
+    table = torch.randperm(P, generator=g, device="cuda").to(torch.int32).reshape(B, P // B)
+    for N, lens in ((1, [17, 200]), (20, [100, 250]), (150, [0, 100])):
+        q = torch.randn(B, N, 4, D, generator=g, device="cuda").to(BF)
+        for kw in (dict(), dict(window=40, sinks=3)):
+            want = sv.paged_attention(q, own, table, i32(lens), **kw)
+            assert torch.equal(sv.paged_attention(q, shared, table, i32(lens), **kw), want)
+        for x, y in zip(sv.read_cache(shared, table, i32(lens), N), sv.read_cache(own, table, i32(lens), N)):
+            assert torch.equal(x, y)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got = sv.paged_attention(q, shared, table, i32(lens), stream=st, **kw)
+    st.synchronize()
+    assert torch.equal(got, want)
+    lens = i32(lens)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = sv.paged_attention(q, shared, table, lens, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    new = torch.randn(B, 3, H, D, generator=g, device="cuda").to(BF)
+    with pytest.raises(ValueError, match="share a scale"):
+        sv.rotate_append(new, new, new, sv.rotary_table(300, D), shared, table, i32([5, 60]))
