@@ -207,7 +207,9 @@ int spec_verify_rotate_append(const sv_rotate_args* args, void* stream);
  * Rotation is exact up to that rounding (the table's entries taken as they are), so codes
  * do not depend on how the sums are formed.  What a block held past cache_lens[b] (tokens
  * that were rejected) has no part in it: the scale follows the live tokens down as well as
- * up, and rescaling by a power of two loses nothing but what falls below 2^-9 scale.
+ * up, and rescaling by a power of two loses nothing but what falls below 2^-9 scale.  That does
+ * not come back: what shared a block with tokens that were rejected later was rounded under
+ * their scale, and stays off by up to 2^-10 of that scale (or 2^-4 of itself).
  * Codes past the new tokens stay as they are.  The blocks that two sequences of a call
  * write to must be different ones.
  */

@@ -365,8 +365,9 @@ class PagedCache8:
 
     A key is its code times its scale.  ``rotate_append`` keeps the scales at powers of two; ``paged_attention`` and
     ``read_cache`` take any that are finite and not negative.  Half the memory of a ``PagedCache``; attention over it takes
-    about as long up to 32 rows a cache head (new tokens x query heads that share it), longer above.  Values are off by
-    up to 2^-4 of themselves.  The calls read the tensors as they are then.
+    about as long up to 32 rows a cache head (new tokens x query heads that share it), longer above.  A value is off by
+    up to 2^-4 of itself or 2^-10 of its block's scale, whichever is more, for each scale that it was rounded under.  The
+    calls read the tensors as they are then.
     """
 
     def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda"):
@@ -539,7 +540,9 @@ def rotate_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torc
     interleaved.  Returns the rotated q (``out``, which may be q; rows past num_new are zeros).
     Into a ``PagedCache8`` (q, k, v bfloat16 or float16) each block of 16 positions that gets new tokens gets a new
     scale, the least power of two that holds what is live in it after the call, and what it held is rescaled; blocks
-    that two sequences write to must be different ones.
+    that two sequences write to must be different ones.  Tokens that are rejected later are live in their own call: the
+    scale forgets them with the next one, but what was rounded beside them (held tokens, and accepted ones of that call)
+    keeps what it lost under their scale, 2^-10 of it at most.
     """
     if stream is None:
         scales = (cache.k_scales, cache.v_scales) if isinstance(cache, PagedCache8) else (None, None)
