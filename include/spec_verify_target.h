@@ -289,8 +289,8 @@ int spec_verify_attention(const sv_attention_args* args, void* stream);
  *         their entries in the page table may be anything.
  * scales  scales.k != NULL: a cache held in 8 bits; q and out are of args->dtype.  Products
  *         are formed of the codes, in SV_F16 with 32-bit sums: q enters divided by a power
- *         of two of its row's (SV_BF16; elements below 2^-38 of the row's largest lose
- *         bits), scales of keys multiply the scores in 32 bits, and those of values,
+ *         of two of its row's (SV_BF16; elements below 2^-31 of the power of two below the
+ *         row's largest are off by up to 2^-39 of it), scales of keys multiply the scores in 32 bits, and those of values,
  *         relative to the largest met so far, the weights before these are rounded; above 32
  *         rows a cache head (new tokens x query heads that share it) the values, in SV_F16:
  *         what is not a power of two is rounded there, and the product with it.
