@@ -314,8 +314,9 @@ int spec_verify_attention_ex(const sv_attention_args* args, const sv_attention_o
  *          of these those with w >= M
  *   token = the least t with sum of kept w up to t > u * sum of kept w
  *   prob  = w(token) / sum of kept w
- * T = 0 is greedy: the first of the largest, prob 1.  This is the q that spec_verify forms
- * of draft logits with the same temperature, top_k and top_p.
+ * T = 0 is greedy: the first of the largest, prob 1.  With M = 0 this is the q that
+ * spec_verify forms of draft logits with the same temperature, top_k and top_p; drafts drawn
+ * with M > 0 are samples of another q, and not to be verified as if they were of that one.
  * temperature, top_k, top_p, min_p  [B] or NULL (1, 0, 1, 0); uniforms [B, N] (row stride
  * uniform_stride), each in [0, 1).  tokens, probs [B, N] contiguous; probs may be NULL.
  * A sequence with a bad parameter, and a row with a bad random number, a NaN or +inf logit

@@ -704,7 +704,8 @@ def sample(logits: torch.Tensor, uniforms: torch.Tensor, temperature=None, top_k
     tensors, sequences or scalars.  Kept are the top_k largest (of equal logits the lower id first), of these the
     shortest run of the likeliest with a mass of at least top_p of theirs, of these those at least min_p times as likely
     as the likeliest; the token is the first in the order of ids up to which the kept mass exceeds uniform times all of
-    it.  This is the q that spec_verify forms of the logits with the same temperature, top_k and top_p.
+    it.  Without min_p this is the q that spec_verify forms of the logits with the same temperature, top_k and top_p;
+    it has no min_p, so drafts for it are drawn without one (with one the accepted text is not the target's).
     Returns tokens int32 [B, N] and the probability that each had, float32 [B, N].  Rows with a bad parameter or random
     number, a NaN or +inf logit or no finite logit get -1 and NaN (and their bits in row_status).
     """
