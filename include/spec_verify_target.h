@@ -291,9 +291,11 @@ int spec_verify_attention(const sv_attention_args* args, void* stream);
  *         are formed of the codes, in SV_F16 with 32-bit sums: q enters divided by a power
  *         of two of its row's (SV_BF16; elements below 2^-31 of the power of two below the
  *         row's largest are off by up to 2^-39 of it), scales of keys multiply the scores in 32 bits, and those of values,
- *         relative to the largest met so far, the weights before these are rounded; above 32
- *         rows a cache head (new tokens x query heads that share it) the values, in SV_F16:
- *         what is not a power of two is rounded there, and the product with it.
+ *         relative to the largest met so far, the weights before these are rounded (to
+ *         2^-11, or 2^-32 of the row's largest weight at the largest scale); above 32 rows
+ *         a cache head (new tokens x query heads that share it) the values, in SV_F16: what is
+ *         not a power of two is rounded there, and the product with it, in steps of at least
+ *         2^-31 of the largest scale.  A block of zeros counts with its scale, 1.
  * The workspace is that of spec_verify_attention.
  */
 typedef struct {

@@ -41,7 +41,7 @@
 //
 // Over a cache held in 8 bits (E8) warp 9 loads codes, and four more warps turn them into the
 // operand tiles in fp16, a thread a row: keys as they are, values times their scale over the
-// largest that the unit has met (vref); the keys' scales multiply the scores, in sixteens.  Keys
+// largest that the unit has met (vref, less kValueLift); the keys' scales multiply the scores, in sixteens.  Keys
 // and values have a ring of operand tiles each.  Such calls read half the bytes but
 // are slower than 16-bit pages (2 x 6 tokens behind 90-131k: 122 us, 87; the chunks above 464): the
 // conversion takes some 2800 cycles a tile beside the softmax, for each row tile anew, and the
@@ -65,6 +65,10 @@ namespace {
 constexpr int kBadSlots = 16;  // units that the loader can be ahead by, and more
 constexpr int kSlots = 16;     // E8: tiles that it can be ahead of the softmax by, and more (the rings hold 4 to 7)
 constexpr int kSubs = kKeyTile / SV_SCALE_BLOCK;  // E8: scales of a tile's keys, and of its values
+// E8: values are brought to the top of fp16 (448 * 2^7 < 65504), whose steps end at 2^-24: they are off by up to 2^-32 of the
+// largest scale there, and a scale's quotient by it vanishes below 2^-32.  (Up to 448 it was 2^-25: beside a block of zeros,
+// whose scale is 1, values below 2^-16 were lost.)
+constexpr float kValueLift = 128.0f;
 
 template <int D, bool SPLIT, bool E8>
 struct TilesCfg {
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(TilesCfg<D, SPLIT, E8>::kThreads, 1)
     __shared__ int s_bad[kBadSlots];
     // E8: the ring of codes, and what a stage of it holds: values?, the tile's slot, and the rows that nobody sees,
     // [z, w) of it and from w >> 16 on; per slot the scales of keys, those of values over vref, and vref, the largest
-    // scale of values that the unit has met; SPLIT: what a row's scores are multiplied by, of four units
+    // scale of values that the unit has met, over kValueLift; SPLIT: what a row's scores are multiplied by, of four units
     constexpr int kRaw1 = E8 ? C::kRaw : 1, kSlots1 = E8 ? kSlots : 1;
     __shared__ uint64_t s_raw[kRaw1], s_raw_empty[kRaw1];
     __shared__ int4 s_desc[kRaw1];
@@ -1034,8 +1038,8 @@ __global__ void __launch_bounds__(TilesCfg<D, SPLIT, E8>::kThreads, 1)
                         first = false;
                         if (lane < kSubs) {
                             s_ks[slot][lane] = ks;
-                            s_vs[slot][lane] = vs / vref;
-                            if (lane == 0) s_vref[slot] = vref;
+                            s_vs[slot][lane] = vs / vref * kValueLift;
+                            if (lane == 0) s_vref[slot] = vref / kValueLift;
                         }
                         __syncwarp();
                         const int z0 = max(0, min(kKeyTile, lo - k0)), z1 = max(0, min(kKeyTile, hi + 1 - k0));
