@@ -18,8 +18,8 @@ constexpr double kLog2e = 1.4426950408889634;
 //    32 rows   333 /  190 / 201 / 204       132 rows  1437 / 859 / 398 / 239
 // (Of calls of some 20 us, 36 rows take 14.7 us in tiles of 32 and 18.0 in one of 128.)
 // Over a cache held in 8 bits the borders are the same: 64 sequences x 8 tokens behind 1.5-8k (32 rows)
-// take 231 us in a tile of 32 and 440 in one of 128; 2 x 6 tokens behind 90-131k (48 rows) 133 in two of
-// 32 and 122 in one of 128; two chunks of 2048 (8192 rows) 1774 in tiles of 32 and 464 in tiles of 256.
+// take 226 us in a tile of 32 and 436 in one of 128; 2 x 6 tokens behind 90-131k (48 rows) 128 in two of
+// 32 and 121 in one of 128; two chunks of 2048 (8192 rows) 1741 in tiles of 32 and 462 in tiles of 256.
 int row_tile(int64_t N, int64_t group) {
     const int64_t rows = N * group;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;

@@ -43,7 +43,7 @@
 // operand tiles in fp16, a thread a row: keys as they are, values times their scale over the
 // largest that the unit has met (vref, less kValueLift); the keys' scales multiply the scores, in sixteens.  Keys
 // and values have a ring of operand tiles each.  Such calls read half the bytes but
-// are slower than 16-bit pages (2 x 6 tokens behind 90-131k: 122 us, 87; the chunks above 464): the
+// are slower than 16-bit pages (2 x 6 tokens behind 90-131k: 121 us, 87; the chunks above 464, 307): the
 // conversion takes some 2800 cycles a tile beside the softmax, for each row tile anew, and the
 // kernel's code is larger than the instruction cache.  Tried and slower: a team of four warps each
 // for keys and values (134 us / 490), with two loading warps besides (124 / 472), softmax and

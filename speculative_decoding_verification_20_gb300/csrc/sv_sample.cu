@@ -41,7 +41,12 @@ namespace cg = cooperative_groups;
 
 constexpr int kSThreads = 512, kSWarps = kSThreads / 32;
 constexpr int kSCluster = 8;      // CTAs a row at most
-constexpr int kList = 2048;       // tokens that one CTA sorts
+// Tokens of a list: what one CTA sorts, and (kShort) what needs no order.  us for 4 rows of 32000 and a top-k of 50 / 100 /
+// 200 / 400 / 1000 (lists of 1.2 k): 9.8 / 10.5 / 14.1 / 29.7 / 35.7; in an order from 257 tokens on 9.8 / 10.5 / 14.1 / 21.4 /
+// 35.7, from 129 on 17.7 for 200, always 14.0 / 15.5 / 17.8 / 21.5 / 35.7: lists of 257 to 512 would be better off in order.
+// A list of 1024 at most: 52.3 for 1000; rows of up to as many tokens are one list (2000 tokens, top-p: 39.6, where the
+// histograms take 16.4).
+constexpr int kList = 2048;
 constexpr int kPer = kList / kSThreads;
 constexpr int kPivots = 7;
 constexpr int kFix = 44;          // weights are whole numbers of 2^-44: sums of 2^18 of them stay below 2^62
@@ -1040,7 +1045,12 @@ extern "C" int spec_verify_sample(const sv_sample_args* args, void* stream) {
     if (!a.logits || !a.uniforms || !a.tokens || a.stride_b < 0 || a.stride_n < 0 || a.uniform_stride < 0) return SV_EINVAL;
     if ((uintptr_t)a.logits % es || (((uintptr_t)a.uniforms | (uintptr_t)a.tokens | (uintptr_t)a.probs) & 3u)) return SV_EINVAL;
     // CTAs a row: slices of at most 80 KB, so that two CTAs have room on an SM (one's loads run while
-    // the other computes), and more while the rows leave SMs empty and a slice keeps 2048 tokens
+    // the other computes), and more while the rows leave SMs empty and a slice keeps 2048 tokens.
+    // us with 1 / 2 / 4 / 8 (the rule's: *; bf16, top-k 50 or 200 and top-p; nuclei: fp32, top-p alone):
+    //    4 x 8000                  9.1 /  9.8* /  9.6 /      32 x 32000             11.7 / 11.0 / 10.4* / 12.4
+    //    4 x 32000                11.0 / 10.6 /  9.8 / 10.0* 32 x 32000 bf16 nuclei 42.7 / 31.4 / 25.2* / 25.4
+    //  256 x 32000                15.3* / 25.1 / 39.6 /      256 x 128256              - / 74.2 / 67.0* / 103.1
+    //  192 x 151936 nuclei           - /    - / 227.6 / 208.1*
     int C = 1;
     while (C < kSCluster && ((a.V + C - 1) / C * es > 80 * 1024 || (a.B * a.N * C * 2 <= 152 && a.V / (2 * C) >= 2048))) C *= 2;
     const int slice = (int)(((a.V + C - 1) / C + 7) / 8 * 8);
