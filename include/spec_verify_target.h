@@ -316,7 +316,8 @@ int spec_verify_attention_ex(const sv_attention_args* args, const sv_attention_o
  *          of these those with w >= M
  *   token = the least t with sum of kept w up to t > u * sum of kept w
  *   prob  = w(token) / sum of kept w
- * T = 0 is greedy: the first of the largest, prob 1.  With M = 0 this is the q that
+ * T = 0 is greedy: the first of the largest, prob 1; a T below 1e-30 counts as that, and with
+ * one above 2^100 weights lose bits.  With M = 0 this is the q that
  * spec_verify forms of draft logits with the same temperature, top_k and top_p; drafts drawn
  * with M > 0 are samples of another q, and not to be verified as if they were of that one.
  * temperature, top_k, top_p, min_p  [B] or NULL (1, 0, 1, 0); uniforms [B, N] (row stride
